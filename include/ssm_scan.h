@@ -1,6 +1,8 @@
 /*
  * ssm_scan.h -- C ABI of libssmscan.so, the selective state-space scan
- * (Mamba's S6 layer core) for AMD Instinct MI355X (gfx950).
+ * (Mamba's S6 layer core) for AMD Instinct MI355X (gfx950), and beside it the
+ * head-decay mixer: decay attention and the group norm that follows it (their
+ * own conventions stand with them below).
  *
  * What is computed.  For every batch row b, channel d and state n the library
  * runs one diagonal single-input single-output state-space model:
@@ -310,6 +312,200 @@ size_t ssm_scan_bwd_workspace_size(const ssm_scan_bwd_args_t* args);
  * hip_stream; outputs must not overlap each other, the inputs or the
  * workspace.  Errors as for ssm_scan_fwd. */
 ssm_status_t ssm_scan_bwd(const ssm_scan_bwd_args_t* args, void* hip_stream);
+
+/* ---------------------------------------------------------------------------
+ * Decay attention: linear attention with a decay for each head, the state-space
+ * model whose A is one scalar per head.  For every batch row b and head h
+ *
+ *   S_t = exp(log_decay[b,t,h]) S_{t-1} + k_t v_t^T       S (key_dim, value_dim)
+ *   o_t = S_t^T q_t
+ *
+ * with S_{-1} = h0 (zero when NULL), v_t = v[b,t,h,:] and q_t, k_t those of key
+ * head h / (heads / key_heads): heads that share a key head are consecutive.
+ * The recurrence is the one of "连续到离散的转换" (gsyq.cn, "Mamba 状态空间模型
+ * 深度解析") with Abar a scalar of the head, Bbar x = k v^T and C = q.
+ *
+ * Conventions, where they differ from the scan's:
+ *   Layout   q, k (batch, L, key_heads, key_dim); v, o, dout (batch, L, heads,
+ *            value_dim); log_decay (batch, L, heads); states (batch, heads,
+ *            key_dim, value_dim) fp32.  The last dimension of q, k, v, dout is
+ *            contiguous; the others have the strides given (in elements, not
+ *            negative, 0 for a broadcast), so slices of one projection's
+ *            output need no copy.  Outputs and states are dense.
+ *   Lengths  lengths[b] (device, int32, taken as clamped to 0..L; NULL = all L)
+ *            is the number of tokens of row b.  Later tokens are not read (they
+ *            may hold anything, NaN included): o and every gradient are 0
+ *            there, and h_last is the state after the last of the row's tokens
+ *            (h0 for a row without any).
+ *   Decay    any log_decay is taken; -inf, or a value whose exp is 0, resets
+ *            the state.  Values below -128 act as -128 (exp is 0 in fp32).
+ *   Dtypes   q, k, v, o, dout, dq, dk, dv share dtype; log_decay and dlog_decay
+ *            have decay_dtype; states and their gradients are fp32, and so are
+ *            all sums.  With bf16 inputs the products of decayed scores with
+ *            values run on operands rounded once to bf16; updates of the state
+ *            keep 24 bits.
+ *   Non-finite values of a token reach that token and later ones as the
+ *            recurrence says, and may reach earlier tokens of the same block of
+ *            64 (they share its matrix products); rows past a length reach none.
+ *   Sizes    1 <= key_dim, value_dim <= 256; heads a multiple of key_heads.
+ *            Empty problems are valid: with L == 0, h_last = h0, dh0 = dh_last.
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  int64_t batch, seqlen, heads, key_heads, key_dim, value_dim;
+  int32_t dtype;                      /* ssm_dtype_t of q, k, v, o */
+  int32_t decay_dtype;                /* ssm_dtype_t of log_decay */
+  int32_t span;                       /* tokens per span of the time axis, a multiple of 64;
+                                         0 = plan */
+  int32_t reserved;                   /* must be 0 */
+  const void* q;                      /* (batch, L, key_heads, key_dim) */
+  const void* k;                      /* (batch, L, key_heads, key_dim) */
+  const void* v;                      /* (batch, L, heads, value_dim) */
+  const void* log_decay;              /* (batch, L, heads) */
+  int64_t q_stride[3];                /* batch, token, head, in elements */
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t decay_stride[3];
+  const int32_t* lengths;             /* (batch) or NULL */
+  const float* h0;                    /* (batch, heads, key_dim, value_dim) or NULL = 0 */
+  float* h_last;                      /* like h0, or NULL */
+  void* o;                            /* (batch, L, heads, value_dim) */
+  void* workspace;                    /* >= ssm_decay_attn_workspace_size() bytes */
+  size_t workspace_bytes;
+} ssm_decay_attn_args_t;
+
+typedef struct {
+  int64_t batch, heads, key_heads, key_dim, value_dim;
+  int32_t dtype;                      /* ssm_dtype_t of q, k, v, o */
+  int32_t decay_dtype;                /* ssm_dtype_t of log_decay */
+  const void* q;                      /* (batch, key_heads, key_dim) */
+  const void* k;                      /* (batch, key_heads, key_dim) */
+  const void* v;                      /* (batch, heads, value_dim) */
+  const void* log_decay;              /* (batch, heads) */
+  int64_t q_stride[2];                /* batch, head, in elements */
+  int64_t k_stride[2];
+  int64_t v_stride[2];
+  int64_t decay_stride[2];
+  float* h;                           /* (batch, heads, key_dim, value_dim), updated in place */
+  void* o;                            /* (batch, heads, value_dim), read from the updated state */
+} ssm_decay_attn_step_args_t;
+
+/* Gradients of  loss = sum(dout * o) + sum(dh_last * h_last).  With G_t the
+ * gradient of S_t (chain rule of the recurrence; G_{L-1} also gets dh_last):
+ *   G_t = q_t dout_t^T + exp(log_decay_{t+1}) G_{t+1},
+ *   dq_t = S_t dout_t, dk_t = G_t v_t, dv_t = G_t^T k_t,
+ *   dlog_decay_t = exp(log_decay_t) <S_{t-1}, G_t>, dh0 = exp(log_decay_0) G_0;
+ * dq and dk are summed over the heads that share a key head, in a fixed
+ * order.  All gradients are dense and overwritten. */
+typedef struct {
+  int64_t batch, seqlen, heads, key_heads, key_dim, value_dim;
+  int32_t dtype;                      /* ssm_dtype_t of q, k, v, dout, dq, dk, dv */
+  int32_t decay_dtype;                /* ssm_dtype_t of log_decay, dlog_decay */
+  int32_t span;                       /* as in ssm_decay_attn_args_t */
+  int32_t reserved;                   /* must be 0 */
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* log_decay;
+  const void* dout;                   /* (batch, L, heads, value_dim) gradient of o */
+  int64_t q_stride[3];
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t decay_stride[3];
+  int64_t dout_stride[3];
+  const int32_t* lengths;             /* (batch) or NULL */
+  const float* h0;                    /* or NULL = 0 */
+  const float* dh_last;               /* gradient of h_last, or NULL = 0 */
+  void* dq;                           /* (batch, L, key_heads, key_dim) */
+  void* dk;                           /* (batch, L, key_heads, key_dim) */
+  void* dv;                           /* (batch, L, heads, value_dim) */
+  void* dlog_decay;                   /* (batch, L, heads) */
+  float* dh0;                         /* (batch, heads, key_dim, value_dim) or NULL */
+  void* workspace;                    /* >= ssm_decay_attn_bwd_workspace_size() bytes */
+  size_t workspace_bytes;
+} ssm_decay_attn_bwd_args_t;
+
+/* Bytes of device workspace the call needs (0: none).  Pure host functions that
+ * read the sizes, dtypes and span; 0 for invalid sizes. */
+size_t ssm_decay_attn_workspace_size(const ssm_decay_attn_args_t* args);
+size_t ssm_decay_attn_bwd_workspace_size(const ssm_decay_attn_bwd_args_t* args);
+
+/* Decay attention over whole sequences. */
+ssm_status_t ssm_decay_attn_fwd(const ssm_decay_attn_args_t* args, void* hip_stream);
+
+/* One token per sequence, the state updated in place. */
+ssm_status_t ssm_decay_attn_step(const ssm_decay_attn_step_args_t* args, void* hip_stream);
+
+/* Its gradients. */
+ssm_status_t ssm_decay_attn_bwd(const ssm_decay_attn_bwd_args_t* args, void* hip_stream);
+
+/* ---------------------------------------------------------------------------
+ * Group norm with an activation or a gate, channels last.  Every row (token)
+ * of x is normalized on its own, in groups of channels / groups neighbouring
+ * channels (a causal model's statistics cannot span tokens):
+ *
+ *   u = x, or x silu(z) (SSM_NORM_GATE_FIRST)
+ *   n = (u - mean) / sqrt(var + eps), or u / sqrt(mean(u^2) + eps) with rms
+ *   a = n * weight + bias
+ *   y = a (SSM_NORM_PLAIN, SSM_NORM_GATE_FIRST), silu(a) (SSM_NORM_SILU) or
+ *       a silu(z) (SSM_NORM_GATE)
+ *
+ * var is the mean of (u - mean)^2.  x, z, y, dy, dx, dz share dtype; x, z and
+ * dy have contiguous channels and the row strides given; outputs are dense;
+ * weight, bias (NULL = 1, 0) and their gradients are (channels) fp32;
+ * statistics and sums are fp32.  y may not overlap an input.
+ * ------------------------------------------------------------------------- */
+
+typedef enum {
+  SSM_NORM_PLAIN = 0,
+  SSM_NORM_SILU = 1,
+  SSM_NORM_GATE = 2,
+  SSM_NORM_GATE_FIRST = 3
+} ssm_norm_mode_t;
+
+typedef struct {
+  int64_t rows, channels, groups;
+  int64_t x_stride, z_stride;         /* elements from row to row (z_stride ignored without z) */
+  int32_t dtype;                      /* ssm_dtype_t of x, z, y */
+  int32_t mode;                       /* ssm_norm_mode_t */
+  int32_t rms;                        /* 1: no mean is subtracted; 0: group norm */
+  float eps;                          /* >= 0 */
+  const void* x;                      /* (rows, channels) */
+  const void* z;                      /* (rows, channels), with the two gate modes only */
+  const float* weight;                /* (channels) or NULL = 1 */
+  const float* bias;                  /* (channels) or NULL = 0 */
+  void* y;                            /* (rows, channels) */
+} ssm_group_norm_args_t;
+
+typedef struct {
+  int64_t rows, channels, groups;
+  int64_t x_stride, z_stride, dy_stride;
+  int32_t dtype;                      /* ssm_dtype_t of x, z, dy, dx, dz */
+  int32_t mode;
+  int32_t rms;
+  float eps;
+  const void* x;
+  const void* z;
+  const float* weight;
+  const float* bias;
+  const void* dy;                     /* (rows, channels) gradient of y */
+  void* dx;                           /* (rows, channels) */
+  void* dz;                           /* (rows, channels), with the two gate modes only */
+  float* dweight;                     /* (channels) or NULL */
+  float* dbias;                       /* (channels) or NULL */
+  void* workspace;                    /* >= ssm_group_norm_bwd_workspace_size() bytes */
+  size_t workspace_bytes;
+} ssm_group_norm_bwd_args_t;
+
+ssm_status_t ssm_group_norm_fwd(const ssm_group_norm_args_t* args, void* hip_stream);
+
+/* Bytes of device workspace ssm_group_norm_bwd needs (0 without dweight and
+ * dbias, or for invalid sizes).  Pure host function. */
+size_t ssm_group_norm_bwd_workspace_size(const ssm_group_norm_bwd_args_t* args);
+
+/* Gradients of sum(dy * y); the statistics are formed again from x (and z), and
+ * dweight and dbias are summed over the rows in a fixed order. */
+ssm_status_t ssm_group_norm_bwd(const ssm_group_norm_bwd_args_t* args, void* hip_stream);
 
 /* Static description of a status code. */
 const char* ssm_status_string(ssm_status_t status);

@@ -17,6 +17,10 @@ are float32.  Optional fused steps: delta_softplus (Delta = softplus(delta +
 delta_bias)), the gate z (y * silu(z)) and the conv window carried across
 calls (conv_state_in / conv_state_out for the scan, conv_state for step).
 
+Beside the scan, for models with one decay per head, ``mixer`` binds decay
+attention and the group norm that follows it (``decay_attn``,
+``decay_attn_step``, ``decay_attn_bwd``, ``group_norm``, ``group_norm_bwd``).
+
 If the library is not built, importing works but every call raises: there is
 no CPU fallback.
 """
@@ -110,7 +114,10 @@ class BwdArgs(ctypes.Structure):
 EXPORTS = ["ssm_abi_version", "ssm_scan_workspace_size", "ssm_scan_plan_chunk_len",
            "ssm_scan_plan_lane_scan",
            "ssm_scan_fwd", "ssm_scan_fwd_noalloc", "ssm_step", "ssm_scan_bwd_workspace_size",
-           "ssm_scan_bwd", "ssm_status_string", "ssm_last_error_message"]
+           "ssm_scan_bwd", "ssm_status_string", "ssm_last_error_message",
+           "ssm_decay_attn_workspace_size", "ssm_decay_attn_bwd_workspace_size",
+           "ssm_decay_attn_fwd", "ssm_decay_attn_step", "ssm_decay_attn_bwd",
+           "ssm_group_norm_fwd", "ssm_group_norm_bwd_workspace_size", "ssm_group_norm_bwd"]
 
 # bytes of device scratch ssm_scan_fwd_noalloc keeps per GPU (SSM_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -153,6 +160,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ssm_status_string.argtypes = [ctypes.c_int]
     lib.ssm_last_error_message.restype = ctypes.c_char_p
     lib.ssm_last_error_message.argtypes = []
+    mixer.declare(lib)
     got = int(lib.ssm_abi_version())
     if got != ABI_VERSION:
         raise RuntimeError("%s has ABI version %d, this binding mirrors version %d; rebuild it"
@@ -634,3 +642,9 @@ def scan_bwd(x, delta, A, B, C, dy, D=None, h0=None, dh_last=None, zoh=False, wa
         status = lib.ssm_scan_bwd(ctypes.byref(args), _stream_handle(stream))
     _raise_for(lib, status)
     return {k: v for k, v in g.items() if v is not None}
+
+
+# the head-decay mixer's part of the binding (it uses the helpers above)
+from . import mixer  # noqa: E402
+from .mixer import (decay_attn, decay_attn_bwd, decay_attn_step, group_norm,  # noqa: E402,F401
+                    group_norm_bwd)

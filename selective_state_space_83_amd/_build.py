@@ -1,8 +1,10 @@
 """Build libssmscan.so (the HIP library) in-tree with hipcc for gfx950."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -10,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libssmscan.so")
 
-SOURCES = [os.path.join(CSRC, "ssm_scan.hip")]
+SOURCES = [os.path.join(CSRC, n) for n in ("ssm_scan.hip", "decay_attn.hip", "group_norm.hip")]
 
 # Packed-FP32 instructions are switched off for all device code.
 HIPCC_FLAGS = [
@@ -28,12 +30,21 @@ def hipcc() -> str:
 def build(out: str = LIB_PATH, verbose: bool = False) -> str:
     """Compile every HIP source into ``out`` (always recompiles)."""
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + HIPCC_FLAGS + SOURCES + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
+
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(src) + ".o") for src in SOURCES]
+        cmds = [[hipcc()] + flags + ["-c", src, "-o", obj] for src, obj in zip(SOURCES, objs)]
+        with concurrent.futures.ThreadPoolExecutor(max_workers=4) as ex:
+            list(ex.map(run, cmds))
+        run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + ["-o", tmp])
     os.replace(tmp, out)
     return out
 

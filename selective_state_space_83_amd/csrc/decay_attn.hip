@@ -1,0 +1,430 @@
+// decay_attn.hip -- host side of decay attention: argument checks, plans and
+// launches.  The device code is decay_attn.hpp; the contract include/ssm_scan.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "ssm_scan.h"
+#include "ssm_host.hpp"
+#include "decay_attn.hpp"
+
+namespace {
+
+using namespace ssmh;
+using namespace ssma;
+
+constexpr int64_t kMaxDim = 256;
+constexpr int64_t kSpanAlign = 64;
+
+// Sizes common to the three calls; `tokens` is batch * seqlen.
+struct Sizes {
+  int64_t B, L, H, Hk, dk, dv;
+  int64_t tokens, state;   // state: batch * heads * dk * dv
+};
+
+ssm_status_t check_sizes(Sizes* z) {
+  if (z->B < 0 || z->L < 0 || z->H < 0 || z->Hk < 0)
+    return fail(SSM_ERR_SHAPE, "negative size: batch=%lld seqlen=%lld heads=%lld key_heads=%lld",
+                (long long)z->B, (long long)z->L, (long long)z->H, (long long)z->Hk);
+  if (z->dk < 1 || z->dv < 1)
+    return fail(SSM_ERR_SHAPE, "key_dim and value_dim must be >= 1 (got %lld, %lld)",
+                (long long)z->dk, (long long)z->dv);
+  if (z->dk > kMaxDim || z->dv > kMaxDim)
+    return fail(SSM_ERR_UNSUPPORTED, "key_dim %lld and value_dim %lld must be <= %lld",
+                (long long)z->dk, (long long)z->dv, (long long)kMaxDim);
+  if (z->H > 0 && (z->Hk < 1 || z->H % z->Hk != 0))
+    return fail(SSM_ERR_SHAPE, "heads %lld is not a multiple of key_heads %lld", (long long)z->H,
+                (long long)z->Hk);
+  // the largest arrays: per token and value head up to kMaxDim fp32 values
+  int64_t bh, n;
+  if (!mul_ok(z->B, z->L, &z->tokens) || !mul_ok(z->B, z->H, &bh) ||
+      !mul_ok(bh, z->dk * z->dv, &z->state) || !mul_ok(z->tokens, z->H, &n) ||
+      !mul_ok(n, kMaxDim, &n) || n > INT64_MAX / 64 || z->state > INT64_MAX / 64)
+    return fail(SSM_ERR_SHAPE, "sizes overflow");
+  if (bh > kMaxGrid) return fail(SSM_ERR_SHAPE, "problem too large for one launch");
+  return SSM_OK;
+}
+
+ssm_status_t check_dtypes(int32_t dtype, int32_t decay_dtype) {
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_DTYPE, "unknown dtype %d", dtype);
+  if (decay_dtype != SSM_F32 && decay_dtype != SSM_BF16)
+    return fail(SSM_ERR_DTYPE, "unknown decay_dtype %d", decay_dtype);
+  return SSM_OK;
+}
+
+// The bytes from p on that a strided array of `rank` outer dimensions spans.
+bool extent(const void* p, const int64_t* size, const int64_t* stride, int rank, int64_t inner,
+            size_t elem, Range* r) {
+  int64_t last = inner - 1;
+  bool empty = false;
+  for (int i = 0; i < rank; ++i) {
+    int64_t n;
+    if (stride[i] < 0) return false;
+    if (size[i] == 0) empty = true;
+    if (size[i] > 0 && (!mul_ok(size[i] - 1, stride[i], &n) || last > INT64_MAX / 16 - n)) return false;
+    if (size[i] > 0) last += n;
+  }
+  if (last > INT64_MAX / 16) return false;
+  *r = Range{p, empty ? 0 : size_t(last + 1) * elem};
+  return true;
+}
+
+ssm_status_t check_rows(const char* name, const void* p, const int64_t* size, const int64_t* stride,
+                        int rank, int64_t inner, int32_t dtype, Range* r) {
+  if (!extent(p, size, stride, rank, inner, dtype_size(dtype), r))
+    return fail(SSM_ERR_SHAPE, "%s has a negative or overflowing stride", name);
+  if (misaligned(p, dtype_size(dtype))) return fail(SSM_ERR_UNSUPPORTED, "misaligned %s", name);
+  return SSM_OK;
+}
+
+struct Named {
+  const char* name;
+  Range r;
+};
+
+ssm_status_t check_alias(const Named* outs, int nout, const Named* ins, int nin) {
+  for (int i = 0; i < nout; ++i) {
+    for (int k = 0; k < nin; ++k)
+      if (overlap(outs[i].r, ins[k].r))
+        return fail(SSM_ERR_ALIAS, "%s overlaps %s", outs[i].name, ins[k].name);
+    for (int k = i + 1; k < nout; ++k)
+      if (overlap(outs[i].r, outs[k].r))
+        return fail(SSM_ERR_ALIAS, "%s overlaps %s", outs[i].name, outs[k].name);
+  }
+  return SSM_OK;
+}
+
+ssm_status_t check_fwd(const ssm_decay_attn_args_t* a, Sizes* z) {
+  if (!a) return fail(SSM_ERR_NULL, "args is NULL");
+  *z = Sizes{a->batch, a->seqlen, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
+  if (ssm_status_t st = check_sizes(z)) return st;
+  if (ssm_status_t st = check_dtypes(a->dtype, a->decay_dtype)) return st;
+  if (a->span < 0 || a->span % kSpanAlign != 0)
+    return fail(SSM_ERR_UNSUPPORTED, "span must be a non-negative multiple of %lld", (long long)kSpanAlign);
+  if (a->reserved != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved field must be 0");
+  if (z->B * z->H == 0) return SSM_OK;
+  if (z->L > 0 && (!a->q || !a->k || !a->v || !a->log_decay || !a->o))
+    return fail(SSM_ERR_NULL, "q, k, v, log_decay and o are required");
+  if (misaligned(a->lengths, 4) || misaligned(a->h0, 4) || misaligned(a->h_last, 4) ||
+      misaligned(a->o, dtype_size(a->dtype)))
+    return fail(SSM_ERR_UNSUPPORTED, "misaligned pointer (element alignment)");
+  const int64_t kn[] = {z->B, z->L, z->Hk}, vn[] = {z->B, z->L, z->H};
+  Range q, k, v, g;
+  if (ssm_status_t st = check_rows("q", a->q, kn, a->q_stride, 3, z->dk, a->dtype, &q)) return st;
+  if (ssm_status_t st = check_rows("k", a->k, kn, a->k_stride, 3, z->dk, a->dtype, &k)) return st;
+  if (ssm_status_t st = check_rows("v", a->v, vn, a->v_stride, 3, z->dv, a->dtype, &v)) return st;
+  if (ssm_status_t st = check_rows("log_decay", a->log_decay, vn, a->decay_stride, 3, 1, a->decay_dtype, &g))
+    return st;
+  const size_t state = size_t(z->state) * 4;
+  const Named outs[] = {
+      {"o", {a->o, size_t(z->tokens) * size_t(z->H * z->dv) * dtype_size(a->dtype)}},
+      {"h_last", {a->h_last, state}}};
+  const Named ins[] = {{"q", q}, {"k", k}, {"v", v}, {"log_decay", g}, {"h0", {a->h0, state}},
+                       {"lengths", {a->lengths, size_t(z->B) * 4}}};
+  return check_alias(outs, 2, ins, 6);
+}
+
+ssm_status_t check_step(const ssm_decay_attn_step_args_t* a, Sizes* z) {
+  if (!a) return fail(SSM_ERR_NULL, "args is NULL");
+  *z = Sizes{a->batch, 1, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
+  if (ssm_status_t st = check_sizes(z)) return st;
+  if (ssm_status_t st = check_dtypes(a->dtype, a->decay_dtype)) return st;
+  if (z->B * z->H == 0) return SSM_OK;
+  if (!a->q || !a->k || !a->v || !a->log_decay || !a->h || !a->o)
+    return fail(SSM_ERR_NULL, "q, k, v, log_decay, h and o are required");
+  if (misaligned(a->h, 4) || misaligned(a->o, dtype_size(a->dtype)))
+    return fail(SSM_ERR_UNSUPPORTED, "misaligned pointer (element alignment)");
+  const int64_t kn[] = {z->B, z->Hk}, vn[] = {z->B, z->H};
+  Range q, k, v, g;
+  if (ssm_status_t st = check_rows("q", a->q, kn, a->q_stride, 2, z->dk, a->dtype, &q)) return st;
+  if (ssm_status_t st = check_rows("k", a->k, kn, a->k_stride, 2, z->dk, a->dtype, &k)) return st;
+  if (ssm_status_t st = check_rows("v", a->v, vn, a->v_stride, 2, z->dv, a->dtype, &v)) return st;
+  if (ssm_status_t st = check_rows("log_decay", a->log_decay, vn, a->decay_stride, 2, 1, a->decay_dtype, &g))
+    return st;
+  const Named outs[] = {{"o", {a->o, size_t(z->B * z->H * z->dv) * dtype_size(a->dtype)}},
+                        {"h", {a->h, size_t(z->state) * 4}}};
+  const Named ins[] = {{"q", q}, {"k", k}, {"v", v}, {"log_decay", g}};
+  return check_alias(outs, 2, ins, 4);
+}
+
+// Workspace of the backward pass.
+struct BwdPlan {
+  int64_t dq_tiles = 0, dk_tiles = 0;   // tiles of key_dim in the dq and dk passes
+  size_t off_s = 0, off_u = 0, off_w = 0, off_dq = 0, off_dk = 0, total = 0;
+};
+
+BwdPlan make_bwd_plan(const Sizes& z) {
+  BwdPlan pl;
+  if (z.tokens == 0 || z.H == 0) return pl;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += align256(bytes);
+    return o;
+  };
+  pl.dq_tiles = pl.dk_tiles = (z.dk + kWave - 1) / kWave;
+  const size_t th = size_t(z.tokens) * size_t(z.H);
+  pl.off_s = take(size_t(z.state) * 4);
+  pl.off_u = take(th * size_t(pl.dq_tiles) * 4);
+  pl.off_w = take(th * size_t(pl.dk_tiles) * 4);
+  const bool shared = z.H != z.Hk;
+  pl.off_dq = take(shared ? th * size_t(z.dk) * 4 : 0);
+  pl.off_dk = take(shared ? th * size_t(z.dk) * 4 : 0);
+  pl.total = off;
+  return pl;
+}
+
+ssm_status_t check_bwd(const ssm_decay_attn_bwd_args_t* a, Sizes* z, BwdPlan* pl) {
+  if (!a) return fail(SSM_ERR_NULL, "args is NULL");
+  *z = Sizes{a->batch, a->seqlen, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
+  if (ssm_status_t st = check_sizes(z)) return st;
+  if (ssm_status_t st = check_dtypes(a->dtype, a->decay_dtype)) return st;
+  if (a->span < 0 || a->span % kSpanAlign != 0)
+    return fail(SSM_ERR_UNSUPPORTED, "span must be a non-negative multiple of %lld", (long long)kSpanAlign);
+  if (a->reserved != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved field must be 0");
+  *pl = make_bwd_plan(*z);
+  if (z->B * z->H == 0) return SSM_OK;
+  if (z->L > 0 && (!a->q || !a->k || !a->v || !a->log_decay || !a->dout || !a->dq || !a->dk ||
+                   !a->dv || !a->dlog_decay))
+    return fail(SSM_ERR_NULL, "q, k, v, log_decay, dout, dq, dk, dv and dlog_decay are required");
+  const size_t es = dtype_size(a->dtype), gs = dtype_size(a->decay_dtype);
+  if (misaligned(a->lengths, 4) || misaligned(a->h0, 4) || misaligned(a->dh_last, 4) ||
+      misaligned(a->dh0, 4) || misaligned(a->dq, es) || misaligned(a->dk, es) ||
+      misaligned(a->dv, es) || misaligned(a->dlog_decay, gs) || misaligned(a->workspace, 256))
+    return fail(SSM_ERR_UNSUPPORTED, "misaligned pointer (element alignment; workspace 256 bytes)");
+  const int64_t kn[] = {z->B, z->L, z->Hk}, vn[] = {z->B, z->L, z->H};
+  Range q, k, v, g, d;
+  if (ssm_status_t st = check_rows("q", a->q, kn, a->q_stride, 3, z->dk, a->dtype, &q)) return st;
+  if (ssm_status_t st = check_rows("k", a->k, kn, a->k_stride, 3, z->dk, a->dtype, &k)) return st;
+  if (ssm_status_t st = check_rows("v", a->v, vn, a->v_stride, 3, z->dv, a->dtype, &v)) return st;
+  if (ssm_status_t st = check_rows("log_decay", a->log_decay, vn, a->decay_stride, 3, 1, a->decay_dtype, &g))
+    return st;
+  if (ssm_status_t st = check_rows("dout", a->dout, vn, a->dout_stride, 3, z->dv, a->dtype, &d)) return st;
+  const size_t state = size_t(z->state) * 4, tok = size_t(z->tokens);
+  const Named ins[] = {{"q", q}, {"k", k}, {"v", v}, {"log_decay", g}, {"dout", d},
+                       {"h0", {a->h0, state}}, {"dh_last", {a->dh_last, state}},
+                       {"lengths", {a->lengths, size_t(z->B) * 4}}};
+  const Named outs[] = {{"dq", {a->dq, tok * size_t(z->Hk * z->dk) * es}},
+                        {"dk", {a->dk, tok * size_t(z->Hk * z->dk) * es}},
+                        {"dv", {a->dv, tok * size_t(z->H * z->dv) * es}},
+                        {"dlog_decay", {a->dlog_decay, tok * size_t(z->H) * gs}},
+                        {"dh0", {a->dh0, state}},
+                        {"workspace", {a->workspace, pl->total}}};
+  if (pl->total > 0) {
+    if (!a->workspace) return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes required", pl->total);
+    if (a->workspace_bytes < pl->total)
+      return fail(SSM_ERR_WORKSPACE, "workspace has %zu bytes, %zu required", a->workspace_bytes,
+                  pl->total);
+  }
+  return check_alias(outs, 6, ins, 8);
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+template <typename T, typename OutT>
+ssm_status_t run_mix(const MixParams& p, hipStream_t s) {
+  const dim3 grid(uint32_t(p.B * p.H), uint32_t((p.N + kWave - 1) / kWave));
+  if (p.M <= 64)
+    hipLaunchKernelGGL((k_mix_simple<T, OutT, 64>), grid, dim3(kWave), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_mix_simple<T, OutT, 256>), grid, dim3(kWave), 0, s, p);
+  return launch_status("k_mix_simple");
+}
+
+ssm_status_t copy_state(float* dst, const float* src, int64_t n, hipStream_t s) {
+  if (!dst || n == 0) return SSM_OK;
+  hipLaunchKernelGGL(k_attn_state_copy, dim3(uint32_t((n + 255) / 256)), dim3(256), 0, s, dst, src, n);
+  return launch_status("k_attn_state_copy");
+}
+
+Rows rows(const void* p, const int64_t* st, int64_t per) {
+  return Rows{p, st[0], st[1], st[2], int32_t(per)};
+}
+
+Decay decay(const void* p, const int64_t* st, int32_t dtype) {
+  return Decay{p, st[0], st[1], st[2], dtype == SSM_BF16};
+}
+
+template <typename T>
+ssm_status_t run_fwd(const ssm_decay_attn_args_t* a, const Sizes& z, hipStream_t s) {
+  MixParams p{};
+  const int64_t per = z.H / z.Hk;
+  p.a = rows(a->q, a->q_stride, per);
+  p.b = rows(a->k, a->k_stride, per);
+  p.c = rows(a->v, a->v_stride, 1);
+  p.g = decay(a->log_decay, a->decay_stride, a->decay_dtype);
+  p.lengths = a->lengths;
+  p.s0 = a->h0;
+  p.s_last = a->h_last;
+  p.sm = z.dv;
+  p.sn = 1;
+  p.out = a->o;
+  p.B = z.B;
+  p.L = z.L;
+  p.H = z.H;
+  p.M = int32_t(z.dk);
+  p.N = int32_t(z.dv);
+  return run_mix<T, T>(p, s);
+}
+
+template <typename T>
+ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const BwdPlan& pl,
+                     hipStream_t s) {
+  char* ws = static_cast<char*>(a->workspace);
+  const int64_t per = z.H / z.Hk;
+  const bool shared = per > 1;
+  const Rows q = rows(a->q, a->q_stride, per), k = rows(a->k, a->k_stride, per);
+  const Rows v = rows(a->v, a->v_stride, 1), d = rows(a->dout, a->dout_stride, 1);
+  MixParams p{};
+  p.g = decay(a->log_decay, a->decay_stride, a->decay_dtype);
+  p.lengths = a->lengths;
+  p.B = z.B;
+  p.L = z.L;
+  p.H = z.H;
+  // dq, with the state transposed: S(m, n) at row n of the stored state
+  MixParams dq = p;
+  dq.a = d;
+  dq.b = v;
+  dq.c = k;
+  dq.x = q;
+  dq.s0 = a->h0;
+  dq.s_last = a->dh_last ? reinterpret_cast<float*>(ws + pl.off_s) : nullptr;
+  dq.sm = 1;
+  dq.sn = z.dv;
+  dq.M = int32_t(z.dv);
+  dq.N = int32_t(z.dk);
+  dq.dots = reinterpret_cast<float*>(ws + pl.off_u);
+  dq.out = shared ? ws + pl.off_dq : a->dq;
+  // dk, backward in time, G transposed
+  MixParams dk = p;
+  dk.reverse = 1;
+  dk.a = v;
+  dk.b = d;
+  dk.c = q;
+  dk.x = k;
+  dk.s0 = a->dh_last;
+  dk.sm = 1;
+  dk.sn = z.dv;
+  dk.M = int32_t(z.dv);
+  dk.N = int32_t(z.dk);
+  dk.dots = reinterpret_cast<float*>(ws + pl.off_w);
+  dk.out = shared ? ws + pl.off_dk : a->dk;
+  // dv, backward in time
+  MixParams dv = p;
+  dv.reverse = 1;
+  dv.a = k;
+  dv.b = q;
+  dv.c = d;
+  dv.s0 = a->dh_last;
+  dv.s_last = a->dh0;
+  dv.sm = z.dv;
+  dv.sn = 1;
+  dv.M = int32_t(z.dk);
+  dv.N = int32_t(z.dv);
+  dv.out = a->dv;
+  if (ssm_status_t st = run_mix<T, T>(dv, s)) return st;
+  if (shared) {
+    if (ssm_status_t st = run_mix<T, float>(dq, s)) return st;
+    if (ssm_status_t st = run_mix<T, float>(dk, s)) return st;
+    const int64_t n = z.tokens * z.Hk * z.dk;
+    const dim3 grid(uint32_t((n + 255) / 256));
+    for (int i = 0; i < 2; ++i) {
+      hipLaunchKernelGGL((k_sum_heads<T>), grid, dim3(256), 0, s, static_cast<T*>(i ? a->dk : a->dq),
+                         static_cast<const float*>(i ? dk.out : dq.out), n, int32_t(z.dk), int32_t(per));
+      if (ssm_status_t st = launch_status("k_sum_heads")) return st;
+    }
+  } else {
+    if (ssm_status_t st = run_mix<T, T>(dq, s)) return st;
+    if (ssm_status_t st = run_mix<T, T>(dk, s)) return st;
+  }
+  DecayGradParams gp{};
+  gp.u = dq.dots;
+  gp.w = dk.dots;
+  gp.s_last = dq.s_last;
+  gp.dh_last = a->dh_last;
+  gp.lengths = a->lengths;
+  gp.dg = a->dlog_decay;
+  gp.B = z.B;
+  gp.L = z.L;
+  gp.H = z.H;
+  gp.inner = z.dk * z.dv;
+  gp.utiles = int32_t(pl.dq_tiles);
+  gp.wtiles = int32_t(pl.dk_tiles);
+  gp.bf16 = a->decay_dtype == SSM_BF16;
+  hipLaunchKernelGGL(k_decay_grad_simple, dim3(uint32_t(z.B * z.H)), dim3(kWave), 0, s, gp);
+  return launch_status("k_decay_grad_simple");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_decay_attn_workspace_size(const ssm_decay_attn_args_t* a) {
+  (void)a;
+  return 0;
+}
+
+size_t ssm_decay_attn_bwd_workspace_size(const ssm_decay_attn_bwd_args_t* a) {
+  if (!a) return 0;
+  Sizes z{a->batch, a->seqlen, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
+  if (check_sizes(&z)) return 0;
+  return make_bwd_plan(z).total;
+}
+
+ssm_status_t ssm_decay_attn_fwd(const ssm_decay_attn_args_t* a, void* hip_stream) {
+  clear_message();
+  Sizes z;
+  if (ssm_status_t st = check_fwd(a, &z)) return st;
+  hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  if (z.B * z.H == 0) return SSM_OK;
+  if (z.L == 0) return copy_state(a->h_last, a->h0, z.state, s);
+  return a->dtype == SSM_F32 ? run_fwd<float>(a, z, s) : run_fwd<bf16_t>(a, z, s);
+}
+
+ssm_status_t ssm_decay_attn_step(const ssm_decay_attn_step_args_t* a, void* hip_stream) {
+  clear_message();
+  Sizes z;
+  if (ssm_status_t st = check_step(a, &z)) return st;
+  hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  if (z.B * z.H == 0) return SSM_OK;
+  AttnStepParams p{};
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.g = a->log_decay;
+  for (int i = 0; i < 2; ++i) {
+    p.qs[i] = a->q_stride[i];
+    p.ks[i] = a->k_stride[i];
+    p.vs[i] = a->v_stride[i];
+    p.gs[i] = a->decay_stride[i];
+  }
+  p.h = a->h;
+  p.o = a->o;
+  p.B = z.B;
+  p.H = z.H;
+  p.per = int32_t(z.H / z.Hk);
+  p.dk = int32_t(z.dk);
+  p.dv = int32_t(z.dv);
+  p.g_bf16 = a->decay_dtype == SSM_BF16;
+  const dim3 grid(uint32_t(z.B * z.H), uint32_t((z.dv + kWave - 1) / kWave));
+  if (a->dtype == SSM_F32)
+    hipLaunchKernelGGL((k_attn_step_simple<float>), grid, dim3(kWave), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_attn_step_simple<bf16_t>), grid, dim3(kWave), 0, s, p);
+  return launch_status("k_attn_step_simple");
+}
+
+ssm_status_t ssm_decay_attn_bwd(const ssm_decay_attn_bwd_args_t* a, void* hip_stream) {
+  clear_message();
+  Sizes z;
+  BwdPlan pl;
+  if (ssm_status_t st = check_bwd(a, &z, &pl)) return st;
+  hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  if (z.B * z.H == 0) return SSM_OK;
+  if (z.L == 0) return copy_state(a->dh0, a->dh_last, z.state, s);
+  return a->dtype == SSM_F32 ? run_bwd<float>(a, z, pl, s) : run_bwd<bf16_t>(a, z, pl, s);
+}
+
+}  // extern "C"

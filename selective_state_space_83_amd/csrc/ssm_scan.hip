@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "ssm_scan.h"
+#include "ssm_host.hpp"
 #include "ssm_kernels.hpp"
 #include "ssm_bwd.hpp"
 
@@ -22,8 +23,12 @@ constexpr size_t kNoallocScratchBytes = size_t(SSM_NOALLOC_SCRATCH_BYTES);
 static __device__ __align__(256) unsigned char scratch[kNoallocScratchBytes];
 
 namespace {
-
 thread_local char g_msg[512] = "";
+}
+
+namespace ssmh {
+
+void clear_message() { g_msg[0] = '\0'; }
 
 ssm_status_t fail(ssm_status_t s, const char* fmt, ...) {
   va_list ap;
@@ -32,6 +37,12 @@ ssm_status_t fail(ssm_status_t s, const char* fmt, ...) {
   va_end(ap);
   return s;
 }
+
+}  // namespace ssmh
+
+namespace {
+
+using namespace ssmh;
 
 // The plan targets MI355X: 256 CUs x 4 SIMDs, and scan kernels small enough
 // for four waves per SIMD.  A chunked plan uses at most kTargetWaves waves in
@@ -74,17 +85,6 @@ constexpr int64_t kMaxChunk = int64_t(1) << 30;   // kernels count steps in 32 b
 // A chunk's rows of x / Delta / y are addressed through one buffer resource
 // with 32-bit offsets: keep steps * D * 4 bytes below 2^31.
 constexpr int64_t kMaxChunkBytes = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
-
-size_t dtype_size(int32_t dt) { return dt == SSM_BF16 ? 2 : 4; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  if (a < 0 || b < 0) return false;
-  if (a != 0 && b > INT64_MAX / a) return false;
-  *out = a * b;
-  return true;
-}
-
 bool supported_n(int64_t n) { return n == 1 || n == 2 || n == 4 || n == 8 || n == 16; }
 
 // States kept for the backward pass: those entering steps 16, 32, ... < L.
@@ -129,8 +129,6 @@ struct Plan {
   size_t ws_gS = 0, ws_gB = 0;
   size_t ws_total = 0;
 };
-
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Sizes are assumed validated (non-negative, no overflow).
 Plan make_plan(int64_t Bt, int64_t L, int64_t D, int64_t N, int32_t chunk_len) {
@@ -203,21 +201,6 @@ Plan one_pass_plan(const ssm_scan_args_t* a, const Plan& chunked) {
   pl.C = 1;
   pl.dtiles = chunked.dtiles;
   return pl;
-}
-
-struct Range {
-  const void* p;
-  size_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-  if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-bool misaligned(const void* p, size_t align) {
-  return p && (reinterpret_cast<uintptr_t>(p) % align) != 0;
 }
 
 // The plan of the allocation-free entry point: the library's plan when its
@@ -449,12 +432,6 @@ ssm_status_t scratch_address(hipStream_t s, void** out) {
     g_scratch_ptr[dev] = p;
   }
   *out = g_scratch_ptr[dev];
-  return SSM_OK;
-}
-
-ssm_status_t launch_status(const char* what) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(SSM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
   return SSM_OK;
 }
 
@@ -963,14 +940,14 @@ ssm_status_t scan_fwd_run(const ssm_scan_args_t* a, const Plan& pl, void* ws, hi
 extern "C" {
 
 ssm_status_t ssm_scan_fwd(const ssm_scan_args_t* a, void* hip_stream) {
-  g_msg[0] = '\0';
+  clear_message();
   Plan pl;
   if (ssm_status_t st = check_scan(a, &pl)) return st;
   return scan_fwd_run(a, pl, a->workspace, static_cast<hipStream_t>(hip_stream));
 }
 
 ssm_status_t ssm_scan_fwd_noalloc(const ssm_scan_args_t* a, void* hip_stream) {
-  g_msg[0] = '\0';
+  clear_message();
   Plan pl;
   if (ssm_status_t st = check_scan(a, &pl, true)) return st;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
@@ -982,7 +959,7 @@ ssm_status_t ssm_scan_fwd_noalloc(const ssm_scan_args_t* a, void* hip_stream) {
 }
 
 ssm_status_t ssm_step(const ssm_step_args_t* a, void* hip_stream) {
-  g_msg[0] = '\0';
+  clear_message();
   if (ssm_status_t st = check_step(a)) return st;
   if (a->batch * a->dim == 0) return SSM_OK;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
@@ -1028,7 +1005,7 @@ size_t ssm_scan_bwd_workspace_size(const ssm_scan_bwd_args_t* a) {
 }
 
 ssm_status_t ssm_scan_bwd(const ssm_scan_bwd_args_t* a, void* hip_stream) {
-  g_msg[0] = '\0';
+  clear_message();
   BwdPlan pl;
   if (ssm_status_t st = check_bwd(a, &pl)) return st;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);

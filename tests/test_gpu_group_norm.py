@@ -1,0 +1,236 @@
+"""The group norm on the GPU against its 64-bit definition: modes, types, group
+sizes, layouts and gradients."""
+import pytest
+import torch
+
+import mixer_ref as R
+import selective_state_space_83_amd as ssm
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+MODES = ["none", "silu", "gate", "gate_first"]
+
+
+def make(rows, C, dtype, seed=0, offset=0.3, scale=1.0):
+    gen = torch.Generator().manual_seed(2000 + seed)
+    n = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    return {"x": (scale * n(rows, C) + offset * n(rows, 1)).to(dtype).cuda(), "z": n(rows, C).to(dtype).cuda(),
+            "dy": n(rows, C).to(dtype).cuda(), "weight": (1 + 0.2 * n(C)).cuda(), "bias": (0.2 * n(C)).cuda()}
+
+
+def how(t, mode):
+    return dict(z=t["z"] if mode in ("gate", "gate_first") else None, act="silu" if mode == "silu" else None,
+                gate_first=mode == "gate_first")
+
+
+def run(t, groups, mode, rms=False, affine=True, eps=1e-5, back=True):
+    kw = dict(how(t, mode), rms=rms, eps=eps)
+    if affine:
+        kw.update(weight=t["weight"], bias=t["bias"])
+    y = ssm.group_norm(t["x"], groups, **kw)
+    g = ssm.group_norm_bwd(t["x"], t["dy"], groups, **kw) if back else {}
+    torch.cuda.synchronize()
+    return y, g, kw
+
+
+def check(t, groups, mode, rms=False, affine=True, eps=1e-5):
+    y, g, kw = run(t, groups, mode, rms, affine, eps)
+    ref = R.norm(t["x"], groups, dy=t["dy"], **kw)
+    low = t["x"].dtype == BF16
+    R.check("y", y, ref["y"], low)
+    R.check("dx", g["dx"], ref["dx"], low)
+    assert ("dz" in g) == (mode in ("gate", "gate_first"))
+    if "dz" in g:
+        R.check("dz", g["dz"], ref["dz"], low)
+    for n in ("dweight", "dbias"):
+        assert g[n].dtype == F32
+        R.check(n, g[n], ref[n], False)
+    return y, g
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_modes(dtype, mode, rms):
+    check(make(37, 320, dtype, seed=1), 5, mode, rms)
+    check(make(37, 320, dtype, seed=2), 5, mode, rms, affine=False)
+
+
+SIZES = [(1, 1), (1, 2), (3, 5), (7, 8), (5, 16), (3, 33), (2, 63), (4, 64), (2, 100), (3, 128), (1, 255),
+         (2, 256), (2, 500), (1, 512), (1, 1000), (1, 1024), (2, 2048), (1, 2560), (1, 4097), (1, 5120), (1, 12000),
+         (1, 20001), (80, 64), (41, 24)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("groups,size", SIZES)
+def test_group_sizes(groups, size, dtype):
+    # one value in a group: centred it is 0 whatever x, so its rms form is tested
+    check(make(9, groups * size, dtype, seed=size), groups, "gate", rms=size == 1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [1, 2, 63, 64, 65, 300, 1031])
+def test_rows(rows, dtype):
+    check(make(rows, 192, dtype, seed=rows), 3, "silu")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_strided_rows(dtype):
+    """Slices of wider rows, at offsets that leave 16-byte alignment or keep it,
+    and a (batch, L, channels) view."""
+    for off in (0, 1, 8):
+        t = make(24, 3 * 64 + 16, dtype, seed=off)
+        for n in ("x", "z", "dy"):
+            t[n] = t[n][:, off:off + 128]
+        t["weight"], t["bias"] = t["weight"][:128].contiguous(), t["bias"][:128].contiguous()
+        y, g = check(t, 2, "gate")
+        u = dict(t)
+        for n in ("x", "z", "dy"):
+            u[n] = t[n].unflatten(0, (4, 6))
+        y3 = ssm.group_norm(u["x"], 2, u["weight"], u["bias"], z=u["z"])
+        assert torch.equal(y3.flatten(0, 1), y)
+    one = t["x"][:1].expand(24, 128)
+    t["x"] = one
+    check(t, 2, "gate_first")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_large_mean_keeps_the_variance(dtype):
+    """A mean 50 times the spread: the variance is formed from the differences."""
+    check(make(20, 256, dtype, seed=5, offset=50.0), 2, "none", eps=1e-6)
+
+
+def test_constant_groups_and_eps():
+    x = torch.full((4, 64), 3.0, device="cuda")
+    y = ssm.group_norm(x, 4, eps=1e-5)
+    assert (y == 0).all()
+    y = ssm.group_norm(torch.zeros(4, 64, device="cuda"), 4, rms=True, eps=1e-5)
+    assert (y == 0).all()
+
+
+def test_non_finite_rows_stay_alone():
+    t = make(6, 128, F32, seed=6)
+    clean, _, _ = run(t, 2, "gate", back=False)
+    t["x"][2, 5] = float("nan")
+    t["x"][4, 100] = float("inf")
+    y, _, _ = run(t, 2, "gate", back=False)
+    assert torch.isnan(y[2, :64]).all() and torch.isnan(y[4, 64:]).any()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[2, :64] = keep[4, 64:] = False
+    assert torch.equal(y[keep], clean[keep])
+
+
+def test_gates_at_the_ends():
+    """silu far out on both sides: 0 and z, no NaN."""
+    x = torch.randn(2, 64, generator=torch.Generator().manual_seed(1)).cuda()
+    z = torch.tensor([-1e30, -200.0, -88.0, 200.0]).repeat(16).expand(2, 64).contiguous().cuda()
+    y = ssm.group_norm(x, 1, z=z)
+    n = ssm.group_norm(x, 1)
+    zz = z.double()
+    want = n.double() * torch.where(zz > -300, zz * torch.sigmoid(zz), torch.zeros_like(zz))
+    assert torch.isfinite(y).all()
+    assert torch.allclose(y.double(), want, rtol=1e-5, atol=1e-30)
+    g = ssm.group_norm_bwd(x, torch.ones_like(x), 1, z=z)
+    assert torch.isfinite(g["dx"]).all() and torch.isfinite(g["dz"]).all()
+
+
+def test_gradients_against_differences():
+    """Central differences of the 64-bit definition along a random direction."""
+    gen = torch.Generator().manual_seed(3)
+    for mode in MODES:
+        t = make(5, 48, F32, seed=8)
+        _, g, kw = run(t, 3, mode)
+        names = [("x", "dx"), ("weight", "dweight"), ("bias", "dbias")] + ([("z", "dz")] if kw["z"] is not None else [])
+        for n, gn in names:
+            d = torch.randn(t[n].shape, generator=gen).double()
+            e = 1e-5
+
+            def loss(s):
+                u = {m: (None if t[m] is None else t[m].cpu().double()) for m in ("x", "z", "weight", "bias")}
+                u[n] = u[n] + s * d
+                k2 = dict(kw, weight=u["weight"], bias=u["bias"])
+                if kw["z"] is not None:
+                    k2["z"] = u["z"]
+                return float((R.norm(u["x"], 3, **k2)["y"][0] * t["dy"].cpu().double()).sum())
+
+            want = (loss(e) - loss(-e)) / (2 * e)
+            terms = g[gn].cpu().double() * d
+            assert abs(float(terms.sum()) - want) <= 1e-5 * float(terms.abs().sum()), (mode, n)
+
+
+def test_gradients_asked_for():
+    t = make(70, 96, F32, seed=9)
+    kw = dict(weight=t["weight"], bias=t["bias"])
+    full = ssm.group_norm_bwd(t["x"], t["dy"], 3, **kw)
+    some = ssm.group_norm_bwd(t["x"], t["dy"], 3, want_dweight=False, want_dbias=False, **kw)
+    one = ssm.group_norm_bwd(t["x"], t["dy"], 3, want_dbias=False, **kw)
+    torch.cuda.synchronize()
+    assert set(some) == {"dx"} and torch.equal(some["dx"], full["dx"])
+    assert "dbias" not in one and torch.equal(one["dweight"], full["dweight"])
+    again = ssm.group_norm_bwd(t["x"], t["dy"], 3, **kw)
+    for n in full:
+        assert torch.equal(full[n], again[n])
+
+
+def test_empty():
+    x = torch.zeros(0, 64, device="cuda")
+    assert ssm.group_norm(x, 2).shape == (0, 64)
+    g = ssm.group_norm_bwd(x, x, 2)
+    assert (g["dweight"] == 0).all() and (g["dbias"] == 0).all()
+    assert ssm.group_norm(torch.zeros(3, 0, device="cuda"), 1).shape == (3, 0)
+
+
+def test_offsets_past_32_bits():
+    far = 3 << 29
+    buf = torch.empty(far * 2 + 64, dtype=F32, device="cuda")
+    x = buf.as_strided((3, 64), (far, 1))
+    u = make(3, 64, F32, seed=12)
+    x.copy_(u["x"])
+    t = dict(u, x=x)
+    y, g = check(t, 2, "gate")
+    y2, g2 = check(u, 2, "gate")
+    assert torch.equal(y, y2) and torch.equal(g["dx"], g2["dx"])
+
+
+def test_graph_replays():
+    t = make(100, 256, BF16, seed=13)
+    kw = dict(weight=t["weight"], bias=t["bias"], z=t["z"])
+
+    def body():
+        g = ssm.group_norm_bwd(t["x"], t["dy"], 4, **kw)
+        return [ssm.group_norm(t["x"], 4, **kw)] + [g[n] for n in sorted(g)]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        body()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = body()
+    for i in range(4):
+        u = make(100, 256, BF16, seed=300 + i)
+        for n in t:
+            t[n].copy_(u[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in outs]
+        for a, b in zip(got, body()):
+            assert torch.equal(a, b)
+        torch.cuda.synchronize()
+
+
+def test_binding_refuses():
+    x = torch.zeros(4, 64, device="cuda")
+    for args, kw in [((x.cpu(), 2), {}), ((x.half(), 2), {}), ((x, 3), {}), ((x, 0), {}),
+                     ((x, 2), dict(act="gelu")), ((x, 2), dict(act="silu", z=x)), ((x, 2), dict(gate_first=True)),
+                     ((x, 2), dict(z=x[:2])), ((x, 2), dict(z=x.bfloat16())), ((x, 2), dict(y=x)),
+                     ((x, 2), dict(weight=x[0].bfloat16())), ((x, 2), dict(weight=x[0, :32])),
+                     ((x, 2), dict(eps=-1.0)), ((x, 2), dict(eps=float("nan"))), ((x.t(), 2), {}),
+                     ((torch.zeros(4, 6, 64, device="cuda").transpose(0, 1)[:, :3], 2), {})]:
+        with pytest.raises(ValueError):
+            ssm.group_norm(*args, **kw)
+    with pytest.raises(ValueError):
+        ssm.group_norm_bwd(x, x[:2], 2)
