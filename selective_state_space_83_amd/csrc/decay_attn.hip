@@ -94,36 +94,6 @@ ssm_status_t check_alias(const Named* outs, int nout, const Named* ins, int nin)
   return SSM_OK;
 }
 
-ssm_status_t check_fwd(const ssm_decay_attn_args_t* a, Sizes* z) {
-  if (!a) return fail(SSM_ERR_NULL, "args is NULL");
-  *z = Sizes{a->batch, a->seqlen, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
-  if (ssm_status_t st = check_sizes(z)) return st;
-  if (ssm_status_t st = check_dtypes(a->dtype, a->decay_dtype)) return st;
-  if (a->span < 0 || a->span % kSpanAlign != 0)
-    return fail(SSM_ERR_UNSUPPORTED, "span must be a non-negative multiple of %lld", (long long)kSpanAlign);
-  if (a->reserved != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved field must be 0");
-  if (z->B * z->H == 0) return SSM_OK;
-  if (z->L > 0 && (!a->q || !a->k || !a->v || !a->log_decay || !a->o))
-    return fail(SSM_ERR_NULL, "q, k, v, log_decay and o are required");
-  if (misaligned(a->lengths, 4) || misaligned(a->h0, 4) || misaligned(a->h_last, 4) ||
-      misaligned(a->o, dtype_size(a->dtype)))
-    return fail(SSM_ERR_UNSUPPORTED, "misaligned pointer (element alignment)");
-  const int64_t kn[] = {z->B, z->L, z->Hk}, vn[] = {z->B, z->L, z->H};
-  Range q, k, v, g;
-  if (ssm_status_t st = check_rows("q", a->q, kn, a->q_stride, 3, z->dk, a->dtype, &q)) return st;
-  if (ssm_status_t st = check_rows("k", a->k, kn, a->k_stride, 3, z->dk, a->dtype, &k)) return st;
-  if (ssm_status_t st = check_rows("v", a->v, vn, a->v_stride, 3, z->dv, a->dtype, &v)) return st;
-  if (ssm_status_t st = check_rows("log_decay", a->log_decay, vn, a->decay_stride, 3, 1, a->decay_dtype, &g))
-    return st;
-  const size_t state = size_t(z->state) * 4;
-  const Named outs[] = {
-      {"o", {a->o, size_t(z->tokens) * size_t(z->H * z->dv) * dtype_size(a->dtype)}},
-      {"h_last", {a->h_last, state}}};
-  const Named ins[] = {{"q", q}, {"k", k}, {"v", v}, {"log_decay", g}, {"h0", {a->h0, state}},
-                       {"lengths", {a->lengths, size_t(z->B) * 4}}};
-  return check_alias(outs, 2, ins, 6);
-}
-
 ssm_status_t check_step(const ssm_decay_attn_step_args_t* a, Sizes* z) {
   if (!a) return fail(SSM_ERR_NULL, "args is NULL");
   *z = Sizes{a->batch, 1, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
@@ -147,13 +117,63 @@ ssm_status_t check_step(const ssm_decay_attn_step_args_t* a, Sizes* z) {
   return check_alias(outs, 2, ins, 4);
 }
 
-// Workspace of the backward pass.
-struct BwdPlan {
-  int64_t dq_tiles = 0, dk_tiles = 0;   // tiles of key_dim in the dq and dk passes
-  size_t off_s = 0, off_u = 0, off_w = 0, off_dq = 0, off_dk = 0, total = 0;
+// How the time axis is cut: `spans` spans of `span` tokens (a multiple of
+// kSpanAlign) walked by workgroups of their own.  `walkers` is the number of
+// workgroups one span gives.  More spans than one cost a second read of the
+// keys and values, so they are cut only as far as fills the GPU (kTargetGroups,
+// two workgroups for each of 256 CUs), and not below kMinSpan tokens.
+constexpr int64_t kTargetGroups = 512;
+constexpr int64_t kMinSpan = 256;
+
+struct Cut {
+  int64_t span = kSpanAlign, spans = 1;
 };
 
-BwdPlan make_bwd_plan(const Sizes& z) {
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+Cut cut_time(int64_t L, int64_t walkers, int32_t span) {
+  Cut c;
+  if (L == 0 || walkers == 0) return c;
+  if (span > 0) {
+    c.span = std::min<int64_t>(span, round_up(L, kSpanAlign));
+  } else {
+    const int64_t n = std::max<int64_t>(1, std::min((kTargetGroups + walkers - 1) / walkers, L / kMinSpan));
+    c.span = round_up((L + n - 1) / n, kSpanAlign);
+  }
+  c.spans = (L + c.span - 1) / c.span;
+  return c;
+}
+
+// Columns a workgroup takes: two tiles of 64 where there are that many and the
+// state's rows leave the registers for it.
+int64_t tile_width(int64_t M, int64_t N) { return M <= 128 && N > 64 ? 128 : 64; }
+int64_t tiles_of(int64_t M, int64_t N) { return (N + tile_width(M, N) - 1) / tile_width(M, N); }
+
+// Workspace of the forward pass: the states entering the spans and their decays.
+struct FwdPlan {
+  Cut cut;
+  size_t off_total = 0, total = 0;
+};
+
+FwdPlan make_fwd_plan(const Sizes& z, int32_t span) {
+  FwdPlan pl;
+  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dk, z.dv), span);
+  if (pl.cut.spans > 1) {
+    pl.off_total = align256(size_t(z.state) * size_t(pl.cut.spans) * 4);
+    pl.total = pl.off_total + align256(size_t(z.B * z.H) * size_t(pl.cut.spans) * 4);
+  }
+  return pl;
+}
+
+// Workspace of the backward pass.
+struct BwdPlan {
+  Cut cut;
+  int64_t slices = 0;   // column slices of key_dim whose dots are kept apart
+  size_t off_carry = 0, off_rcarry = 0, off_total = 0, off_s = 0, off_u = 0, off_w = 0, off_dq = 0, off_dk = 0,
+         total = 0;
+};
+
+BwdPlan make_bwd_plan(const Sizes& z, int32_t span) {
   BwdPlan pl;
   if (z.tokens == 0 || z.H == 0) return pl;
   size_t off = 0;
@@ -162,16 +182,68 @@ BwdPlan make_bwd_plan(const Sizes& z) {
     off += align256(bytes);
     return o;
   };
-  pl.dq_tiles = pl.dk_tiles = (z.dk + kWave - 1) / kWave;
-  const size_t th = size_t(z.tokens) * size_t(z.H);
+  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dv, z.dk), span);
+  pl.slices = 4 * tiles_of(z.dv, z.dk);
+  const size_t th = size_t(z.tokens) * size_t(z.H), spans = pl.cut.spans > 1 ? size_t(pl.cut.spans) : 0;
+  pl.off_carry = take(size_t(z.state) * spans * 4);
+  pl.off_rcarry = take(size_t(z.state) * spans * 4);
+  pl.off_total = take(size_t(z.B * z.H) * spans * 4);
   pl.off_s = take(size_t(z.state) * 4);
-  pl.off_u = take(th * size_t(pl.dq_tiles) * 4);
-  pl.off_w = take(th * size_t(pl.dk_tiles) * 4);
+  pl.off_u = take(th * size_t(pl.slices) * 4);
+  pl.off_w = take(th * size_t(pl.slices) * 4);
   const bool shared = z.H != z.Hk;
   pl.off_dq = take(shared ? th * size_t(z.dk) * 4 : 0);
   pl.off_dk = take(shared ? th * size_t(z.dk) * 4 : 0);
   pl.total = off;
   return pl;
+}
+
+// Launches of a plan stay within one grid.
+ssm_status_t check_grid(const Sizes& z, const Cut& c) {
+  int64_t n, m;
+  if (!mul_ok(z.B * z.H * 4, c.spans, &n) || n > kMaxGrid || !mul_ok(z.B * z.H, 256, &m) || m > kMaxGrid ||
+      !mul_ok(z.state, c.spans, &m) || m > INT64_MAX / 16)
+    return fail(SSM_ERR_SHAPE, "problem too large for one launch");
+  return SSM_OK;
+}
+
+ssm_status_t check_fwd(const ssm_decay_attn_args_t* a, Sizes* z, FwdPlan* pl) {
+  if (!a) return fail(SSM_ERR_NULL, "args is NULL");
+  *z = Sizes{a->batch, a->seqlen, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
+  if (ssm_status_t st = check_sizes(z)) return st;
+  if (ssm_status_t st = check_dtypes(a->dtype, a->decay_dtype)) return st;
+  if (a->span < 0 || a->span % kSpanAlign != 0)
+    return fail(SSM_ERR_UNSUPPORTED, "span must be a non-negative multiple of %lld", (long long)kSpanAlign);
+  if (a->reserved != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved field must be 0");
+  *pl = make_fwd_plan(*z, a->span);
+  if (ssm_status_t st = check_grid(*z, pl->cut)) return st;
+  if (z->B * z->H == 0) return SSM_OK;
+  if (z->L > 0 && (!a->q || !a->k || !a->v || !a->log_decay || !a->o))
+    return fail(SSM_ERR_NULL, "q, k, v, log_decay and o are required");
+  if (misaligned(a->lengths, 4) || misaligned(a->h0, 4) || misaligned(a->h_last, 4) ||
+      misaligned(a->o, dtype_size(a->dtype)) || misaligned(a->workspace, 256))
+    return fail(SSM_ERR_UNSUPPORTED, "misaligned pointer (element alignment; workspace 256 bytes)");
+  const int64_t kn[] = {z->B, z->L, z->Hk}, vn[] = {z->B, z->L, z->H};
+  Range q, k, v, g;
+  if (ssm_status_t st = check_rows("q", a->q, kn, a->q_stride, 3, z->dk, a->dtype, &q)) return st;
+  if (ssm_status_t st = check_rows("k", a->k, kn, a->k_stride, 3, z->dk, a->dtype, &k)) return st;
+  if (ssm_status_t st = check_rows("v", a->v, vn, a->v_stride, 3, z->dv, a->dtype, &v)) return st;
+  if (ssm_status_t st = check_rows("log_decay", a->log_decay, vn, a->decay_stride, 3, 1, a->decay_dtype, &g))
+    return st;
+  const size_t state = size_t(z->state) * 4;
+  const Named outs[] = {
+      {"o", {a->o, size_t(z->tokens) * size_t(z->H * z->dv) * dtype_size(a->dtype)}},
+      {"h_last", {a->h_last, state}},
+      {"workspace", {a->workspace, pl->total}}};
+  const Named ins[] = {{"q", q}, {"k", k}, {"v", v}, {"log_decay", g}, {"h0", {a->h0, state}},
+                       {"lengths", {a->lengths, size_t(z->B) * 4}}};
+  if (pl->total > 0) {
+    if (!a->workspace) return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes required", pl->total);
+    if (a->workspace_bytes < pl->total)
+      return fail(SSM_ERR_WORKSPACE, "workspace has %zu bytes, %zu required", a->workspace_bytes,
+                  pl->total);
+  }
+  return check_alias(outs, 3, ins, 6);
 }
 
 ssm_status_t check_bwd(const ssm_decay_attn_bwd_args_t* a, Sizes* z, BwdPlan* pl) {
@@ -182,7 +254,9 @@ ssm_status_t check_bwd(const ssm_decay_attn_bwd_args_t* a, Sizes* z, BwdPlan* pl
   if (a->span < 0 || a->span % kSpanAlign != 0)
     return fail(SSM_ERR_UNSUPPORTED, "span must be a non-negative multiple of %lld", (long long)kSpanAlign);
   if (a->reserved != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved field must be 0");
-  *pl = make_bwd_plan(*z);
+  *pl = make_bwd_plan(*z, a->span);
+  if (ssm_status_t st = check_grid(*z, pl->cut)) return st;
+  if (z->tokens * z->Hk * z->dk / 256 >= kMaxGrid) return fail(SSM_ERR_SHAPE, "problem too large for one launch");
   if (z->B * z->H == 0) return SSM_OK;
   if (z->L > 0 && (!a->q || !a->k || !a->v || !a->log_decay || !a->dout || !a->dq || !a->dk ||
                    !a->dv || !a->dlog_decay))
@@ -223,14 +297,52 @@ ssm_status_t check_bwd(const ssm_decay_attn_bwd_args_t* a, Sizes* z, BwdPlan* pl
 // launches
 // ---------------------------------------------------------------------------
 
-template <typename T, typename OutT>
-ssm_status_t run_mix(const MixParams& p, hipStream_t s) {
-  const dim3 grid(uint32_t(p.B * p.H), uint32_t((p.N + kWave - 1) / kWave));
-  if (p.M <= 64)
-    hipLaunchKernelGGL((k_mix_simple<T, OutT, 64>), grid, dim3(kWave), 0, s, p);
-  else
-    hipLaunchKernelGGL((k_mix_simple<T, OutT, 256>), grid, dim3(kWave), 0, s, p);
-  return launch_status("k_mix_simple");
+// Whether every row of an input starts on 16 bytes and holds whole 16 bytes.
+bool wide(const Rows& r, int64_t n, size_t elem) {
+  const int64_t k = int64_t(16 / elem);
+  return !misaligned(r.p, 16) && n % k == 0 && r.sb % k == 0 && r.st % k == 0 && r.sh % k == 0;
+}
+
+template <typename T, int MP, int NT, int SP, typename OutT, bool STATE>
+ssm_status_t launch_mix(const MixParams& p, hipStream_t s) {
+  // fp32 takes chunks of 32 tokens: its products are the bound, and those of
+  // the scores grow with the chunk
+  constexpr int CT = sizeof(T) == 2 ? 64 : 32;
+  hipLaunchKernelGGL((k_mix<T, MP, NT, CT, sizeof(T) == 2 ? SP : 1, OutT, STATE>),
+                     dim3(uint32_t(p.B * p.H * p.tiles * p.spans)), dim3(256), 0, s, p);
+  return launch_status("k_mix");
+}
+
+template <typename T, int SP, typename OutT, bool STATE>
+ssm_status_t run_mix(MixParams p, hipStream_t s) {
+  p.va = STATE ? 0 : wide(p.a, p.M, sizeof(T));
+  p.vb = wide(p.b, p.M, sizeof(T));
+  p.vc = wide(p.c, p.N, sizeof(T));
+  p.vx = p.dots ? wide(p.x, p.N, sizeof(T)) : 0;
+  p.vo = !STATE && !misaligned(p.out, 16) && p.N % (16 / int64_t(sizeof(OutT))) == 0;
+  const bool two = tile_width(p.M, p.N) == 128;
+  p.tiles = int32_t(tiles_of(p.M, p.N));
+  if (p.M <= 32) return two ? launch_mix<T, 32, 2, SP, OutT, STATE>(p, s) : launch_mix<T, 32, 1, SP, OutT, STATE>(p, s);
+  if (p.M <= 64) return two ? launch_mix<T, 64, 2, SP, OutT, STATE>(p, s) : launch_mix<T, 64, 1, SP, OutT, STATE>(p, s);
+  if (p.M <= 128)
+    return two ? launch_mix<T, 128, 2, SP, OutT, STATE>(p, s) : launch_mix<T, 128, 1, SP, OutT, STATE>(p, s);
+  return launch_mix<T, 256, 1, SP, OutT, STATE>(p, s);
+}
+
+// The states entering the spans of p (which has its b, c, s0 and span set): the
+// state pass into `carry`, then the join.
+template <typename T>
+ssm_status_t run_carries(MixParams p, float* carry, float* total, hipStream_t s) {
+  p.sum = carry;
+  p.total = total;
+  p.dots = nullptr;
+  p.out = nullptr;
+  p.s_last = nullptr;
+  if (ssm_status_t st = run_mix<T, 1, T, true>(p, s)) return st;
+  JoinParams j{carry, total, p.s0, p.sm, p.sn, int64_t(p.M) * p.N, p.N, p.spans};
+  const int64_t blocks = p.B * p.H * ((j.inner + 255) / 256);
+  hipLaunchKernelGGL(k_join_spans, dim3(uint32_t(blocks)), dim3(256), 0, s, j);
+  return launch_status("k_join_spans");
 }
 
 ssm_status_t copy_state(float* dst, const float* src, int64_t n, hipStream_t s) {
@@ -248,7 +360,7 @@ Decay decay(const void* p, const int64_t* st, int32_t dtype) {
 }
 
 template <typename T>
-ssm_status_t run_fwd(const ssm_decay_attn_args_t* a, const Sizes& z, hipStream_t s) {
+ssm_status_t run_fwd(const ssm_decay_attn_args_t* a, const Sizes& z, const FwdPlan& pl, hipStream_t s) {
   MixParams p{};
   const int64_t per = z.H / z.Hk;
   p.a = rows(a->q, a->q_stride, per);
@@ -257,16 +369,26 @@ ssm_status_t run_fwd(const ssm_decay_attn_args_t* a, const Sizes& z, hipStream_t
   p.g = decay(a->log_decay, a->decay_stride, a->decay_dtype);
   p.lengths = a->lengths;
   p.s0 = a->h0;
-  p.s_last = a->h_last;
   p.sm = z.dv;
   p.sn = 1;
-  p.out = a->o;
   p.B = z.B;
   p.L = z.L;
   p.H = z.H;
   p.M = int32_t(z.dk);
   p.N = int32_t(z.dv);
-  return run_mix<T, T>(p, s);
+  p.span = pl.cut.span;
+  p.spans = int32_t(pl.cut.spans);
+  if (p.spans > 1) {
+    char* ws = static_cast<char*>(a->workspace);
+    float* carry = reinterpret_cast<float*>(ws);
+    if (ssm_status_t st = run_carries<T>(p, carry, reinterpret_cast<float*>(ws + pl.off_total), s)) return st;
+    p.carry = carry;
+    p.cm = z.dv;
+    p.cn = 1;
+  }
+  p.s_last = a->h_last;
+  p.out = a->o;
+  return run_mix<T, 1, T, false>(p, s);
 }
 
 template <typename T>
@@ -277,12 +399,17 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   const bool shared = per > 1;
   const Rows q = rows(a->q, a->q_stride, per), k = rows(a->k, a->k_stride, per);
   const Rows v = rows(a->v, a->v_stride, 1), d = rows(a->dout, a->dout_stride, 1);
+  float* carry = reinterpret_cast<float*>(ws + pl.off_carry);
+  float* rcarry = reinterpret_cast<float*>(ws + pl.off_rcarry);
+  float* total = reinterpret_cast<float*>(ws + pl.off_total);
   MixParams p{};
   p.g = decay(a->log_decay, a->decay_stride, a->decay_dtype);
   p.lengths = a->lengths;
   p.B = z.B;
   p.L = z.L;
   p.H = z.H;
+  p.span = pl.cut.span;
+  p.spans = int32_t(pl.cut.spans);
   // dq, with the state transposed: S(m, n) at row n of the stored state
   MixParams dq = p;
   dq.a = d;
@@ -290,28 +417,21 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   dq.c = k;
   dq.x = q;
   dq.s0 = a->h0;
-  dq.s_last = a->dh_last ? reinterpret_cast<float*>(ws + pl.off_s) : nullptr;
   dq.sm = 1;
   dq.sn = z.dv;
   dq.M = int32_t(z.dv);
   dq.N = int32_t(z.dk);
-  dq.dots = reinterpret_cast<float*>(ws + pl.off_u);
-  dq.out = shared ? ws + pl.off_dq : a->dq;
+  dq.cm = z.dk;
+  dq.cn = 1;
   // dk, backward in time, G transposed
-  MixParams dk = p;
+  MixParams dk = dq;
   dk.reverse = 1;
   dk.a = v;
   dk.b = d;
   dk.c = q;
   dk.x = k;
   dk.s0 = a->dh_last;
-  dk.sm = 1;
-  dk.sn = z.dv;
-  dk.M = int32_t(z.dv);
-  dk.N = int32_t(z.dk);
-  dk.dots = reinterpret_cast<float*>(ws + pl.off_w);
-  dk.out = shared ? ws + pl.off_dk : a->dk;
-  // dv, backward in time
+  // dv, backward in time, the same G
   MixParams dv = p;
   dv.reverse = 1;
   dv.a = k;
@@ -323,11 +443,24 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   dv.sn = 1;
   dv.M = int32_t(z.dk);
   dv.N = int32_t(z.dv);
+  dv.cm = 1;
+  dv.cn = z.dk;
   dv.out = a->dv;
-  if (ssm_status_t st = run_mix<T, T>(dv, s)) return st;
+  if (p.spans > 1) {
+    if (ssm_status_t st = run_carries<T>(dq, carry, total, s)) return st;
+    if (ssm_status_t st = run_carries<T>(dk, rcarry, total, s)) return st;
+    dq.carry = carry;
+    dk.carry = dv.carry = rcarry;
+  }
+  dq.s_last = a->dh_last ? reinterpret_cast<float*>(ws + pl.off_s) : nullptr;
+  dq.dots = reinterpret_cast<float*>(ws + pl.off_u);
+  dk.dots = reinterpret_cast<float*>(ws + pl.off_w);
+  dq.out = shared ? ws + pl.off_dq : a->dq;
+  dk.out = shared ? ws + pl.off_dk : a->dk;
+  if (ssm_status_t st = run_mix<T, 1, T, false>(dv, s)) return st;
   if (shared) {
-    if (ssm_status_t st = run_mix<T, float>(dq, s)) return st;
-    if (ssm_status_t st = run_mix<T, float>(dk, s)) return st;
+    if (ssm_status_t st = run_mix<T, 2, float, false>(dq, s)) return st;
+    if (ssm_status_t st = run_mix<T, 2, float, false>(dk, s)) return st;
     const int64_t n = z.tokens * z.Hk * z.dk;
     const dim3 grid(uint32_t((n + 255) / 256));
     for (int i = 0; i < 2; ++i) {
@@ -336,25 +469,29 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
       if (ssm_status_t st = launch_status("k_sum_heads")) return st;
     }
   } else {
-    if (ssm_status_t st = run_mix<T, T>(dq, s)) return st;
-    if (ssm_status_t st = run_mix<T, T>(dk, s)) return st;
+    if (ssm_status_t st = run_mix<T, 2, T, false>(dq, s)) return st;
+    if (ssm_status_t st = run_mix<T, 2, T, false>(dk, s)) return st;
   }
   DecayGradParams gp{};
   gp.u = dq.dots;
   gp.w = dk.dots;
+  gp.carry = carry;
+  gp.rcarry = rcarry;
   gp.s_last = dq.s_last;
   gp.dh_last = a->dh_last;
+  gp.g = p.g;
   gp.lengths = a->lengths;
   gp.dg = a->dlog_decay;
   gp.B = z.B;
   gp.L = z.L;
   gp.H = z.H;
   gp.inner = z.dk * z.dv;
-  gp.utiles = int32_t(pl.dq_tiles);
-  gp.wtiles = int32_t(pl.dk_tiles);
+  gp.span = pl.cut.span;
+  gp.spans = int32_t(pl.cut.spans);
+  gp.uslices = gp.wslices = int32_t(pl.slices);
   gp.bf16 = a->decay_dtype == SSM_BF16;
-  hipLaunchKernelGGL(k_decay_grad_simple, dim3(uint32_t(z.B * z.H)), dim3(kWave), 0, s, gp);
-  return launch_status("k_decay_grad_simple");
+  hipLaunchKernelGGL(k_decay_grad, dim3(uint32_t(z.B * z.H * gp.spans)), dim3(256), 0, s, gp);
+  return launch_status("k_decay_grad");
 }
 
 }  // namespace
@@ -362,25 +499,28 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
 extern "C" {
 
 size_t ssm_decay_attn_workspace_size(const ssm_decay_attn_args_t* a) {
-  (void)a;
-  return 0;
+  if (!a || a->span < 0 || a->span % kSpanAlign != 0) return 0;
+  Sizes z{a->batch, a->seqlen, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
+  if (check_sizes(&z)) return 0;
+  return make_fwd_plan(z, a->span).total;
 }
 
 size_t ssm_decay_attn_bwd_workspace_size(const ssm_decay_attn_bwd_args_t* a) {
-  if (!a) return 0;
+  if (!a || a->span < 0 || a->span % kSpanAlign != 0) return 0;
   Sizes z{a->batch, a->seqlen, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
   if (check_sizes(&z)) return 0;
-  return make_bwd_plan(z).total;
+  return make_bwd_plan(z, a->span).total;
 }
 
 ssm_status_t ssm_decay_attn_fwd(const ssm_decay_attn_args_t* a, void* hip_stream) {
   clear_message();
   Sizes z;
-  if (ssm_status_t st = check_fwd(a, &z)) return st;
+  FwdPlan pl;
+  if (ssm_status_t st = check_fwd(a, &z, &pl)) return st;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   if (z.B * z.H == 0) return SSM_OK;
   if (z.L == 0) return copy_state(a->h_last, a->h0, z.state, s);
-  return a->dtype == SSM_F32 ? run_fwd<float>(a, z, s) : run_fwd<bf16_t>(a, z, s);
+  return a->dtype == SSM_F32 ? run_fwd<float>(a, z, pl, s) : run_fwd<bf16_t>(a, z, pl, s);
 }
 
 ssm_status_t ssm_decay_attn_step(const ssm_decay_attn_step_args_t* a, void* hip_stream) {
