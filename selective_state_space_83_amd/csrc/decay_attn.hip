@@ -118,36 +118,56 @@ ssm_status_t check_step(const ssm_decay_attn_step_args_t* a, Sizes* z) {
 }
 
 // How the time axis is cut: `spans` spans of `span` tokens (a multiple of
-// kSpanAlign) walked by workgroups of their own.  `walkers` is the number of
-// workgroups one span gives.  More spans than one cost a second read of the
-// keys and values, so they are cut only as far as fills the GPU (kTargetGroups,
-// two workgroups for each of 256 CUs), and not below kMinSpan tokens.
-constexpr int64_t kTargetGroups = 512;
-constexpr int64_t kMinSpan = 256;
-
+// kSpanAlign), each walked by workgroups of its own.
 struct Cut {
   int64_t span = kSpanAlign, spans = 1;
 };
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-Cut cut_time(int64_t L, int64_t walkers, int32_t span) {
+// The plan's cut, the cheapest by this count.  `walkers` workgroups walk a span
+// of n chunks in n + 1 steps (one to fill), and m of them on a CU take 0.4 +
+// 0.6 m times as long as one (measured, 32 chunks each of 128 x 128 bf16 / 64 x
+// 64 bf16 / 64 x 64 fp32, us for one, two, three on a CU: 163, 278, - / 99, 139,
+// 219 / 201, 320, 424).  More than one span costs the first pass over all but
+// the last (`state`, its share of a step), two launches (two steps), and reading
+// and writing the spans' states five times (16 MB a step).  Measured, us by
+// number of spans: 80 walkers of 128 chunks, 128 x 128 bf16: 3 330, 6 293, 12
+// 307, 24 329; 4 walkers of 2048 chunks: 64 234, 128 213, 256 264; 320 walkers
+// of 32 chunks: 1 246, 3 315; 192 walkers of 32 chunks, 64 x 64 fp32: 1 182, 2
+// 216, 4 157, 8 171.
+Cut cut_time(int64_t L, int64_t walkers, int64_t inner, double state, int32_t span) {
+  constexpr int64_t kCus = 256, kMaxSpans = 1024;
   Cut c;
   if (L == 0 || walkers == 0) return c;
+  const int64_t chunks = (L + kSpanAlign - 1) / kSpanAlign;
+  int64_t best = chunks;   // chunks of a span
   if (span > 0) {
-    c.span = std::min<int64_t>(span, round_up(L, kSpanAlign));
+    best = std::min<int64_t>(span / kSpanAlign, chunks);
   } else {
-    const int64_t n = std::max<int64_t>(1, std::min((kTargetGroups + walkers - 1) / walkers, L / kMinSpan));
-    c.span = round_up((L + n - 1) / n, kSpanAlign);
+    const int64_t most = std::min({chunks, kMaxSpans, 1 + 8 * kCus / walkers});
+    double least = 0.0;
+    auto step = [&](int64_t groups) { return 0.4 + 0.6 * double((groups + kCus - 1) / kCus); };
+    for (int64_t want = 1; want <= most; ++want) {
+      const int64_t per = (chunks + want - 1) / want, n = (chunks + per - 1) / per;
+      if (n != want) continue;
+      double cost = double(per + 1) * step(walkers * n);
+      if (n > 1)
+        cost += state * double(per + 1) * step(walkers * (n - 1)) + 2.0 + double(n * walkers) * double(inner) / 0.8e6;
+      if (want == 1 || cost < least) {
+        least = cost;
+        best = per;
+      }
+    }
   }
-  c.spans = (L + c.span - 1) / c.span;
+  c.span = best * kSpanAlign;
+  c.spans = (chunks + best - 1) / best;
   return c;
 }
 
-// Columns a workgroup takes: two tiles of 64 where there are that many and the
-// state's rows leave the registers for it.
-int64_t tile_width(int64_t M, int64_t N) { return M <= 128 && N > 64 ? 128 : 64; }
-int64_t tiles_of(int64_t M, int64_t N) { return (N + tile_width(M, N) - 1) / tile_width(M, N); }
+// Columns a workgroup takes, 16 for each of its 4 or 8 waves.
+int64_t tile_width(int64_t N) { return N > 64 ? 128 : 64; }
+int64_t tiles_of(int64_t N) { return (N + tile_width(N) - 1) / tile_width(N); }
 
 // Workspace of the forward pass: the states entering the spans and their decays.
 struct FwdPlan {
@@ -157,7 +177,7 @@ struct FwdPlan {
 
 FwdPlan make_fwd_plan(const Sizes& z, int32_t span) {
   FwdPlan pl;
-  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dk, z.dv), span);
+  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dv), z.dk * z.dv, 0.5, span);
   if (pl.cut.spans > 1) {
     pl.off_total = align256(size_t(z.state) * size_t(pl.cut.spans) * 4);
     pl.total = pl.off_total + align256(size_t(z.B * z.H) * size_t(pl.cut.spans) * 4);
@@ -182,8 +202,8 @@ BwdPlan make_bwd_plan(const Sizes& z, int32_t span) {
     off += align256(bytes);
     return o;
   };
-  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dv, z.dk), span);
-  pl.slices = 4 * tiles_of(z.dv, z.dk);
+  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dk), z.dk * z.dv, 0.25, span);
+  pl.slices = tile_width(z.dk) / 16 * tiles_of(z.dk);
   const size_t th = size_t(z.tokens) * size_t(z.H), spans = pl.cut.spans > 1 ? size_t(pl.cut.spans) : 0;
   pl.off_carry = take(size_t(z.state) * spans * 4);
   pl.off_rcarry = take(size_t(z.state) * spans * 4);
@@ -297,48 +317,63 @@ ssm_status_t check_bwd(const ssm_decay_attn_bwd_args_t* a, Sizes* z, BwdPlan* pl
 // launches
 // ---------------------------------------------------------------------------
 
-// Whether every row of an input starts on 16 bytes and holds whole 16 bytes.
-bool wide(const Rows& r, int64_t n, size_t elem) {
+// Whether rows can be read through windows (Stage in decay_attn.hpp): they
+// start on 16 bytes, hold whole 16 bytes, do not overlap, and 64 of them lie
+// within 2^31 bytes.
+bool fast_rows(const Rows& r, int64_t n, size_t elem) {
   const int64_t k = int64_t(16 / elem);
-  return !misaligned(r.p, 16) && n % k == 0 && r.sb % k == 0 && r.st % k == 0 && r.sh % k == 0;
+  return !misaligned(r.p, 16) && n % k == 0 && r.sb % k == 0 && r.st % k == 0 && r.sh % k == 0 && r.st >= n &&
+         r.st < (int64_t(1) << 31) / 64 / int64_t(elem);
 }
 
-template <typename T, int MP, int NT, int SP, typename OutT, bool STATE>
+template <typename T, int MP, int W, int SP, typename OutT, Part PART, bool REV, bool FAST>
 ssm_status_t launch_mix(const MixParams& p, hipStream_t s) {
   // fp32 takes chunks of 32 tokens: its products are the bound, and those of
   // the scores grow with the chunk
   constexpr int CT = sizeof(T) == 2 ? 64 : 32;
-  hipLaunchKernelGGL((k_mix<T, MP, NT, CT, sizeof(T) == 2 ? SP : 1, OutT, STATE>),
-                     dim3(uint32_t(p.B * p.H * p.tiles * p.spans)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((k_mix<T, MP, W, CT, sizeof(T) == 2 ? SP : 1, OutT, PART, REV, FAST>),
+                     dim3(uint32_t(p.B * p.H * p.tiles * p.walked)), dim3(64 * W), 0, s, p);
   return launch_status("k_mix");
 }
 
-template <typename T, int SP, typename OutT, bool STATE>
+template <typename T, int MP, int SP, typename OutT, Part PART, bool REV, bool FAST>
+ssm_status_t tile_mix(const MixParams& p, hipStream_t s) {
+  return tile_width(p.N) == 128 ? launch_mix<T, MP, 8, SP, OutT, PART, REV, FAST>(p, s)
+                                : launch_mix<T, MP, 4, SP, OutT, PART, REV, FAST>(p, s);
+}
+
+template <typename T, int SP, typename OutT, Part PART, bool REV, bool FAST>
+ssm_status_t size_mix(const MixParams& p, hipStream_t s) {
+  if (p.M <= 32) return tile_mix<T, 32, SP, OutT, PART, REV, FAST>(p, s);
+  if (p.M <= 64) return tile_mix<T, 64, SP, OutT, PART, REV, FAST>(p, s);
+  if (p.M <= 128) return tile_mix<T, 128, SP, OutT, PART, REV, FAST>(p, s);
+  return tile_mix<T, 256, SP, OutT, PART, REV, FAST>(p, s);
+}
+
+template <typename T, int SP, typename OutT, Part PART, bool REV>
 ssm_status_t run_mix(MixParams p, hipStream_t s) {
-  p.va = STATE ? 0 : wide(p.a, p.M, sizeof(T));
-  p.vb = wide(p.b, p.M, sizeof(T));
-  p.vc = wide(p.c, p.N, sizeof(T));
-  p.vx = p.dots ? wide(p.x, p.N, sizeof(T)) : 0;
-  p.vo = !STATE && !misaligned(p.out, 16) && p.N % (16 / int64_t(sizeof(OutT))) == 0;
-  const bool two = tile_width(p.M, p.N) == 128;
-  p.tiles = int32_t(tiles_of(p.M, p.N));
-  if (p.M <= 32) return two ? launch_mix<T, 32, 2, SP, OutT, STATE>(p, s) : launch_mix<T, 32, 1, SP, OutT, STATE>(p, s);
-  if (p.M <= 64) return two ? launch_mix<T, 64, 2, SP, OutT, STATE>(p, s) : launch_mix<T, 64, 1, SP, OutT, STATE>(p, s);
-  if (p.M <= 128)
-    return two ? launch_mix<T, 128, 2, SP, OutT, STATE>(p, s) : launch_mix<T, 128, 1, SP, OutT, STATE>(p, s);
-  return launch_mix<T, 256, 1, SP, OutT, STATE>(p, s);
+  const size_t e = sizeof(T);
+  const int64_t k = int64_t(16 / sizeof(OutT));
+  p.tiles = int32_t(tiles_of(p.N));
+  p.walked = PART == kState ? p.spans - 1 : p.spans;
+  bool fast = fast_rows(p.b, p.M, e) && fast_rows(p.c, p.N, e);
+  if (PART != kState)
+    fast = fast && fast_rows(p.a, p.M, e) && !misaligned(p.out, 16) && p.N % k == 0 &&
+           p.H * p.N < (int64_t(1) << 31) / 64 / int64_t(sizeof(OutT));
+  if (PART == kOutDots) fast = fast && fast_rows(p.x, p.N, e);
+  return fast ? size_mix<T, SP, OutT, PART, REV, true>(p, s) : size_mix<T, SP, OutT, PART, REV, false>(p, s);
 }
 
 // The states entering the spans of p (which has its b, c, s0 and span set): the
 // state pass into `carry`, then the join.
-template <typename T>
+template <typename T, bool REV>
 ssm_status_t run_carries(MixParams p, float* carry, float* total, hipStream_t s) {
   p.sum = carry;
   p.total = total;
   p.dots = nullptr;
   p.out = nullptr;
   p.s_last = nullptr;
-  if (ssm_status_t st = run_mix<T, 1, T, true>(p, s)) return st;
+  if (ssm_status_t st = run_mix<T, 1, T, kState, REV>(p, s)) return st;
   JoinParams j{carry, total, p.s0, p.sm, p.sn, int64_t(p.M) * p.N, p.N, p.spans};
   const int64_t blocks = p.B * p.H * ((j.inner + 255) / 256);
   hipLaunchKernelGGL(k_join_spans, dim3(uint32_t(blocks)), dim3(256), 0, s, j);
@@ -381,14 +416,14 @@ ssm_status_t run_fwd(const ssm_decay_attn_args_t* a, const Sizes& z, const FwdPl
   if (p.spans > 1) {
     char* ws = static_cast<char*>(a->workspace);
     float* carry = reinterpret_cast<float*>(ws);
-    if (ssm_status_t st = run_carries<T>(p, carry, reinterpret_cast<float*>(ws + pl.off_total), s)) return st;
+    if (ssm_status_t st = run_carries<T, false>(p, carry, reinterpret_cast<float*>(ws + pl.off_total), s)) return st;
     p.carry = carry;
     p.cm = z.dv;
     p.cn = 1;
   }
   p.s_last = a->h_last;
   p.out = a->o;
-  return run_mix<T, 1, T, false>(p, s);
+  return run_mix<T, 1, T, kOut, false>(p, s);
 }
 
 template <typename T>
@@ -425,7 +460,6 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   dq.cn = 1;
   // dk, backward in time, G transposed
   MixParams dk = dq;
-  dk.reverse = 1;
   dk.a = v;
   dk.b = d;
   dk.c = q;
@@ -433,7 +467,6 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   dk.s0 = a->dh_last;
   // dv, backward in time, the same G
   MixParams dv = p;
-  dv.reverse = 1;
   dv.a = k;
   dv.b = q;
   dv.c = d;
@@ -447,8 +480,8 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   dv.cn = z.dk;
   dv.out = a->dv;
   if (p.spans > 1) {
-    if (ssm_status_t st = run_carries<T>(dq, carry, total, s)) return st;
-    if (ssm_status_t st = run_carries<T>(dk, rcarry, total, s)) return st;
+    if (ssm_status_t st = run_carries<T, false>(dq, carry, total, s)) return st;
+    if (ssm_status_t st = run_carries<T, true>(dk, rcarry, total, s)) return st;
     dq.carry = carry;
     dk.carry = dv.carry = rcarry;
   }
@@ -457,10 +490,10 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   dk.dots = reinterpret_cast<float*>(ws + pl.off_w);
   dq.out = shared ? ws + pl.off_dq : a->dq;
   dk.out = shared ? ws + pl.off_dk : a->dk;
-  if (ssm_status_t st = run_mix<T, 1, T, false>(dv, s)) return st;
+  if (ssm_status_t st = run_mix<T, 1, T, kOut, true>(dv, s)) return st;
   if (shared) {
-    if (ssm_status_t st = run_mix<T, 2, float, false>(dq, s)) return st;
-    if (ssm_status_t st = run_mix<T, 2, float, false>(dk, s)) return st;
+    if (ssm_status_t st = run_mix<T, 2, float, kOutDots, false>(dq, s)) return st;
+    if (ssm_status_t st = run_mix<T, 2, float, kOutDots, true>(dk, s)) return st;
     const int64_t n = z.tokens * z.Hk * z.dk;
     const dim3 grid(uint32_t((n + 255) / 256));
     for (int i = 0; i < 2; ++i) {
@@ -469,8 +502,8 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
       if (ssm_status_t st = launch_status("k_sum_heads")) return st;
     }
   } else {
-    if (ssm_status_t st = run_mix<T, 2, T, false>(dq, s)) return st;
-    if (ssm_status_t st = run_mix<T, 2, T, false>(dk, s)) return st;
+    if (ssm_status_t st = run_mix<T, 2, T, kOutDots, false>(dq, s)) return st;
+    if (ssm_status_t st = run_mix<T, 2, T, kOutDots, true>(dk, s)) return st;
   }
   DecayGradParams gp{};
   gp.u = dq.dots;
@@ -488,7 +521,7 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   gp.inner = z.dk * z.dv;
   gp.span = pl.cut.span;
   gp.spans = int32_t(pl.cut.spans);
-  gp.uslices = gp.wslices = int32_t(pl.slices);
+  gp.slices = int32_t(pl.slices);
   gp.bf16 = a->decay_dtype == SSM_BF16;
   hipLaunchKernelGGL(k_decay_grad, dim3(uint32_t(z.B * z.H * gp.spans)), dim3(256), 0, s, gp);
   return launch_status("k_decay_grad");

@@ -58,7 +58,7 @@ struct Rows {
 
 template <typename T>
 __device__ __forceinline__ const T* row_base(const Rows& r, int64_t b, int64_t h) {
-  return static_cast<const T*>(r.p) + b * r.sb + (h / r.per) * r.sh;
+  return static_cast<const T*>(r.p) + b * r.sb + int64_t(uint32_t(h) / uint32_t(r.per)) * r.sh;
 }
 
 struct Decay {
@@ -67,10 +67,18 @@ struct Decay {
   int32_t bf16;
 };
 
-__device__ __forceinline__ float log_decay(const Decay& d, int64_t b, int64_t t, int64_t h) {
+// A log decay's bits, and its value from them: read apart, so that the read can
+// be in flight while others are made.
+__device__ __forceinline__ uint32_t log_decay_bits(const Decay& d, int64_t b, int64_t t, int64_t h) {
   const int64_t i = b * d.sb + t * d.st + h * d.sh;
-  const float g = d.bf16 ? ld(static_cast<const bf16_t*>(d.p) + i) : static_cast<const float*>(d.p)[i];
+  return d.bf16 ? static_cast<const bf16_t*>(d.p)[i] : static_cast<const uint32_t*>(d.p)[i];
+}
+__device__ __forceinline__ float log_decay_of(const Decay& d, uint32_t bits) {
+  const float g = __uint_as_float(d.bf16 ? bits << 16 : bits);
   return g < kMinLogDecay ? kMinLogDecay : g;   // a NaN stays one
+}
+__device__ __forceinline__ float log_decay(const Decay& d, int64_t b, int64_t t, int64_t h) {
+  return log_decay_of(d, log_decay_bits(d, b, t, h));
 }
 
 __device__ __forceinline__ int64_t live_tokens(const int32_t* lengths, int64_t b, int64_t L) {
@@ -93,8 +101,8 @@ struct MixParams {
   void* out;             // (B, L, H, N)
   float* dots;           // (slices of N, B, H, L): out_t . x_t over a wave's slice
   int64_t B, L, H, span; // span: tokens per span, a multiple of the chunk
-  int32_t M, N, spans, tiles, reverse;
-  int32_t va, vb, vc, vx, vo;   // rows may be read / written 16 bytes at a time
+  int32_t M, N, spans, tiles;
+  int32_t walked;        // spans of this launch: all, or (the state pass) all but the last
 };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -110,9 +118,9 @@ __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_ex
 // (lane / 16 = g and an index within the lane), and give the product with
 // column lane % 16 and rows 4 g + i.  The contracted index may be dealt to the
 // slots in any order as long as both operands agree: here lane group g holds
-// indices 4 g + i and 16 + 4 g + i (i = 0..3).  So a product, read as an
-// operand over its row index, is already in place: scores and states go from
-// one product into the next without crossing lanes.
+// indices (tile, 4 g + i), tile = 0, 1 and i = 0..3, of two products of 16 rows.
+// So a product, read as an operand over its row index, is already in place:
+// scores and states go from one product into the next without crossing lanes.
 template <typename T>
 struct Operand;
 
@@ -169,10 +177,13 @@ __device__ __forceinline__ void split(Operand<float> (&o)[SP], f32x4 lo, f32x4 h
   o[0].set(lo, hi);
 }
 
-// Rows in LDS.  bf16 rows that are read along the row hold the columns of each
-// block of 32 in the operands' order (g, half, i), so that an operand is one
-// 16-byte read; bf16 operands down the rows come from the transposing LDS read
-// (16 lanes name 4 rows x 16 columns, each lane gets one column of them).
+// Rows in LDS, read along the row (16 bytes a lane) or, as an operand over the
+// rows, down the columns: bf16 with the transposing LDS read (16 lanes name 4
+// rows x 16 columns, in any 4 groups of 4, and each lane gets one column).
+//
+// A product's rows become a contracted index in the order (tile, 4 g + i); read
+// along, lane group g holds 8 columns side by side.  Both name the same index
+// when the rows of the state's tiles are the columns m_of below.
 template <typename T>
 struct Lds;
 
@@ -180,18 +191,8 @@ template <>
 struct Lds<bf16_t> {
   static constexpr int kVec = 8;         // elements in 16 bytes
   static constexpr int kPad = 24;        // 12 words: rows fall on different banks
-  static constexpr int kPadC = 16;
-  __device__ static __forceinline__ int pos(int col) {   // col a multiple of 4
-    return (col & ~31) + 2 * (col & 12) + ((col & 16) >> 2);
-  }
-  __device__ static __forceinline__ void put(bf16_t* row, int col, u32x4 v) {
-    *reinterpret_cast<u32x2*>(row + pos(col)) = u32x2{v[0], v[1]};
-    *reinterpret_cast<u32x2*>(row + pos(col + 4)) = u32x2{v[2], v[3]};
-  }
-  __device__ static __forceinline__ void put_plain(bf16_t* row, int col, u32x4 v) {
-    *reinterpret_cast<u32x4*>(row + col) = v;
-  }
-  // along the row: block t of 32 columns
+  static constexpr int kPadC = 8;
+  // block t of 32 columns of a row
   __device__ static __forceinline__ Operand<bf16_t> along(const bf16_t* row, int t, int g) {
     Operand<bf16_t> o;
     o.v = *reinterpret_cast<const bf16x8*>(row + 32 * t + 8 * g);
@@ -211,18 +212,13 @@ struct Lds<bf16_t> {
     o.v = __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
     return o;
   }
-  // the column group a lane names for the 16 columns of tile m (rows as put())
-  __device__ static __forceinline__ int tile_col(int m, int r) { return pos(16 * m + 4 * (r & 3)); }
-  // for the out tiles (rows as put_plain()): with two tiles a lane's 4 + 4
-  // columns lie side by side, so that it stores 16 bytes
-  template <int NT>
-  __device__ static __forceinline__ int out_col(int nt, int r) {
-    return NT == 2 ? 8 * (r & 3) + 4 * nt : 4 * (r & 3);
+  // the column of the state's tile mt, row 4 g + i, and the columns a lane names
+  // to read down that tile
+  __device__ static __forceinline__ int m_of(int mt, int g, int i) {
+    return 32 * (mt >> 1) + 8 * g + 4 * (mt & 1) + i;
   }
-  template <int NT>
-  __device__ static __forceinline__ int n_of(int nt, int r) {   // column of tile nt, lane r
-    return NT == 2 ? 8 * (r >> 2) + 4 * nt + (r & 3) : r;
-  }
+  __device__ static __forceinline__ int tile_col(int mt, int r) { return m_of(mt, r & 3, 0); }
+  __device__ static __forceinline__ int group_col(int r) { return 4 * (r & 3); }   // of 16 in order
 };
 
 template <>
@@ -230,10 +226,6 @@ struct Lds<float> {
   static constexpr int kVec = 4;
   static constexpr int kPad = 4;
   static constexpr int kPadC = 4;
-  __device__ static __forceinline__ void put(float* row, int col, u32x4 v) {
-    *reinterpret_cast<u32x4*>(row + col) = v;
-  }
-  __device__ static __forceinline__ void put_plain(float* row, int col, u32x4 v) { put(row, col, v); }
   __device__ static __forceinline__ Operand<float> along(const float* row, int t, int g) {
     Operand<float> o;
     o.v[0] = *reinterpret_cast<const f32x4*>(row + 32 * t + 4 * g);
@@ -249,63 +241,119 @@ struct Lds<float> {
       for (int i = 0; i < 4; ++i) o.v[h][i] = s[(32 * t + 16 * h + 4 * g + i) * stride + col];
     return o;
   }
-  __device__ static __forceinline__ int tile_col(int m, int r) { return 16 * m + r; }
-  template <int NT>
-  __device__ static __forceinline__ int out_col(int nt, int r) { return 16 * nt + r; }
-  template <int NT>
-  __device__ static __forceinline__ int n_of(int nt, int r) { return 16 * nt + r; }
+  __device__ static __forceinline__ int m_of(int mt, int g, int i) { return 16 * mt + 4 * g + i; }
+  __device__ static __forceinline__ int tile_col(int mt, int r) { return 16 * mt + r; }
+  __device__ static __forceinline__ int group_col(int r) { return r; }
 };
 
-// 16 bytes of a row from column col on, zeros past its end.
-template <typename T>
-__device__ __forceinline__ u32x4 load16(const T* row, int col, int n, bool vec) {
-  u32x4 v{0, 0, 0, 0};
-  if (vec) {
-    if (col < n) v = *reinterpret_cast<const u32x4*>(row + col);
-    return v;
-  }
-  if constexpr (sizeof(T) == 2) {
+constexpr int kBufferFlags = 0x00020000;       // gfx9-family raw buffer, 32-bit data
+constexpr uint32_t kOutside = 0x80000000u;     // an offset past any buffer: loads 0, stores nothing
+
+// A window of memory: `rows` rows (at most 0: none), `stride` bytes apart, of
+// which `width` bytes count.  Reads outside give zeros, writes nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void* base, int rows, uint32_t stride, int width) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
+                                           rows > 0 ? int(uint32_t(rows - 1) * stride) + width : 0, kBufferFlags);
+}
+
+// The rows of a chunk, on their way from memory to LDS through registers.  Rows
+// are taken in the order of their tokens; `first` is the lowest.
+//
+// FAST: rows start on 16 bytes, hold whole 16 bytes, do not overlap, and a
+// chunk's span less than 2^31 bytes (checked by the host): they are read through
+// a window that ends with the row's last token.  Otherwise element by element.
+template <typename T, int ROWS, int COLS, int THREADS, bool FAST>
+struct Stage {
+  static constexpr int kPerRow = COLS / Lds<T>::kVec;
+  static constexpr int kStep = THREADS / kPerRow;   // rows between a lane's loads
+  static constexpr bool kFew = ROWS < kStep;        // fewer loads than lanes
+  static constexpr int kCount = kFew ? 1 : ROWS / kStep;
+  static_assert(kFew || kCount * kStep == ROWS, "");
+  u32x4 v[kCount];
+  __device__ __forceinline__ void load(const T* base, int64_t st, int64_t first, int64_t live, int col0, int n) {
+    const int row = threadIdx.x / kPerRow, col = threadIdx.x % kPerRow * Lds<T>::kVec + col0;
+    if constexpr (FAST) {
+      // a window for each load, so that one offset serves them all
+      const int left = live - first < ROWS ? int(live - first) : ROWS;
+      const uint32_t pitch = uint32_t(st) * uint32_t(sizeof(T));
+      const uint32_t off =
+          col < n && (!kFew || row < ROWS) ? uint32_t(row) * pitch + uint32_t(col) * uint32_t(sizeof(T)) : kOutside;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (col + e < n) v[e >> 1] |= static_cast<uint32_t>(row[col + e]) << (16 * (e & 1));
-  } else {
+      for (int k = 0; k < kCount; ++k)
+        v[k] = __builtin_amdgcn_raw_buffer_load_b128(
+            window(base + (first + k * kStep) * st, left - k * kStep, pitch, n * int(sizeof(T))), off, 0, 0);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kCount; ++k) {
+        const int64_t t = first + row + k * kStep;
+        u32x4 u{0, 0, 0, 0};
+        if (t < live && (!kFew || row < ROWS)) {
+          const T* p = base + t * st;
+          for (int e = 0; e < Lds<T>::kVec; ++e)
+            if (col + e < n) {
+              if constexpr (sizeof(T) == 2) {
+                const uint32_t x = static_cast<uint32_t>(p[col + e]) << (16 * (e & 1));
+                u[0] |= e >> 1 == 0 ? x : 0;
+                u[1] |= e >> 1 == 1 ? x : 0;
+                u[2] |= e >> 1 == 2 ? x : 0;
+                u[3] |= e >> 1 == 3 ? x : 0;
+              } else {
+                const uint32_t x = __float_as_uint(p[col + e]);
+                u[0] = e == 0 ? x : u[0];
+                u[1] = e == 1 ? x : u[1];
+                u[2] = e == 2 ? x : u[2];
+                u[3] = e == 3 ? x : u[3];
+              }
+            }
+        }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (col + e < n) v[e] = __float_as_uint(row[col + e]);
+        for (int j = 0; j < kCount; ++j)
+          if (j == k) v[j] = u;
+      }
+    }
   }
+  // REV: the last row first
+  template <bool REV>
+  __device__ __forceinline__ void store(T* s, int stride) const {
+    const int row = threadIdx.x / kPerRow, col = threadIdx.x % kPerRow * Lds<T>::kVec;
+    if (kFew && row >= ROWS) return;
+    T* p = s + (REV ? (kFew ? ROWS : kStep) - 1 - row : row) * stride + col;
+#pragma unroll
+    for (int k = 0; k < kCount; ++k)
+      *reinterpret_cast<u32x4*>(p + (REV ? kCount - 1 - k : k) * kStep * stride) = v[k];
+  }
+};
+
+// v plus its value in other lanes (0 where there is none), over two registers.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double add_lanes(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, uint32_t(u), CTRL, ROW_MASK, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, uint32_t(u >> 32), CTRL, ROW_MASK, 0xf, false);
+  return v + __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+
+// Running sum over the wave's lanes.
+__device__ __forceinline__ double wave_running_sum(double v) {
+  v = add_lanes<0x111, 0xf>(v);   // within rows of 16: lanes 1, 2, 4 and 8 below
+  v = add_lanes<0x112, 0xf>(v);
+  v = add_lanes<0x114, 0xf>(v);
+  v = add_lanes<0x118, 0xf>(v);
+  v = add_lanes<0x142, 0xa>(v);   // row 0's last lane into row 1, row 2's into row 3
+  v = add_lanes<0x143, 0xc>(v);   // lane 31 into rows 2 and 3
   return v;
 }
 
-// The rows of a chunk, on their way from memory to LDS through registers.
-template <typename T, int ROWS, int COLS>
-struct Stage {
-  static constexpr int kPerRow = COLS / Lds<T>::kVec;
-  static constexpr int kCount = ROWS * kPerRow / 256;
-  static_assert(kCount * 256 == ROWS * kPerRow, "");
-  u32x4 v[kCount];
-  // first: token of row 0, step its direction; rows at or past live are zeros
-  __device__ __forceinline__ void load(const T* base, int64_t st, int64_t first, int step, int64_t live, int col0,
-                                       int n, bool vec) {
-#pragma unroll
-    for (int k = 0; k < kCount; ++k) {
-      const int i = threadIdx.x + 256 * k, row = i / kPerRow, col = i % kPerRow * Lds<T>::kVec + col0;
-      const int64_t t = first + int64_t(step) * row;
-      v[k] = u32x4{0, 0, 0, 0};
-      if (t < live) v[k] = load16<T>(base + t * st, col, n, vec);
-    }
-  }
-  template <bool PLAIN>
-  __device__ __forceinline__ void store(T* s, int stride) const {
-#pragma unroll
-    for (int k = 0; k < kCount; ++k) {
-      const int i = threadIdx.x + 256 * k, row = i / kPerRow, col = i % kPerRow * Lds<T>::kVec;
-      if (PLAIN)
-        Lds<T>::put_plain(s + row * stride, col, v[k]);
-      else
-        Lds<T>::put(s + row * stride, col, v[k]);
-    }
-  }
-};
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(u), 63);
+  const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(u >> 32), 63);
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+
+// What a launch forms: only the state, from zero (the first pass over spans);
+// the rows out; the rows out and their dots with x.
+enum Part : int { kState = 0, kOut = 1, kOutDots = 2 };
 
 // ---------------------------------------------------------------------------
 // The sum over a chunk of CT tokens at a time (b_i: running sum of the log
@@ -314,329 +362,322 @@ struct Stage {
 //   out_i = sum_{j <= i} exp(b_i - b_j) (a_i . b_j) c_j + exp(b_i) S^T a_i
 //   S'    = exp(b_CT) S + sum_j exp(b_CT - b_j) b_j c_j^T
 //
-// A workgroup of four waves walks the chunks of one span of one head, for 64 NT
-// of the N columns; wave w holds S for its 16 NT columns in registers.  The
-// decayed scores of 16 queries are formed by one wave and shared through LDS.
+// A workgroup walks the chunks of one span of one head, its W waves with 16 of
+// the N columns each and S for them in registers.  The decayed scores of a chunk
+// are formed once, a query tile by one or two waves, and shared through LDS.
 // Log decays are summed in 64 bits and kept as a rounded value and its rest, so
-// that differences of long sums stay exact to 2^-24 (a chunk may hold resets).
+// that differences of long sums stay exact to 2^-24 (a chunk may hold resets);
+// wave 0 does it a chunk ahead.
 //
 // With bf16 rows the products' operands are bf16: scores and the state as read
 // are rounded once (SP = 1), or kept to 16 bits (SP = 2; the gradient of the
 // decay sums differences of what they give).  The state itself is fp32: its
 // update takes the decayed rows in three parts, 24 bits.
-// STATE: only the state, from zero (the first pass over spans).
 // ---------------------------------------------------------------------------
-template <typename T, int MP, int NT, int CT, int SP, typename OutT, bool STATE>
-__global__ __launch_bounds__(256, sizeof(T) == 2 && MP <= 128 ? 2 : 1) void k_mix(MixParams p) {
+template <typename T, int MP, int W>
+constexpr int waves_per_simd() {
+  // four where registers (128 each) and LDS allow: the chunk's steps wait on
+  // each other, and other waves fill the gaps
+  return MP <= 128 ? 4 : 2;
+}
+
+template <typename T, int MP, int W, int CT, int SP, typename OutT, Part PART, bool REV, bool FAST>
+__global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(MixParams p) {
   using LD = Lds<T>;
-  constexpr int NW = 64 * NT, MT = MP / 16, QT = CT / 16, KT = CT / 32;
+  constexpr bool OUT = PART != kState;
+  constexpr int NW = 16 * W, MT = MP / 16, QT = CT / 16, KT = CT / 32;
   constexpr int SU = sizeof(T) == 2 ? 3 : 1;   // parts of the decayed rows in the state's update
   constexpr int kStride = MP + LD::kPad, kStrideC = NW + LD::kPadC;
-  __shared__ __align__(16) T sA[STATE ? 1 : CT * kStride];
+  constexpr int kScores = CT == 64 ? 6 : 2;    // operands of scores: (query tile, 32 keys) on or under the diagonal
+  __shared__ __align__(16) T sA[OUT ? CT * kStride : 1];
   __shared__ __align__(16) T sB[CT * kStride];
   __shared__ __align__(16) T sC[CT * kStrideC];
-  __shared__ __align__(16) Operand<T> sP[STATE ? 1 : SP * QT * KT * kWave];
-  __shared__ __align__(16) float sBh[CT], sBl[CT];
+  __shared__ __align__(16) Operand<T> sP[OUT ? SP * kScores * kWave : 1];
+  __shared__ __align__(16) float sBh[2][CT], sBl[2][CT], sTot[2][2];
+  // where query tile q's scores with keys 32 t.. lie: 0 0 | 1 1 2 2 and on
+  auto score_at = [](int s, int q, int t) { return (s * kScores + (q < 2 ? q : 2 * q - 2 + t)) * kWave; };
 
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, r = lane & 15;
-  int64_t id = blockIdx.x;
-  const int tile = int(id % p.tiles);
-  id /= p.tiles;
-  const int span = int(id % p.spans);
-  const int64_t bh = id / p.spans, b = bh / p.H, h = bh % p.H;
-  const int n0 = tile * NW, nw = n0 + w * 16 * NT;   // the workgroup's and the wave's columns
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t id = blockIdx.x / uint32_t(p.tiles);   // the grid is below 2^31
+  const int tile = int(blockIdx.x % uint32_t(p.tiles)), span = int(id % uint32_t(p.walked));
+  const uint32_t bh32 = id / uint32_t(p.walked);
+  const int64_t bh = bh32, b = bh32 / uint32_t(p.H), h = bh32 % uint32_t(p.H);
+  const int n0 = tile * NW, nw = n0 + w * 16;   // the workgroup's and the wave's columns
   const int64_t live = live_tokens(p.lengths, b, p.L);
 
-  const T* pa = STATE ? nullptr : row_base<T>(p.a, b, h);
+  const T* pa = OUT ? row_base<T>(p.a, b, h) : nullptr;
   const T* pb = row_base<T>(p.b, b, h);
   const T* pc = row_base<T>(p.c, b, h);
-  const T* px = !STATE && p.dots ? row_base<T>(p.x, b, h) : nullptr;
+  const T* px = PART == kOutDots ? row_base<T>(p.x, b, h) : nullptr;
+  OutT* const po = OUT ? static_cast<OutT*>(p.out) + (b * p.L * p.H + h) * p.N : nullptr;
+  const int64_t ost = p.H * p.N;
+  float* const dots = PART == kOutDots ? p.dots + ((int64_t(tile) * W + w) * p.B * p.H + bh) * p.L : nullptr;
 
-  // chunk k of the span covers positions; a position's token counts from the
-  // front or, backward, from the end of the last span: boundaries coincide
-  const int64_t pos0 = span * p.span, padded = p.span * p.spans;
+  // the lowest token of chunk k; backward, positions count from the end of the
+  // last span, so that spans and chunks have the same boundaries either way
   const int chunks = int(p.span / CT);
-  const int step = p.reverse ? -1 : 1;
-  auto first_token = [&](int k) {
-    const int64_t pos = pos0 + int64_t(k) * CT;
-    return p.reverse ? padded - 1 - pos : pos;
-  };
-  auto chunk_live = [&](int k) {   // any token of the chunk before the row's end
-    const int64_t t = first_token(k);
-    return (p.reverse ? t - (CT - 1) : t) < live;
+  auto lowest = [&](int k) {
+    const int64_t pos = span * p.span + int64_t(k) * CT;
+    return REV ? p.span * p.spans - CT - pos : pos;
   };
 
-  f32x4 S[MT][NT];
+  f32x4 S[MT];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int mt = 0; mt < MT; ++mt) S[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (OUT && (span > 0 || p.s0)) {
+    const float* src = span > 0 ? p.carry + (bh * p.spans + span) * p.M * p.N : p.s0 + bh * p.M * p.N;
+    const int64_t sm = span > 0 ? p.cm : p.sm, sn = span > 0 ? p.cn : p.sn;
+    const int n = nw + r;
+    const float* col = src + n * sn;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int n = nw + LD::template n_of<NT>(nt, r);
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int m = 16 * mt + 4 * g + i;
-        float v = 0.0f;
-        if (!STATE && m < p.M && n < p.N) {
-          if (span > 0)
-            v = p.carry[(bh * p.spans + span) * p.M * p.N + m * p.cm + n * p.cn];
-          else if (p.s0)
-            v = p.s0[bh * p.M * p.N + m * p.sm + n * p.sn];
-        }
-        S[mt][nt][i] = v;
+        const int m = LD::m_of(mt, g, i);
+        if (m < p.M && n < p.N) S[mt][i] = col[m * sm];
       }
-    }
+  }
 
-  Stage<T, CT, MP> qa, qb;
-  Stage<T, CT, NW> qc;
-  float gl = 0.0f;   // the lane's log decay, base 2
-  auto fetch = [&](int k) {
-    const int64_t t0 = first_token(k);
-    if constexpr (!STATE) qa.load(pa, p.a.st, t0, step, live, 0, p.M, p.va);
-    qb.load(pb, p.b.st, t0, step, live, 0, p.M, p.vb);
-    qc.load(pc, p.c.st, t0, step, live, n0, p.N, p.vc);
-    gl = 0.0f;
-    if (lane < CT) {
-      const int64_t t = t0 + int64_t(step) * lane;
-      const int64_t td = p.reverse ? t + 1 : t;   // backward, the decay stands behind the token
-      if (td < live) gl = log_decay(p.g, b, td, h) * kLog2e;
+  Stage<T, CT, MP, 64 * W, FAST> qa, qb;
+  Stage<T, CT, NW, 64 * W, FAST> qc;
+  uint32_t gl = 0;   // wave 0: the lane's log decay (all zeros: none)
+  auto fetch = [&](int64_t low) {
+    if (w == 0) {
+      // backward, the decay stands behind the token
+      const int64_t t = low + (REV ? CT - lane : lane);
+      gl = 0;
+      if (lane < CT && t < live) gl = log_decay_bits(p.g, b, t, h);
     }
+    if constexpr (OUT) qa.load(pa, p.a.st, low, live, 0, p.M);
+    qb.load(pb, p.b.st, low, live, 0, p.M);
+    qc.load(pc, p.c.st, low, live, n0, p.N);
+  };
+  double all = 0.0;   // wave 0: sum of the span's log decays (the state pass)
+  auto sum_decays = [&](int buf) {
+    if (w != 0) return;
+    const double bs = wave_running_sum(log_decay_of(p.g, gl) * kLog2e), tot = last_lane(bs);
+    const float hi = float(bs), toth = float(tot);
+    if (lane < CT) {
+      sBh[buf][lane] = hi;
+      sBl[buf][lane] = float(bs - hi);
+    }
+    if (lane == 0) {
+      sTot[buf][0] = toth;
+      sTot[buf][1] = float(tot - toth);
+    }
+    if (!OUT) all += tot;
   };
 
-  double all = 0.0;   // sum of the span's log decays (the state pass)
   bool have = false;
   for (int k = 0; k < chunks; ++k) {
-    const int64_t t0 = first_token(k);
-    if (!chunk_live(k)) {
-      if constexpr (!STATE) {   // nothing but zeros
-        for (int i = tid; i < CT * NW; i += 256) {
-          const int64_t t = t0 + int64_t(step) * (i / NW);
+    const int64_t low = lowest(k);
+    const int buf = k & 1;
+    if (low >= live) {   // no token: zeros
+      if constexpr (OUT) {
+        for (int i = tid; i < CT * NW; i += 64 * W) {
+          const int64_t t = low + i / NW;
           const int n = n0 + i % NW;
-          if (t < p.L && n < p.N) st(static_cast<OutT*>(p.out) + ((b * p.L + t) * p.H + h) * p.N + n, 0.0f);
+          if (t < p.L && n < p.N) st(po + t * ost + n, 0.0f);
         }
       }
       have = false;
       continue;
     }
-    if (!have) fetch(k);
-    __syncthreads();
-    if constexpr (!STATE) qa.template store<false>(sA, kStride);
-    qb.template store<false>(sB, kStride);
-    qc.template store<true>(sC, kStrideC);
-    // running sums of the log decays
-    double bs = gl;
-#pragma unroll
-    for (int d = 1; d < CT; d <<= 1) {
-      const double o = __shfl_up(bs, d);
-      if (lane >= d) bs += o;
+    if (!have) {
+      fetch(low);
+      sum_decays(buf);
     }
-    const double tot = __shfl(bs, CT - 1);
-    const float toth = float(tot), totl = float(tot - toth);
-    if (w == 0 && lane < CT) {
-      const float hi = float(bs);
-      sBh[lane] = hi;
-      sBl[lane] = float(bs - hi);
-    }
-    if (STATE) all += tot;
     __syncthreads();
-    have = k + 1 < chunks && chunk_live(k + 1);
-    if (have) fetch(k + 1);
+    if constexpr (OUT) qa.template store<REV>(sA, kStride);
+    qb.template store<REV>(sB, kStride);
+    qc.template store<REV>(sC, kStrideC);
+    __syncthreads();
+    have = k + 1 < chunks && lowest(k + 1) < live;
+    if (have) fetch(lowest(k + 1));
+    const int rows = live - low < CT ? int(live - low) : CT;       // of the chunk, with tokens
+    const int orows = p.L - low < CT ? int(p.L - low) : CT;        // with a place in out
 
-    if constexpr (!STATE) {
-      // scores of 16 queries; with 32 tokens the waves share a query tile
-      const int qt = CT == 64 ? w : w & 1;
-      const float qh = sBh[16 * qt + r], ql = sBl[16 * qt + r];
-      f32x4 pr[QT];
+    f32x4 acc[OUT ? QT : 1];
+    u32x4 xr[PART == kOutDots ? QT : 1];
+    if constexpr (OUT) {
+      if constexpr (PART == kOutDots && FAST) {
+        // the rows the dots are taken with: the lane's query, its 4 columns
+        const uint32_t pitch = uint32_t(p.x.st) * uint32_t(sizeof(T));
+        const int n = nw + 4 * g;
+        const uint32_t off =
+            n < p.N ? uint32_t(REV ? 15 - r : r) * pitch + uint32_t(n) * uint32_t(sizeof(T)) : kOutside;
 #pragma unroll
-      for (int kt = 0; kt < QT; ++kt) {
-        f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
-        if (kt <= qt && (CT == 64 || kt == (w >> 1))) {
-#pragma unroll
-          for (int t = 0; t < MP / 32; ++t)
-            acc = mma(LD::along(sB + (16 * kt + r) * kStride, t, g), LD::along(sA + (16 * qt + r) * kStride, t, g),
-                      acc);
-          const f32x4 kh = *reinterpret_cast<const f32x4*>(sBh + 16 * kt + 4 * g);
-          const f32x4 kl = *reinterpret_cast<const f32x4*>(sBl + 16 * kt + 4 * g);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e = exp2_fast((qh - kh[i]) + (ql - kl[i]));
-            acc[i] = 16 * kt + 4 * g + i <= 16 * qt + r ? acc[i] * e : 0.0f;
+        for (int q = 0; q < QT; ++q) {
+          const int row = REV ? CT - 16 - 16 * q : 16 * q;
+          const auto win = window(px + (low + row) * p.x.st, rows - row, pitch, p.N * int(sizeof(T)));
+          if constexpr (sizeof(T) == 4) {
+            xr[q] = __builtin_amdgcn_raw_buffer_load_b128(win, off, 0, 0);
+          } else {
+            const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(win, off, 0, 0);
+            xr[q] = u32x4{u[0], u[1], 0, 0};
           }
         }
-        pr[kt] = acc;
       }
-      if constexpr (CT == 64) {
+      // scores: the keys kt0.. of query tile qt that the wave takes
+      constexpr int PER = CT == 32 ? 1 : W == 8 ? 2 : 4;   // key tiles of a wave
+      const int qt = CT == 32 ? w & 1 : W == 8 ? w >> 1 : w;
+      const int kt0 = CT == 32 ? w >> 1 : W == 8 ? 2 * (w & 1) : 0;
+      if (kt0 < QT && (kt0 <= qt || CT == 32)) {
+        const float qh = sBh[buf][16 * qt + r], ql = sBl[buf][16 * qt + r];
+        f32x4 pr[PER];
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          if (2 * t <= qt) {
-            Operand<T> o[SP];
-            split<SP>(o, pr[2 * t], pr[2 * t + 1]);
+        for (int j = 0; j < PER; ++j) {
+          const int kt = kt0 + j;
+          f32x4 d{0.0f, 0.0f, 0.0f, 0.0f};
+          if (kt <= qt) {
 #pragma unroll
-            for (int s = 0; s < SP; ++s) sP[((s * QT + qt) * KT + t) * kWave + lane] = o[s];
+            for (int t = 0; t < MP / 32; ++t)
+              d = mma(LD::along(sB + (16 * kt + r) * kStride, t, g), LD::along(sA + (16 * qt + r) * kStride, t, g), d);
+            const f32x4 kh = *reinterpret_cast<const f32x4*>(sBh[buf] + 16 * kt + 4 * g);
+            const f32x4 kl = *reinterpret_cast<const f32x4*>(sBl[buf] + 16 * kt + 4 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float e = exp2_fast((qh - kh[i]) + (ql - kl[i]));
+              d[i] = 16 * kt + 4 * g + i <= 16 * qt + r ? d[i] * e : 0.0f;
+            }
           }
+          pr[j] = d;
         }
-      } else {
-        static_assert(sizeof(T) == 4 || CT == 64, "");
-        if constexpr (sizeof(T) == 4) sP[qt * kWave + lane].v[w >> 1] = (w >> 1) ? pr[1] : pr[0];
+        if constexpr (CT == 64) {
+#pragma unroll
+          for (int t = 0; t < PER / 2; ++t) {
+            if (kt0 + 2 * t <= qt) {
+              Operand<T> o[SP];
+              split<SP>(o, pr[2 * t], pr[2 * t + 1]);
+#pragma unroll
+              for (int s = 0; s < SP; ++s) sP[score_at(s, qt, kt0 / 2 + t) + lane] = o[s];
+            }
+          }
+        } else {
+          static_assert(sizeof(T) == 4 || CT == 64, "");
+          if constexpr (sizeof(T) == 4) sP[score_at(0, qt, 0) + lane].v[kt0] = pr[0];
+        }
       }
-    }
 
-    // what the state gives
-    f32x4 acc[QT][NT];
-    if constexpr (!STATE) {
+      // what the state gives
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[qt][nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int q = 0; q < QT; ++q) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int t = 0; t < MP / 32; ++t) {
-        Operand<T> so[NT][SP];
+        Operand<T> so[SP];
+        split<SP>(so, S[2 * t], S[2 * t + 1]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) split<SP>(so[nt], S[2 * t][nt], S[2 * t + 1][nt]);
+        for (int q = 0; q < QT; ++q) {
+          const Operand<T> a = LD::along(sA + (16 * q + r) * kStride, t, g);
 #pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-          const Operand<T> a = LD::along(sA + (16 * qt + r) * kStride, t, g);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int s = 0; s < SP; ++s) acc[qt][nt] = mma(so[nt][s], a, acc[qt][nt]);
+          for (int s = 0; s < SP; ++s) acc[q] = mma(so[s], a, acc[q]);
         }
       }
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) {
-        const float e = exp2_fast(sBh[16 * qt + r]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[qt][nt][i] *= e;
-      }
+      for (int q = 0; q < QT; ++q) acc[q] *= exp2_fast(sBh[buf][16 * q + r]);
       __syncthreads();
     }
 
-    Operand<T> c[KT][NT];
+    Operand<T> c[KT];
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        c[t][nt] = LD::down(sC, kStrideC, t, g, r, w * 16 * NT + LD::template out_col<NT>(nt, r));
+    for (int t = 0; t < KT; ++t) c[t] = LD::down(sC, kStrideC, t, g, r, w * 16 + LD::group_col(r));
 
-    if constexpr (!STATE) {
+    if constexpr (OUT) {
+      const uint32_t opitch = uint32_t(ost) * uint32_t(sizeof(OutT));
+      const int n = nw + 4 * g;   // the lane's columns n..n + 3
+      const uint32_t off =
+          n < p.N ? uint32_t(REV ? 15 - r : r) * opitch + uint32_t(n) * uint32_t(sizeof(OutT)) : kOutside;
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) {
+      for (int q = 0; q < QT; ++q) {
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-          if (2 * t > qt) continue;
+          if (2 * t > q) continue;
 #pragma unroll
-          for (int s = 0; s < SP; ++s) {
-            const Operand<T> o = sP[((s * QT + qt) * KT + t) * kWave + lane];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[qt][nt] = mma(c[t][nt], o, acc[qt][nt]);
-          }
+          for (int s = 0; s < SP; ++s) acc[q] = mma(c[t], sP[score_at(s, q, t) + lane], acc[q]);
         }
-        // the lane's query and its columns nw + n_of(nt, 4 g + i)
-        const int64_t t = t0 + int64_t(step) * (16 * qt + r);
-        const bool on = t < live;
-        if (t < p.L) {
-          OutT* out = static_cast<OutT*>(p.out) + ((b * p.L + t) * p.H + h) * p.N;
-          if (!on) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[qt][nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          }
-          if (sizeof(OutT) == 2 && NT == 2 && p.vo) {
-            Operand<bf16_t> o;
-            o.set(acc[qt][0], acc[qt][NT - 1]);
-            const int n = nw + 8 * g;
-            if (n < p.N) *reinterpret_cast<bf16x8*>(out + n) = o.v;
+        const int row0 = REV ? CT - 16 - 16 * q : 16 * q, row = row0 + (REV ? 15 - r : r);   // the lane's query
+        const bool on = row < rows;
+        if (!on) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (FAST) {
+          const auto win = window(po + (low + row0) * ost, orows - row0, opitch, p.N * int(sizeof(OutT)));
+          if constexpr (sizeof(OutT) == 4) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[q]), win, off, 0, 0);
           } else {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const int n = nw + LD::template n_of<NT>(nt, 4 * g);
-              if (p.vo) {
-                if (n < p.N) {
-                  if constexpr (sizeof(OutT) == 2) {
-                    Operand<bf16_t> o;
-                    o.set(acc[qt][nt], acc[qt][nt]);
-                    const u32x4 u = __builtin_bit_cast(u32x4, o.v);
-                    *reinterpret_cast<u32x2*>(out + n) = u32x2{u[0], u[1]};
-                  } else {
-                    *reinterpret_cast<f32x4*>(out + n) = acc[qt][nt];
-                  }
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (n + i < p.N) st(out + n + i, acc[qt][nt][i]);
-              }
-            }
+            Operand<bf16_t> v;
+            v.set(acc[q], acc[q]);
+            const u32x4 u = __builtin_bit_cast(u32x4, v.v);
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{u[0], u[1]}, win, off, 0, 0);
           }
+        } else if (row < orows) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) st(po + (low + row) * ost + n + i, acc[q][i]);
         }
-        if (px) {
+        if constexpr (PART == kOutDots) {
           float d = 0.0f;
-          if (on) {
-            const T* xr = px + t * p.x.st;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int n = nw + LD::template n_of<NT>(nt, 4 * g) + i;
-                if (n < p.N) d += acc[qt][nt][i] * ld(xr + n);
-              }
+          for (int i = 0; i < 4; ++i) {
+            float x = 0.0f;
+            if constexpr (!FAST) {
+              if (on && n + i < p.N) x = ld(px + (low + row) * p.x.st + n + i);
+            } else if constexpr (sizeof(T) == 4) {
+              x = __uint_as_float(xr[q][i]);
+            } else {
+              const uint32_t u = xr[q][i >> 1];
+              x = __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
+            }
+            d += acc[q][i] * x;
           }
           d += __shfl_xor(d, 16);
           d += __shfl_xor(d, 32);
-          if (g == 0 && t < p.L) p.dots[((int64_t(tile) * 4 + w) * p.B * p.H + bh) * p.L + t] = d;
+          if (g == 0 && on) dots[low + row] = d;
         }
       }
     }
 
     // the state's update
+    const float toth = sTot[buf][0], totl = sTot[buf][1];
     const float etot = exp2_fast(toth);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[mt][nt][i] *= etot;
+    for (int mt = 0; mt < MT; ++mt) S[mt] *= etot;
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       f32x4 e[2];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const f32x4 kh = *reinterpret_cast<const f32x4*>(sBh + 32 * t + 16 * hf + 4 * g);
-        const f32x4 kl = *reinterpret_cast<const f32x4*>(sBl + 32 * t + 16 * hf + 4 * g);
+        const f32x4 kh = *reinterpret_cast<const f32x4*>(sBh[buf] + 32 * t + 16 * hf + 4 * g);
+        const f32x4 kl = *reinterpret_cast<const f32x4*>(sBl[buf] + 32 * t + 16 * hf + 4 * g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[hf][i] = exp2_fast((toth - kh[i]) + (totl - kl[i]));
       }
-      Operand<T> cs[NT][SU];
+      f32x4 lo, hi;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        f32x4 lo, hi;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (sizeof(T) == 2) {
-            lo[i] = static_cast<float>(c[t][nt].v[i]) * e[0][i];
-            hi[i] = static_cast<float>(c[t][nt].v[4 + i]) * e[1][i];
-          } else {
-            lo[i] = c[t][nt].v[0][i] * e[0][i];
-            hi[i] = c[t][nt].v[1][i] * e[1][i];
-          }
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2) {
+          lo[i] = static_cast<float>(c[t].v[i]) * e[0][i];
+          hi[i] = static_cast<float>(c[t].v[4 + i]) * e[1][i];
+        } else {
+          lo[i] = c[t].v[0][i] * e[0][i];
+          hi[i] = c[t].v[1][i] * e[1][i];
         }
-        split<SU>(cs[nt], lo, hi);
       }
+      Operand<T> cs[SU];
+      split<SU>(cs, lo, hi);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const Operand<T> bo = LD::down(sB, kStride, t, g, r, LD::tile_col(mt, r));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int s = SU - 1; s >= 0; --s) S[mt][nt] = mma(bo, cs[nt][s], S[mt][nt]);
+        for (int s = SU - 1; s >= 0; --s) S[mt] = mma(bo, cs[s], S[mt]);
       }
     }
+    if (have) sum_decays(buf ^ 1);
   }
 
   float* dst = nullptr;
   float f = 1.0f;
   int64_t dm = p.N, dn = 1;
-  if (STATE) {
+  if (!OUT) {
     dst = p.sum + (bh * p.spans + span) * p.M * p.N;
     if (tid == 0 && tile == 0) p.total[bh * p.spans + span] = exp2_fast(float(all));
   } else if (span == p.spans - 1 && p.s_last) {
@@ -644,19 +685,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && MP <= 128 ? 2 : 1) void k_mi
     dm = p.sm;
     dn = p.sn;
     // going backward, the first token's own decay stands between G_0 and h0
-    if (p.reverse && live > 0) f = exp2_fast(log_decay(p.g, b, 0, h) * kLog2e);
+    if (REV && live > 0) f = exp2_fast(log_decay(p.g, b, 0, h) * kLog2e);
   }
   if (dst) {
+    int g2 = g;   // kept apart from the loads above: their conditions would be held through the loop
+    asm volatile("" : "+v"(g2));
+    const int n = nw + r;
+    float* col = dst + n * dn;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int n = nw + LD::template n_of<NT>(nt, r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = 16 * mt + 4 * g + i;
-          if (m < p.M && n < p.N) dst[m * dm + n * dn] = S[mt][nt][i] * f;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int m = LD::m_of(mt, g2, i);
+        if (m < p.M && n < p.N) col[m * dm] = S[mt][i] * f;
       }
   }
 }
@@ -679,7 +720,7 @@ static __global__ __launch_bounds__(256) void k_join_spans(JoinParams p) {
   float* s = p.sum + bh * p.spans * p.inner + e;
   const float* tot = p.total + bh * p.spans;
   float run = p.s0 ? p.s0[bh * p.inner + e / p.N * p.sm + e % p.N * p.sn] : 0.0f;
-  constexpr int U = 8;
+  constexpr int U = 32;
   float v[U];
   for (int k = 0; k < p.spans; k += U) {
 #pragma unroll
@@ -695,8 +736,8 @@ static __global__ __launch_bounds__(256) void k_join_spans(JoinParams p) {
 }
 
 struct DecayGradParams {
-  const float* u;        // (uslices, B, H, L)
-  const float* w;        // (wslices, B, H, L)
+  const float* u;        // (slices, B, H, L)
+  const float* w;        // (slices, B, H, L)
   const float* carry;    // (B, H, spans, inner): states entering the spans (dq's layout)
   const float* rcarry;   // same of their gradients, spans counted from the end
   const float* s_last;   // (B, H, dk, dv), with dh_last; null: no flow through the end
@@ -705,8 +746,26 @@ struct DecayGradParams {
   const int32_t* lengths;
   void* dg;              // (B, L, H)
   int64_t B, L, H, inner, span;
-  int32_t uslices, wslices, spans, bf16;
+  int32_t slices, spans, bf16;
 };
+
+// A thread's share of a dot product, eight loads of each at a time.
+__device__ __forceinline__ double partial_dot(const float* a, const float* b, int64_t n) {
+  constexpr int U = 8;
+  double sum = 0.0;
+  for (int64_t base = threadIdx.x; base < n; base += 256 * U) {
+    float x[U], y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = base + 256 * u;
+      x[u] = i < n ? a[i] : 0.0f;
+      y[u] = i < n ? b[i] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) sum += double(x[u]) * y[u];
+  }
+  return sum;
+}
 
 // dg over one span: the flow through its end, then suffix sums of u - w within
 // it.  A workgroup per span; sums in 64 bits.
@@ -722,12 +781,11 @@ static __global__ __launch_bounds__(256) void k_decay_grad(DecayGradParams p) {
   if (span + 1 < p.spans) {
     const float* s = p.carry + (bh * p.spans + span + 1) * p.inner;
     const float* q = p.rcarry + (bh * p.spans + (p.spans - 1 - span)) * p.inner;
-    for (int64_t i = tid; i < p.inner; i += 256) flow += double(s[i]) * q[i];
+    flow = partial_dot(s, q, p.inner);
     const int64_t e = t_begin + p.span;   // the decay between the two
     if (e < live) flow *= exp2_fast(log_decay(p.g, b, e, h) * kLog2e);
   } else if (p.s_last) {
-    for (int64_t i = tid; i < p.inner; i += 256)
-      flow += double(p.s_last[bh * p.inner + i]) * p.dh_last[bh * p.inner + i];
+    flow = partial_dot(p.s_last + bh * p.inner, p.dh_last + bh * p.inner, p.inner);
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) flow += __shfl_xor(flow, d);
@@ -740,8 +798,16 @@ static __global__ __launch_bounds__(256) void k_decay_grad(DecayGradParams p) {
     double v = 0.0;
     if (t < t_end && t < live) {
       const int64_t i = bh * p.L + t;
-      for (int k = 0; k < p.uslices; ++k) v += p.u[k * n + i];
-      for (int k = 0; k < p.wslices; ++k) v -= p.w[k * n + i];
+      for (int k = 0; k < p.slices; k += 4) {   // a multiple of 4
+        float x[4], y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] = p.u[(k + j) * n + i];
+          y[j] = p.w[(k + j) * n + i];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v += double(x[j]) - double(y[j]);
+      }
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
