@@ -14,6 +14,8 @@ using namespace ssmh;
 using namespace ssma;
 
 constexpr int64_t kMaxDim = 256;
+// A launch holds at most 2^32 - 1 lanes; workgroups have up to 512.
+constexpr int64_t kMaxGroups = int64_t(UINT32_MAX) / 512;
 constexpr int64_t kSpanAlign = 64;
 
 // Sizes common to the three calls; `tokens` is batch * seqlen.
@@ -218,11 +220,12 @@ BwdPlan make_bwd_plan(const Sizes& z, int32_t span) {
   return pl;
 }
 
-// Launches of a plan stay within one grid.
+// Launches of a plan stay within one grid: workgroups of 512 lanes, two for a
+// head's span at most, and with spans to join a lane for an element of a state.
 ssm_status_t check_grid(const Sizes& z, const Cut& c) {
   int64_t n, m;
-  if (!mul_ok(z.B * z.H * 4, c.spans, &n) || n > kMaxGrid || !mul_ok(z.B * z.H, 256, &m) || m > kMaxGrid ||
-      !mul_ok(z.state, c.spans, &m) || m > INT64_MAX / 16)
+  if (!mul_ok(z.B * z.H * 4, c.spans, &n) || n > kMaxGroups || !mul_ok(z.state, c.spans, &m) ||
+      m > INT64_MAX / 16 || (c.spans > 1 && z.B * z.H * round_up(z.dk * z.dv, 256) > int64_t(UINT32_MAX)))
     return fail(SSM_ERR_SHAPE, "problem too large for one launch");
   return SSM_OK;
 }
@@ -276,7 +279,6 @@ ssm_status_t check_bwd(const ssm_decay_attn_bwd_args_t* a, Sizes* z, BwdPlan* pl
   if (a->reserved != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved field must be 0");
   *pl = make_bwd_plan(*z, a->span);
   if (ssm_status_t st = check_grid(*z, pl->cut)) return st;
-  if (z->tokens * z->Hk * z->dk / 256 >= kMaxGrid) return fail(SSM_ERR_SHAPE, "problem too large for one launch");
   if (z->B * z->H == 0) return SSM_OK;
   if (z->L > 0 && (!a->q || !a->k || !a->v || !a->log_decay || !a->dout || !a->dq || !a->dk ||
                    !a->dv || !a->dlog_decay))
@@ -382,7 +384,8 @@ ssm_status_t run_carries(MixParams p, float* carry, float* total, hipStream_t s)
 
 ssm_status_t copy_state(float* dst, const float* src, int64_t n, hipStream_t s) {
   if (!dst || n == 0) return SSM_OK;
-  hipLaunchKernelGGL(k_attn_state_copy, dim3(uint32_t((n + 255) / 256)), dim3(256), 0, s, dst, src, n);
+  const uint32_t groups = uint32_t(std::min<int64_t>((n + 255) / 256, 1 << 20));
+  hipLaunchKernelGGL(k_attn_state_copy, dim3(groups), dim3(256), 0, s, dst, src, n);
   return launch_status("k_attn_state_copy");
 }
 
@@ -495,10 +498,15 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
     if (ssm_status_t st = run_mix<T, 2, float, kOutDots, false>(dq, s)) return st;
     if (ssm_status_t st = run_mix<T, 2, float, kOutDots, true>(dk, s)) return st;
     const int64_t n = z.tokens * z.Hk * z.dk;
-    const dim3 grid(uint32_t((n + 255) / 256));
+    const bool four = z.dk % 4 == 0;
+    const dim3 grid(uint32_t(std::min<int64_t>((n / (four ? 4 : 1) + 255) / 256, 1 << 20)));
     for (int i = 0; i < 2; ++i) {
-      hipLaunchKernelGGL((k_sum_heads<T>), grid, dim3(256), 0, s, static_cast<T*>(i ? a->dk : a->dq),
-                         static_cast<const float*>(i ? dk.out : dq.out), n, int32_t(z.dk), int32_t(per));
+      T* out = static_cast<T*>(i ? a->dk : a->dq);
+      const float* in = static_cast<const float*>(i ? dk.out : dq.out);
+      if (four)
+        hipLaunchKernelGGL((k_sum_heads<T, 4>), grid, dim3(256), 0, s, out, in, n, int32_t(z.dk), int32_t(per));
+      else
+        hipLaunchKernelGGL((k_sum_heads<T, 1>), grid, dim3(256), 0, s, out, in, n, int32_t(z.dk), int32_t(per));
       if (ssm_status_t st = launch_status("k_sum_heads")) return st;
     }
   } else {
@@ -525,6 +533,25 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   gp.bf16 = a->decay_dtype == SSM_BF16;
   hipLaunchKernelGGL(k_decay_grad, dim3(uint32_t(z.B * z.H * gp.spans)), dim3(256), 0, s, gp);
   return launch_status("k_decay_grad");
+}
+
+template <typename T, int V, int LC>
+ssm_status_t launch_step(AttnStepParams p, hipStream_t s) {
+  p.tiles = (p.dv + LC * V - 1) / (LC * V);
+  const int64_t groups = p.B * p.H * p.tiles;
+  if (groups > kMaxGroups) return fail(SSM_ERR_SHAPE, "problem too large for one launch");
+  hipLaunchKernelGGL((k_attn_step<T, V, LC>), dim3(uint32_t(groups)), dim3(256), 0, s, p);
+  return launch_status("k_attn_step");
+}
+
+template <typename T>
+ssm_status_t run_step(const AttnStepParams& p, hipStream_t s) {
+  if (p.dv % 4 == 0 && !misaligned(p.h, 16)) {
+    if (p.dv <= 16) return launch_step<T, 4, 4>(p, s);
+    if (p.dv <= 32) return launch_step<T, 4, 8>(p, s);
+    return launch_step<T, 4, 16>(p, s);
+  }
+  return p.dv <= 16 ? launch_step<T, 1, 16>(p, s) : launch_step<T, 1, 64>(p, s);
 }
 
 }  // namespace
@@ -581,12 +608,7 @@ ssm_status_t ssm_decay_attn_step(const ssm_decay_attn_step_args_t* a, void* hip_
   p.dk = int32_t(z.dk);
   p.dv = int32_t(z.dv);
   p.g_bf16 = a->decay_dtype == SSM_BF16;
-  const dim3 grid(uint32_t(z.B * z.H), uint32_t((z.dv + kWave - 1) / kWave));
-  if (a->dtype == SSM_F32)
-    hipLaunchKernelGGL((k_attn_step_simple<float>), grid, dim3(kWave), 0, s, p);
-  else
-    hipLaunchKernelGGL((k_attn_step_simple<bf16_t>), grid, dim3(kWave), 0, s, p);
-  return launch_status("k_attn_step_simple");
+  return a->dtype == SSM_F32 ? run_step<float>(p, s) : run_step<bf16_t>(p, s);
 }
 
 ssm_status_t ssm_decay_attn_bwd(const ssm_decay_attn_bwd_args_t* a, void* hip_stream) {

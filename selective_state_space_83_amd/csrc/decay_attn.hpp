@@ -831,15 +831,28 @@ static __global__ __launch_bounds__(256) void k_decay_grad(DecayGradParams p) {
   }
 }
 
-// Sum over the value heads of a key head: (rows, heads, n) fp32 to (rows, key heads, n).
-template <typename T>
-__global__ void k_sum_heads(T* out, const float* in, int64_t total, int32_t n, int32_t per) {
-  const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= total) return;
-  const int64_t row = i / n, c = i % n;   // row: (batch, token, key head)
-  float acc = 0.0f;
-  for (int k = 0; k < per; ++k) acc += in[(row * per + k) * n + c];
-  st(out + i, acc);
+// Sum over the value heads of a key head: (rows, heads, n) fp32 to (rows, key
+// heads, n), in the heads' order.  V = 4 where n is a multiple of it.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_sum_heads(T* out, const float* in, int64_t total, int32_t n, int32_t per) {
+  typedef float fvec __attribute__((ext_vector_type(V)));
+  const int64_t step = int64_t(gridDim.x) * 256;
+  for (int64_t j = int64_t(blockIdx.x) * 256 + threadIdx.x; j * V < total; j += step) {
+    const int64_t i = j * V, row = i / n, c = i % n;   // row: (batch, token, key head)
+    const float* p = in + row * per * n + c;
+    fvec acc = fvec(0.0f);
+    int k = 0;
+    for (; k + 4 <= per; k += 4) {
+      fvec a[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) a[u] = *reinterpret_cast<const fvec*>(p + (k + u) * int64_t(n));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) acc += a[u];
+    }
+    for (; k < per; ++k) acc += *reinterpret_cast<const fvec*>(p + k * int64_t(n));
+#pragma unroll
+    for (int u = 0; u < V; ++u) st(out + i + u, acc[u]);
+  }
 }
 
 struct AttnStepParams {
@@ -851,32 +864,79 @@ struct AttnStepParams {
   float* h;
   void* o;
   int64_t B, H;
-  int32_t per, dk, dv, g_bf16;
+  int32_t per, dk, dv, g_bf16, tiles;
 };
 
-template <typename T>
-__global__ __launch_bounds__(kWave) void k_attn_step_simple(AttnStepParams p) {
-  const int64_t bh = blockIdx.x, b = bh / p.H, h = bh % p.H;
-  const int n = blockIdx.y * kWave + threadIdx.x;
-  if (n >= p.dv) return;
-  const T* q = static_cast<const T*>(p.q) + b * p.qs[0] + h / p.per * p.qs[1];
-  const T* k = static_cast<const T*>(p.k) + b * p.ks[0] + h / p.per * p.ks[1];
-  const float v = ld(static_cast<const T*>(p.v) + b * p.vs[0] + h * p.vs[1] + n);
-  const Decay d{p.g, p.gs[0], 0, p.gs[1], p.g_bf16};
-  const float e = expf(log_decay(d, b, 0, h));
-  float* S = p.h + bh * p.dk * p.dv + n;
-  float acc = 0.0f;
-  for (int m = 0; m < p.dk; ++m) {
-    const float s = S[int64_t(m) * p.dv] * e + ld(k + m) * v;
-    S[int64_t(m) * p.dv] = s;
-    acc += s * ld(q + m);
+// One token: the state streams through once.  A workgroup of 256 takes LC V
+// columns of one head's state (V = 4 side by side where rows are on 16 bytes),
+// its LC lanes a row at a time, 256 / LC rows at once; a lane has eight reads in
+// flight before it needs the first.  The state's lines are used once a step:
+// reads and writes pass the caches by.  o joins the rows over lanes, then waves.
+template <typename T, int V, int LC>
+__global__ __launch_bounds__(256) void k_attn_step(AttnStepParams p) {
+  typedef float fvec __attribute__((ext_vector_type(V)));
+  constexpr int RG = 256 / LC, U = 8;
+  __shared__ float sk[256], sq[256];
+  __shared__ float so[4][LC * V];
+  const int tid = threadIdx.x, lc = tid % LC, rg = tid / LC;
+  const uint32_t id = blockIdx.x / uint32_t(p.tiles), bh = id;
+  const int n = int(blockIdx.x % uint32_t(p.tiles)) * LC * V + lc * V;
+  const int64_t b = bh / uint32_t(p.H), h = bh % uint32_t(p.H), hk = int64_t(uint32_t(h) / uint32_t(p.per));
+  const bool on = n < p.dv;
+  float* S = p.h + int64_t(bh) * p.dk * p.dv + n;
+  fvec s[U];
+  auto load = [&](int m0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int m = m0 + u * RG + rg;
+      s[u] = fvec(0.0f);
+      if (on && m < p.dk) s[u] = __builtin_nontemporal_load(reinterpret_cast<const fvec*>(S + int64_t(m) * p.dv));
+    }
+  };
+  load(0);
+  const T* q = static_cast<const T*>(p.q) + b * p.qs[0] + hk * p.qs[1];
+  const T* k = static_cast<const T*>(p.k) + b * p.ks[0] + hk * p.ks[1];
+  const T* v = static_cast<const T*>(p.v) + b * p.vs[0] + h * p.vs[1];
+  if (tid < p.dk) {
+    sk[tid] = ld(k + tid);
+    sq[tid] = ld(q + tid);
   }
-  st(static_cast<T*>(p.o) + bh * p.dv + n, acc);
+  fvec vv = fvec(0.0f);
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) vv[i] = ld(v + n + i);
+  }
+  const Decay d{p.g, p.gs[0], 0, p.gs[1], p.g_bf16};
+  const float e = exp2_fast(log_decay(d, b, 0, h) * kLog2e);
+  __syncthreads();
+  fvec acc = fvec(0.0f);
+  for (int m0 = 0; m0 < p.dk; m0 += RG * U) {
+    if (m0 > 0) load(m0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int m = m0 + u * RG + rg;
+      if (m < p.dk) {
+        s[u] = s[u] * e + sk[m] * vv;
+        acc += s[u] * sq[m];
+        if (on) __builtin_nontemporal_store(s[u], reinterpret_cast<fvec*>(S + int64_t(m) * p.dv));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int w = LC; w < 64; w <<= 1) acc[i] += __shfl_xor(acc[i], w);
+    if ((tid & 63) < LC) so[tid >> 6][lc * V + i] = acc[i];
+  }
+  __syncthreads();
+  const int c = int(blockIdx.x % uint32_t(p.tiles)) * LC * V + tid;
+  if (tid < LC * V && c < p.dv)
+    st(static_cast<T*>(p.o) + int64_t(bh) * p.dv + c, (so[0][tid] + so[1][tid]) + (so[2][tid] + so[3][tid]));
 }
 
 static __global__ void k_attn_state_copy(float* dst, const float* src, int64_t n) {
-  const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i < n) dst[i] = src ? src[i] : 0.0f;
+  const int64_t step = int64_t(gridDim.x) * blockDim.x;
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) dst[i] = src ? src[i] : 0.0f;
 }
 
 }  // namespace ssma
