@@ -26,7 +26,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import (SSM_BF16, SSM_F32, _on_stream, _raise_for, _stream_handle, _torch, load_library)
+from . import SSM_BF16, SSM_F32, _on_stream, _raise_for, _torch, load_library
 
 SSM_NORM_PLAIN = 0
 SSM_NORM_SILU = 1
@@ -115,51 +115,55 @@ def declare(lib) -> None:
 
 
 # ---------------------------------------------------------------------------
-# checks
+# checks (on the path of single-token calls, where the host's time is the
+# call's: one test in the common case, the reason worked out only on failure)
 # ---------------------------------------------------------------------------
 
 def _code(t, name):
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return SSM_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return SSM_F32
     raise ValueError("unsupported dtype %s of %s (float32 or bfloat16)" % (t.dtype, name))
 
 
-def _placed(t, name, dev):
-    """The address of a tensor on the current device ``dev`` (an index)."""
+def _current(stream):
+    """The current device's index and the handle of the stream to launch on."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    return dev, torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+
+
+def _refuse(t, name, shape, dtype, dev):
+    if t.shape != shape:
+        raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype is not dtype:
+        raise ValueError("%s must have dtype %s" % (name, dtype))
     if not t.is_cuda:
         raise ValueError("%s must be on the GPU" % name)
-    if t.get_device() != dev:
-        raise ValueError("%s is on cuda:%d but the current device is cuda:%d"
-                         % (name, t.get_device(), dev))
-    return t.data_ptr()
+    raise ValueError("%s is on cuda:%d but the current device is cuda:%d" % (name, t.get_device(), dev))
 
 
 def _rows(t, name, shape, dtype, dev):
     """Address and outer strides of an input whose last dimension is contiguous."""
-    if t.shape != shape:
-        raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.dtype != dtype:
-        raise ValueError("%s must have dtype %s" % (name, dtype))
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, shape, dtype, dev)
     s = t.stride()
     if s[-1] != 1 and shape[-1] > 1:
         raise ValueError("the last dimension of %s must be contiguous" % name)
-    return _placed(t, name, dev), s[:-1]
+    return t.data_ptr(), s[:-1]
 
 
 def _dense(t, name, shape, dtype, dev):
     """Address of a contiguous tensor, or None."""
     if t is None:
         return None
-    if t.shape != shape:
-        raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.dtype != dtype:
-        raise ValueError("%s must have dtype %s" % (name, dtype))
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return _placed(t, name, dev)
+    return t.data_ptr()
 
 
 def _workspace(args, need, workspace, like, dev):
@@ -169,36 +173,33 @@ def _workspace(args, need, workspace, like, dev):
         return None
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    args.workspace = _placed(workspace, "workspace", dev)
+    args.workspace = _dense(workspace, "workspace", workspace.shape, torch.uint8, dev)
     args.workspace_bytes = workspace.numel()
     return workspace
 
 
 def _attn_inputs(a, q, k, v, log_decay, step, dev):
-    """Fills sizes, dtypes, inputs and strides; returns the outer shape."""
+    """Fills sizes, dtypes, inputs and strides; returns the shapes of v and of the
+    state."""
+    vs, qs = v.shape, q.shape
     rank = 3 if step else 4
-    if q.dim() != rank or v.dim() != rank:
+    if len(vs) != rank or len(qs) != rank:
         raise ValueError("q and v must have %d dimensions" % rank)
-    outer = v.shape[:-1]
-    key_shape = v.shape[:-2] + q.shape[-2:]
-    a.batch, a.heads, a.key_heads = v.shape[0], v.shape[-2], q.shape[-2]
-    a.key_dim, a.value_dim = q.shape[-1], v.shape[-1]
+    dt, outer = q.dtype, vs[:-1]
+    key_shape = vs[:-2] + qs[-2:]
+    a.batch, a.heads, a.value_dim = vs[0], vs[-2], vs[-1]
+    a.key_heads, a.key_dim = qs[-2], qs[-1]
     if not step:
-        a.seqlen = v.shape[1]
+        a.seqlen = vs[1]
     a.dtype, a.decay_dtype = _code(q, "q"), _code(log_decay, "log_decay")
-    a.q, s = _rows(q, "q", key_shape, q.dtype, dev)
-    a.q_stride[:] = s
-    a.k, s = _rows(k, "k", key_shape, q.dtype, dev)
-    a.k_stride[:] = s
-    a.v, s = _rows(v, "v", v.shape, q.dtype, dev)
-    a.v_stride[:] = s
-    if log_decay.shape != outer:
-        raise ValueError("log_decay must be %s, not %s" % (tuple(outer), tuple(log_decay.shape)))
-    a.log_decay = _placed(log_decay, "log_decay", dev)
+    a.q, a.q_stride[:] = _rows(q, "q", key_shape, dt, dev)
+    a.k, a.k_stride[:] = _rows(k, "k", key_shape, dt, dev)
+    a.v, a.v_stride[:] = _rows(v, "v", vs, dt, dev)
+    if log_decay.shape != outer or log_decay.get_device() != dev:
+        _refuse(log_decay, "log_decay", outer, log_decay.dtype, dev)
+    a.log_decay = log_decay.data_ptr()
     a.decay_stride[:] = log_decay.stride()
-    return outer
+    return vs, (vs[0], vs[-2], qs[-1], vs[-1])
 
 
 # ---------------------------------------------------------------------------
@@ -213,23 +214,23 @@ def decay_attn(q, k, v, log_decay, h0=None, lengths=None, want_h_last=True, o=No
     span of the time axis (0: the library's plan)."""
     torch = _torch()
     lib = load_library()
-    dev = torch.cuda.current_device()
+    dev, handle = _current(stream)
+    f32 = torch.float32
     with _on_stream(stream):
         a = DecayAttnArgs()
-        _attn_inputs(a, q, k, v, log_decay, False, dev)
-        state = (v.shape[0], v.shape[2], q.shape[3], v.shape[3])
+        shape, state = _attn_inputs(a, q, k, v, log_decay, False, dev)
         if o is None:
-            o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            o = v.new_empty(shape)
         if h_last is None and want_h_last:
-            h_last = torch.empty(state, dtype=torch.float32, device=v.device)
-        a.o = _dense(o, "o", v.shape, v.dtype, dev)
-        a.h0 = _dense(h0, "h0", state, torch.float32, dev)
-        a.h_last = _dense(h_last, "h_last", state, torch.float32, dev)
-        a.lengths = _dense(lengths, "lengths", (v.shape[0],), torch.int32, dev)
+            h_last = v.new_empty(state, dtype=f32)
+        a.o = _dense(o, "o", shape, v.dtype, dev)
+        a.h0 = _dense(h0, "h0", state, f32, dev)
+        a.h_last = _dense(h_last, "h_last", state, f32, dev)
+        a.lengths = _dense(lengths, "lengths", shape[:1], torch.int32, dev)
         a.span = int(span)
         need = lib.ssm_decay_attn_workspace_size(ctypes.byref(a))
         workspace = _workspace(a, need, workspace, v, dev)
-        status = lib.ssm_decay_attn_fwd(ctypes.byref(a), _stream_handle(stream))
+        status = lib.ssm_decay_attn_fwd(ctypes.byref(a), handle)
     _raise_for(lib, status)
     return o, h_last
 
@@ -238,17 +239,16 @@ def decay_attn_step(h, q, k, v, log_decay, o=None, stream=None):
     """One token per sequence: h (float32, (batch, heads, key_dim, value_dim))
     is updated in place; q, k (batch, key_heads, key_dim), v (batch, heads,
     value_dim), log_decay (batch, heads).  Returns o (batch, heads, value_dim)."""
-    torch = _torch()
     lib = load_library()
-    dev = torch.cuda.current_device()
+    dev, handle = _current(stream)
     with _on_stream(stream):
         a = DecayAttnStepArgs()
-        _attn_inputs(a, q, k, v, log_decay, True, dev)
+        shape, state = _attn_inputs(a, q, k, v, log_decay, True, dev)
         if o is None:
-            o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-        a.h = _dense(h, "h", (v.shape[0], v.shape[1], q.shape[2], v.shape[2]), torch.float32, dev)
-        a.o = _dense(o, "o", v.shape, v.dtype, dev)
-        status = lib.ssm_decay_attn_step(ctypes.byref(a), _stream_handle(stream))
+            o = v.new_empty(shape)
+        a.h = _dense(h, "h", state, _torch().float32, dev)
+        a.o = _dense(o, "o", shape, v.dtype, dev)
+        status = lib.ssm_decay_attn_step(ctypes.byref(a), handle)
     _raise_for(lib, status)
     return o
 
@@ -261,27 +261,24 @@ def decay_attn_bwd(q, k, v, log_decay, dout, h0=None, dh_last=None, lengths=None
     shape: sum it over the dimensions that a broadcast input repeats."""
     torch = _torch()
     lib = load_library()
-    dev = torch.cuda.current_device()
+    dev, handle = _current(stream)
     with _on_stream(stream):
         a = DecayAttnBwdArgs()
-        outer = _attn_inputs(a, q, k, v, log_decay, False, dev)
-        a.dout, s = _rows(dout, "dout", v.shape, v.dtype, dev)
-        a.dout_stride[:] = s
-        state = (v.shape[0], v.shape[2], q.shape[3], v.shape[3])
-        empty = lambda shape, dt: torch.empty(shape, dtype=dt, device=v.device)  # noqa: E731
-        g = {"dq": empty(q.shape, q.dtype), "dk": empty(q.shape, q.dtype),
-             "dv": empty(v.shape, v.dtype), "dlog_decay": empty(outer, log_decay.dtype)}
+        shape, state = _attn_inputs(a, q, k, v, log_decay, False, dev)
+        a.dout, a.dout_stride[:] = _rows(dout, "dout", shape, v.dtype, dev)
+        g = {"dq": q.new_empty(q.shape), "dk": q.new_empty(q.shape), "dv": v.new_empty(shape),
+             "dlog_decay": log_decay.new_empty(log_decay.shape)}
         if want_dh0:
-            g["dh0"] = empty(state, torch.float32)
+            g["dh0"] = v.new_empty(state, dtype=torch.float32)
         for name, t in g.items():
             setattr(a, name, t.data_ptr())
         a.h0 = _dense(h0, "h0", state, torch.float32, dev)
         a.dh_last = _dense(dh_last, "dh_last", state, torch.float32, dev)
-        a.lengths = _dense(lengths, "lengths", (v.shape[0],), torch.int32, dev)
+        a.lengths = _dense(lengths, "lengths", shape[:1], torch.int32, dev)
         a.span = int(span)
         need = lib.ssm_decay_attn_bwd_workspace_size(ctypes.byref(a))
         workspace = _workspace(a, need, workspace, v, dev)
-        status = lib.ssm_decay_attn_bwd(ctypes.byref(a), _stream_handle(stream))
+        status = lib.ssm_decay_attn_bwd(ctypes.byref(a), handle)
     _raise_for(lib, status)
     return g
 
@@ -293,13 +290,14 @@ def decay_attn_bwd(q, k, v, log_decay, dout, h0=None, dh_last=None, lengths=None
 def _norm_rows(t, name, like, dev):
     """Address and row stride of a (..., channels) tensor whose rows are evenly
     spaced."""
-    if t.shape != like.shape:
-        raise ValueError("%s must have the shape of x" % name)
-    if t.dtype != like.dtype:
-        raise ValueError("%s must have the dtype of x" % name)
-    shape, s = t.shape, t.stride()
+    shape = like.shape
+    if t.shape != shape or t.dtype is not like.dtype or t.get_device() != dev:
+        _refuse(t, name, shape, like.dtype, dev)
+    s = t.stride()
     if s[-1] != 1 and shape[-1] > 1:
         raise ValueError("the channels of %s must be contiguous" % name)
+    if len(shape) == 2:
+        return t.data_ptr(), s[0] if shape[0] > 1 else shape[1]
     row, span = None, 0
     for n, st in zip(reversed(shape[:-1]), reversed(s[:-1])):
         if n == 1:
@@ -309,11 +307,10 @@ def _norm_rows(t, name, like, dev):
         elif st != span:
             raise ValueError("the rows of %s must be evenly spaced" % name)
         span = st * n
-    return _placed(t, name, dev), shape[-1] if row is None else row
+    return t.data_ptr(), shape[-1] if row is None else row
 
 
 def _norm_args(a, x, groups, weight, bias, z, act, gate_first, rms, eps, dev):
-    torch = _torch()
     if x.dim() < 1:
         raise ValueError("x must be (..., channels)")
     if act not in (None, "silu"):
@@ -332,8 +329,9 @@ def _norm_args(a, x, groups, weight, bias, z, act, gate_first, rms, eps, dev):
     a.x, a.x_stride = _norm_rows(x, "x", x, dev)
     if z is not None:
         a.z, a.z_stride = _norm_rows(z, "z", x, dev)
-    a.weight = _dense(weight, "weight", (C,), torch.float32, dev)
-    a.bias = _dense(bias, "bias", (C,), torch.float32, dev)
+    f32 = _torch().float32
+    a.weight = _dense(weight, "weight", (C,), f32, dev)
+    a.bias = _dense(bias, "bias", (C,), f32, dev)
 
 
 def group_norm(x, groups, weight=None, bias=None, z=None, act=None, gate_first=False, rms=False,
@@ -341,16 +339,15 @@ def group_norm(x, groups, weight=None, bias=None, z=None, act=None, gate_first=F
     """Group norm over the channels of each token of x (..., channels), then
     silu (``act="silu"``) or the gate silu(z); with ``gate_first`` x silu(z) is
     normalized instead.  weight and bias are float32 (channels,) or None."""
-    torch = _torch()
     lib = load_library()
-    dev = torch.cuda.current_device()
+    dev, handle = _current(stream)
     with _on_stream(stream):
         a = GroupNormArgs()
         _norm_args(a, x, groups, weight, bias, z, act, gate_first, rms, eps, dev)
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            y = x.new_empty(x.shape)
         a.y = _dense(y, "y", x.shape, x.dtype, dev)
-        status = lib.ssm_group_norm_fwd(ctypes.byref(a), _stream_handle(stream))
+        status = lib.ssm_group_norm_fwd(ctypes.byref(a), handle)
     _raise_for(lib, status)
     return y
 
@@ -363,21 +360,21 @@ def group_norm_bwd(x, dy, groups, weight=None, bias=None, z=None, act=None, gate
     (float32)."""
     torch = _torch()
     lib = load_library()
-    dev = torch.cuda.current_device()
+    dev, handle = _current(stream)
     with _on_stream(stream):
         a = GroupNormBwdArgs()
         _norm_args(a, x, groups, weight, bias, z, act, gate_first, rms, eps, dev)
         a.dy, a.dy_stride = _norm_rows(dy, "dy", x, dev)
-        g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device)}
+        g = {"dx": x.new_empty(x.shape)}
         if z is not None:
-            g["dz"] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            g["dz"] = x.new_empty(x.shape)
         for name, want in (("dweight", want_dweight), ("dbias", want_dbias)):
             if want:
-                g[name] = torch.empty(x.shape[-1:], dtype=torch.float32, device=x.device)
+                g[name] = x.new_empty(x.shape[-1:], dtype=torch.float32)
         for name, t in g.items():
             setattr(a, name, t.data_ptr())
         need = lib.ssm_group_norm_bwd_workspace_size(ctypes.byref(a))
         workspace = _workspace(a, need, workspace, x, dev)
-        status = lib.ssm_group_norm_bwd(ctypes.byref(a), _stream_handle(stream))
+        status = lib.ssm_group_norm_bwd(ctypes.byref(a), handle)
     _raise_for(lib, status)
     return g
