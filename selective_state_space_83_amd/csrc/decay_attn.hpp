@@ -190,8 +190,12 @@ struct Lds;
 template <>
 struct Lds<bf16_t> {
   static constexpr int kVec = 8;         // elements in 16 bytes
-  static constexpr int kPad = 24;        // 12 words: rows fall on different banks
-  static constexpr int kPadC = 8;
+#ifndef PADB
+#define PADB 24
+#define PADC 8
+#endif
+  static constexpr int kPad = PADB;        // 12 words: rows fall on different banks
+  static constexpr int kPadC = PADC;
   // block t of 32 columns of a row
   __device__ static __forceinline__ Operand<bf16_t> along(const bf16_t* row, int t, int g) {
     Operand<bf16_t> o;
@@ -393,7 +397,8 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
   __shared__ __align__(16) T sB[CT * kStride];
   __shared__ __align__(16) T sC[CT * kStrideC];
   __shared__ __align__(16) Operand<T> sP[OUT ? SP * kScores * kWave : 1];
-  __shared__ __align__(16) float sBh[2][CT], sBl[2][CT], sTot[2][2];
+  // of the chunk's running sums b: rounded and rest; exp(b), exp(b_CT - b), exp(b_CT)
+  __shared__ __align__(16) float sBh[2][CT], sBl[2][CT], sIn[2][CT], sEnd[2][CT], sAll[2];
   // where query tile q's scores with keys 32 t.. lie: 0 0 | 1 1 2 2 and on
   auto score_at = [](int s, int q, int t) { return (s * kScores + (q < 2 ? q : 2 * q - 2 + t)) * kWave; };
 
@@ -414,11 +419,13 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
   const int64_t ost = p.H * p.N;
   float* const dots = PART == kOutDots ? p.dots + ((int64_t(tile) * W + w) * p.B * p.H + bh) * p.L : nullptr;
 
-  // the lowest token of chunk k; backward, positions count from the end of the
-  // last span, so that spans and chunks have the same boundaries either way
+  // the lowest token of the chunk taken k-th; backward, positions count from the
+  // end of the last span, so that spans and chunks have the same boundaries
+  // either way.  The state pass takes a span's chunks from its end: what it read
+  // last is what the next pass reads first, and comes from the caches.
   const int chunks = int(p.span / CT);
   auto lowest = [&](int k) {
-    const int64_t pos = span * p.span + int64_t(k) * CT;
+    const int64_t pos = span * p.span + int64_t(OUT ? k : chunks - 1 - k) * CT;
     return REV ? p.span * p.spans - CT - pos : pos;
   };
 
@@ -441,31 +448,35 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
 
   Stage<T, CT, MP, 64 * W, FAST> qa, qb;
   Stage<T, CT, NW, 64 * W, FAST> qc;
-  uint32_t gl = 0;   // wave 0: the lane's log decay (all zeros: none)
   auto fetch = [&](int64_t low) {
-    if (w == 0) {
-      // backward, the decay stands behind the token
-      const int64_t t = low + (REV ? CT - lane : lane);
-      gl = 0;
-      if (lane < CT && t < live) gl = log_decay_bits(p.g, b, t, h);
-    }
     if constexpr (OUT) qa.load(pa, p.a.st, low, live, 0, p.M);
     qb.load(pb, p.b.st, low, live, 0, p.M);
     qc.load(pc, p.c.st, low, live, n0, p.N);
   };
-  double all = 0.0;   // wave 0: sum of the span's log decays (the state pass)
+  // The decays are the work of one wave, one that has few scores to form: read
+  // two chunks ahead and summed one ahead.
+  constexpr int DW = W == 8 ? 1 : 0;
+  uint32_t gl = 0;    // the lane's log decay (all zeros: none)
+  double all = 0.0;   // the state pass: sum of the log decays behind the chunk
+  auto fetch_decays = [&](int64_t low) {
+    // backward, the decay stands behind the token
+    const int64_t t = low + (REV ? CT - lane : lane);
+    gl = 0;
+    if (lane < CT && t < live) gl = log_decay_bits(p.g, b, t, h);
+  };
   auto sum_decays = [&](int buf) {
-    if (w != 0) return;
     const double bs = wave_running_sum(log_decay_of(p.g, gl) * kLog2e), tot = last_lane(bs);
-    const float hi = float(bs), toth = float(tot);
+    const float hi = float(bs);
     if (lane < CT) {
-      sBh[buf][lane] = hi;
-      sBl[buf][lane] = float(bs - hi);
+      if constexpr (OUT) {
+        sBh[buf][lane] = hi;
+        sBl[buf][lane] = float(bs - hi);
+        sIn[buf][lane] = exp2_fast(hi);
+      }
+      // to the chunk's end; in the state pass to the span's
+      sEnd[buf][lane] = exp2_fast(float(OUT ? tot - bs : all + (tot - bs)));
     }
-    if (lane == 0) {
-      sTot[buf][0] = toth;
-      sTot[buf][1] = float(tot - toth);
-    }
+    if (OUT && lane == 0) sAll[buf] = exp2_fast(float(tot));
     if (!OUT) all += tot;
   };
 
@@ -486,7 +497,11 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
     }
     if (!have) {
       fetch(low);
-      sum_decays(buf);
+      if (w == DW) {
+        fetch_decays(low);
+        sum_decays(buf);
+        if (k + 1 < chunks) fetch_decays(lowest(k + 1));
+      }
     }
     __syncthreads();
     if constexpr (OUT) qa.template store<REV>(sA, kStride);
@@ -494,7 +509,13 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
     qc.template store<REV>(sC, kStrideC);
     __syncthreads();
     have = k + 1 < chunks && lowest(k + 1) < live;
-    if (have) fetch(lowest(k + 1));
+    if (have) {
+      if (w == DW) {
+        sum_decays(buf ^ 1);
+        if (k + 2 < chunks) fetch_decays(lowest(k + 2));
+      }
+      fetch(lowest(k + 1));
+    }
     const int rows = live - low < CT ? int(live - low) : CT;       // of the chunk, with tokens
     const int orows = p.L - low < CT ? int(p.L - low) : CT;        // with a place in out
 
@@ -575,7 +596,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
         }
       }
 #pragma unroll
-      for (int q = 0; q < QT; ++q) acc[q] *= exp2_fast(sBh[buf][16 * q + r]);
+      for (int q = 0; q < QT; ++q) acc[q] *= sIn[buf][16 * q + r];
       __syncthreads();
     }
 
@@ -637,20 +658,15 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
     }
 
     // the state's update
-    const float toth = sTot[buf][0], totl = sTot[buf][1];
-    const float etot = exp2_fast(toth);
+    if constexpr (OUT) {
+      const float etot = sAll[buf];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) S[mt] *= etot;
+      for (int mt = 0; mt < MT; ++mt) S[mt] *= etot;
+    }
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      f32x4 e[2];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const f32x4 kh = *reinterpret_cast<const f32x4*>(sBh[buf] + 32 * t + 16 * hf + 4 * g);
-        const f32x4 kl = *reinterpret_cast<const f32x4*>(sBl[buf] + 32 * t + 16 * hf + 4 * g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e[hf][i] = exp2_fast((toth - kh[i]) + (totl - kl[i]));
-      }
+      const f32x4 e[2] = {*reinterpret_cast<const f32x4*>(sEnd[buf] + 32 * t + 4 * g),
+                          *reinterpret_cast<const f32x4*>(sEnd[buf] + 32 * t + 16 + 4 * g)};
       f32x4 lo, hi;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -671,7 +687,6 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
         for (int s = SU - 1; s >= 0; --s) S[mt] = mma(bo, cs[s], S[mt]);
       }
     }
-    if (have) sum_decays(buf ^ 1);
   }
 
   float* dst = nullptr;
@@ -679,7 +694,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
   int64_t dm = p.N, dn = 1;
   if (!OUT) {
     dst = p.sum + (bh * p.spans + span) * p.M * p.N;
-    if (tid == 0 && tile == 0) p.total[bh * p.spans + span] = exp2_fast(float(all));
+    if (w == DW && lane == 0 && tile == 0) p.total[bh * p.spans + span] = exp2_fast(float(all));
   } else if (span == p.spans - 1 && p.s_last) {
     dst = p.s_last + bh * p.M * p.N;
     dm = p.sm;
