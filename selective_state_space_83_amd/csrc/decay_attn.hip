@@ -133,12 +133,14 @@ int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // 64 bf16 / 64 x 64 fp32, us for one, two, three on a CU: 163, 278, - / 99, 139,
 // 219 / 201, 320, 424).  More than one span costs the first pass over all but
 // the last (`state`, its share of a step), two launches (two steps), and reading
-// and writing the spans' states five times (16 MB a step).  Measured, us by
+// and writing the spans' states five times (16 MB a step); the backward's three
+// passes share two such first passes and joins (a third and two thirds of a
+// pass's).  Measured, us by
 // number of spans: 80 walkers of 128 chunks, 128 x 128 bf16: 3 330, 6 293, 12
 // 307, 24 329; 4 walkers of 2048 chunks: 64 234, 128 213, 256 264; 320 walkers
 // of 32 chunks: 1 246, 3 315; 192 walkers of 32 chunks, 64 x 64 fp32: 1 182, 2
 // 216, 4 157, 8 171.
-Cut cut_time(int64_t L, int64_t walkers, int64_t inner, double state, int32_t span) {
+Cut cut_time(int64_t L, int64_t walkers, int64_t inner, double state, double join, int32_t span) {
   constexpr int64_t kCus = 256, kMaxSpans = 1024;
   Cut c;
   if (L == 0 || walkers == 0) return c;
@@ -155,7 +157,8 @@ Cut cut_time(int64_t L, int64_t walkers, int64_t inner, double state, int32_t sp
       if (n != want) continue;
       double cost = double(per + 1) * step(walkers * n);
       if (n > 1)
-        cost += state * double(per + 1) * step(walkers * (n - 1)) + 2.0 + double(n * walkers) * double(inner) / 0.8e6;
+        cost += state * double(per + 1) * step(walkers * (n - 1)) +
+                join * (2.0 + double(n * walkers) * double(inner) / 0.8e6);
       if (want == 1 || cost < least) {
         least = cost;
         best = per;
@@ -179,7 +182,7 @@ struct FwdPlan {
 
 FwdPlan make_fwd_plan(const Sizes& z, int32_t span) {
   FwdPlan pl;
-  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dv), z.dk * z.dv, 0.5, span);
+  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dv), z.dk * z.dv, 0.5, 1.0, span);
   if (pl.cut.spans > 1) {
     pl.off_total = align256(size_t(z.state) * size_t(pl.cut.spans) * 4);
     pl.total = pl.off_total + align256(size_t(z.B * z.H) * size_t(pl.cut.spans) * 4);
@@ -191,8 +194,7 @@ FwdPlan make_fwd_plan(const Sizes& z, int32_t span) {
 struct BwdPlan {
   Cut cut;
   int64_t slices = 0;   // column slices of key_dim whose dots are kept apart
-  size_t off_carry = 0, off_rcarry = 0, off_total = 0, off_s = 0, off_u = 0, off_w = 0, off_dq = 0, off_dk = 0,
-         total = 0;
+  size_t off_carry = 0, off_rcarry = 0, off_total = 0, off_s = 0, off_u = 0, off_w = 0, off_heads = 0, total = 0;
 };
 
 BwdPlan make_bwd_plan(const Sizes& z, int32_t span) {
@@ -204,18 +206,19 @@ BwdPlan make_bwd_plan(const Sizes& z, int32_t span) {
     off += align256(bytes);
     return o;
   };
-  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dk), z.dk * z.dv, 0.25, span);
+  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dk), z.dk * z.dv, 1.0 / 3, 2.0 / 3, span);
   pl.slices = tile_width(z.dk) / 16 * tiles_of(z.dk);
-  const size_t th = size_t(z.tokens) * size_t(z.H), spans = pl.cut.spans > 1 ? size_t(pl.cut.spans) : 0;
+  const size_t th = size_t(z.tokens) * size_t(z.H);
+  const size_t dots = size_t(z.B * z.H) * size_t(pl.cut.span * pl.cut.spans) * size_t(pl.slices) * 4;
+  const size_t spans = pl.cut.spans > 1 ? size_t(pl.cut.spans) : 0;
   pl.off_carry = take(size_t(z.state) * spans * 4);
   pl.off_rcarry = take(size_t(z.state) * spans * 4);
   pl.off_total = take(size_t(z.B * z.H) * spans * 4);
   pl.off_s = take(size_t(z.state) * 4);
-  pl.off_u = take(th * size_t(pl.slices) * 4);
-  pl.off_w = take(th * size_t(pl.slices) * 4);
+  pl.off_u = take(dots);
+  pl.off_w = take(dots);
   const bool shared = z.H != z.Hk;
-  pl.off_dq = take(shared ? th * size_t(z.dk) * 4 : 0);
-  pl.off_dk = take(shared ? th * size_t(z.dk) * 4 : 0);
+  pl.off_heads = take(shared ? th * size_t(z.dk) * 4 : 0);
   pl.total = off;
   return pl;
 }
@@ -376,9 +379,14 @@ ssm_status_t run_carries(MixParams p, float* carry, float* total, hipStream_t s)
   p.out = nullptr;
   p.s_last = nullptr;
   if (ssm_status_t st = run_mix<T, 1, T, kState, REV>(p, s)) return st;
-  JoinParams j{carry, total, p.s0, p.sm, p.sn, int64_t(p.M) * p.N, p.N, p.spans};
-  const int64_t blocks = p.B * p.H * ((j.inner + 255) / 256);
-  hipLaunchKernelGGL(k_join_spans, dim3(uint32_t(blocks)), dim3(256), 0, s, j);
+  const JoinParams j{carry, total, p.s0, p.sm, p.sn, p.M * p.N, p.N, p.spans};
+  // four elements to a lane where that leaves enough lanes; few heads with many
+  // spans want the lanes
+  const int64_t heads = p.B * p.H;
+  if (j.inner % 4 == 0 && heads * j.inner >= int64_t(1) << 19)
+    hipLaunchKernelGGL((k_join_spans<4>), dim3(uint32_t(heads * ((j.inner + 1023) / 1024))), dim3(256), 0, s, j);
+  else
+    hipLaunchKernelGGL((k_join_spans<1>), dim3(uint32_t(heads * ((j.inner + 255) / 256))), dim3(256), 0, s, j);
   return launch_status("k_join_spans");
 }
 
@@ -427,6 +435,22 @@ ssm_status_t run_fwd(const ssm_decay_attn_args_t* a, const Sizes& z, const FwdPl
   p.s_last = a->h_last;
   p.out = a->o;
   return run_mix<T, 1, T, kOut, false>(p, s);
+}
+
+// (tokens, heads, dk) fp32 to (tokens, key heads, dk).
+template <typename T>
+ssm_status_t sum_heads(void* out, const void* in, const Sizes& z, hipStream_t s) {
+  const int64_t n = z.tokens * z.Hk * z.dk;
+  const int32_t per = int32_t(z.H / z.Hk);
+  const bool four = z.dk % 4 == 0;
+  const dim3 grid(uint32_t(std::min<int64_t>((n / (four ? 4 : 1) + 255) / 256, 1 << 20)));
+  if (four)
+    hipLaunchKernelGGL((k_sum_heads<T, 4>), grid, dim3(256), 0, s, static_cast<T*>(out),
+                       static_cast<const float*>(in), n, int32_t(z.dk), per);
+  else
+    hipLaunchKernelGGL((k_sum_heads<T, 1>), grid, dim3(256), 0, s, static_cast<T*>(out),
+                       static_cast<const float*>(in), n, int32_t(z.dk), per);
+  return launch_status("k_sum_heads");
 }
 
 template <typename T>
@@ -491,24 +515,15 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
   dq.s_last = a->dh_last ? reinterpret_cast<float*>(ws + pl.off_s) : nullptr;
   dq.dots = reinterpret_cast<float*>(ws + pl.off_u);
   dk.dots = reinterpret_cast<float*>(ws + pl.off_w);
-  dq.out = shared ? ws + pl.off_dq : a->dq;
-  dk.out = shared ? ws + pl.off_dk : a->dk;
+  dq.out = shared ? ws + pl.off_heads : a->dq;
+  dk.out = shared ? ws + pl.off_heads : a->dk;
   if (ssm_status_t st = run_mix<T, 1, T, kOut, true>(dv, s)) return st;
   if (shared) {
+    // per value head into one buffer, each summed while the caches still hold it
     if (ssm_status_t st = run_mix<T, 2, float, kOutDots, false>(dq, s)) return st;
+    if (ssm_status_t st = sum_heads<T>(a->dq, dq.out, z, s)) return st;
     if (ssm_status_t st = run_mix<T, 2, float, kOutDots, true>(dk, s)) return st;
-    const int64_t n = z.tokens * z.Hk * z.dk;
-    const bool four = z.dk % 4 == 0;
-    const dim3 grid(uint32_t(std::min<int64_t>((n / (four ? 4 : 1) + 255) / 256, 1 << 20)));
-    for (int i = 0; i < 2; ++i) {
-      T* out = static_cast<T*>(i ? a->dk : a->dq);
-      const float* in = static_cast<const float*>(i ? dk.out : dq.out);
-      if (four)
-        hipLaunchKernelGGL((k_sum_heads<T, 4>), grid, dim3(256), 0, s, out, in, n, int32_t(z.dk), int32_t(per));
-      else
-        hipLaunchKernelGGL((k_sum_heads<T, 1>), grid, dim3(256), 0, s, out, in, n, int32_t(z.dk), int32_t(per));
-      if (ssm_status_t st = launch_status("k_sum_heads")) return st;
-    }
+    if (ssm_status_t st = sum_heads<T>(a->dk, dk.out, z, s)) return st;
   } else {
     if (ssm_status_t st = run_mix<T, 2, T, kOutDots, false>(dq, s)) return st;
     if (ssm_status_t st = run_mix<T, 2, T, kOutDots, true>(dk, s)) return st;

@@ -94,12 +94,12 @@ struct MixParams {
   const float* s0;       // state before the first token, or null
   float* s_last;         // state after the last, or null
   int64_t sm, sn;        // strides of S(m, n) within a head's state (s0, s_last)
-  const float* carry;    // (B, H, spans, M x N): state entering each span; null with one span
+  const float* carry;    // (B, H, spans, M x N): slot k, the state entering span k + 1; null with one span
   int64_t cm, cn;        // strides of S(m, n) within a carry
   float* sum;            // (B, H, spans, M, N): a span's end state from zero (the state pass)
   float* total;          // (B, H, spans): a span's decay (the state pass)
   void* out;             // (B, L, H, N)
-  float* dots;           // (slices of N, B, H, L): out_t . x_t over a wave's slice
+  float* dots;           // (slices of N, B, H, span x spans): out_t . x_t over a wave's slice
   int64_t B, L, H, span; // span: tokens per span, a multiple of the chunk
   int32_t M, N, spans, tiles;
   int32_t walked;        // spans of this launch: all, or (the state pass) all but the last
@@ -124,15 +124,22 @@ __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_ex
 template <typename T>
 struct Operand;
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two values rounded to bf16, in one register; and as floats again.
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+__device__ __forceinline__ float low16(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
 template <>
 struct Operand<bf16_t> {
   bf16x8 v;   // [half][i]
   __device__ __forceinline__ void set(const f32x4& lo, const f32x4& hi) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = static_cast<__bf16>(lo[i]);
-      v[4 + i] = static_cast<__bf16>(hi[i]);
-    }
+    v = __builtin_bit_cast(bf16x8, u32x4{round2(lo[0], lo[1]), round2(lo[2], lo[3]), round2(hi[0], hi[1]),
+                                         round2(hi[2], hi[3])});
   }
 };
 
@@ -163,11 +170,9 @@ __device__ __forceinline__ void split(Operand<bf16_t> (&o)[SP], f32x4 lo, f32x4 
   for (int s = 0; s < SP; ++s) {
     o[s].set(lo, hi);
     if (s + 1 < SP) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] -= static_cast<float>(o[s].v[i]);
-        hi[i] -= static_cast<float>(o[s].v[4 + i]);
-      }
+      const u32x4 u = __builtin_bit_cast(u32x4, o[s].v);
+      lo -= f32x4{low16(u[0]), high16(u[0]), low16(u[1]), high16(u[1])};
+      hi -= f32x4{low16(u[2]), high16(u[2]), low16(u[3]), high16(u[3])};
     }
   }
 }
@@ -190,12 +195,11 @@ struct Lds;
 template <>
 struct Lds<bf16_t> {
   static constexpr int kVec = 8;         // elements in 16 bytes
-#ifndef PADB
-#define PADB 24
-#define PADC 8
-#endif
-  static constexpr int kPad = PADB;        // 12 words: rows fall on different banks
-  static constexpr int kPadC = PADC;
+  // rows 8 words apart modulo the 64 banks: reads along and down the rows then
+  // meet no conflicts (counted: 64 reads along 1792 cycles of conflict without
+  // padding, 256 with 24 elements, 0 with 16; down 896, 128-256, 0-128)
+  static constexpr int kPad = 16;
+  static constexpr int kPadC = 16;
   // block t of 32 columns of a row
   __device__ static __forceinline__ Operand<bf16_t> along(const bf16_t* row, int t, int g) {
     Operand<bf16_t> o;
@@ -378,15 +382,18 @@ enum Part : int { kState = 0, kOut = 1, kOutDots = 2 };
 // decay sums differences of what they give).  The state itself is fp32: its
 // update takes the decayed rows in three parts, 24 bits.
 // ---------------------------------------------------------------------------
-template <typename T, int MP, int W>
+// Waves a SIMD is to hold: four (128 registers each) where that does not spill,
+// since a chunk's steps wait on each other and other waves fill the gaps.  The
+// parts of the scores and the state (SP = 2) do spill: every reload from scratch
+// also waits for the rows on their way (training step's two such passes, 4 x 4096
+// x 20 heads x 128 x 128: 200 us each with four, 150 with two).
+template <int MP, int SP>
 constexpr int waves_per_simd() {
-  // four where registers (128 each) and LDS allow: the chunk's steps wait on
-  // each other, and other waves fill the gaps
-  return MP <= 128 ? 4 : 2;
+  return MP <= 128 && SP == 1 ? 4 : 2;
 }
 
 template <typename T, int MP, int W, int CT, int SP, typename OutT, Part PART, bool REV, bool FAST>
-__global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(MixParams p) {
+__global__ __launch_bounds__(64 * W, (waves_per_simd<MP, SP>())) void k_mix(MixParams p) {
   using LD = Lds<T>;
   constexpr bool OUT = PART != kState;
   constexpr int NW = 16 * W, MT = MP / 16, QT = CT / 16, KT = CT / 32;
@@ -417,7 +424,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
   const T* px = PART == kOutDots ? row_base<T>(p.x, b, h) : nullptr;
   OutT* const po = OUT ? static_cast<OutT*>(p.out) + (b * p.L * p.H + h) * p.N : nullptr;
   const int64_t ost = p.H * p.N;
-  float* const dots = PART == kOutDots ? p.dots + ((int64_t(tile) * W + w) * p.B * p.H + bh) * p.L : nullptr;
+  float* const dots = PART == kOutDots ? p.dots + ((int64_t(tile) * W + w) * p.B * p.H + bh) * p.span * p.spans : nullptr;
 
   // the lowest token of the chunk taken k-th; backward, positions count from the
   // end of the last span, so that spans and chunks have the same boundaries
@@ -433,7 +440,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) S[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   if (OUT && (span > 0 || p.s0)) {
-    const float* src = span > 0 ? p.carry + (bh * p.spans + span) * p.M * p.N : p.s0 + bh * p.M * p.N;
+    const float* src = span > 0 ? p.carry + (bh * p.spans + span - 1) * p.M * p.N : p.s0 + bh * p.M * p.N;
     const int64_t sm = span > 0 ? p.cm : p.sm, sn = span > 0 ? p.cn : p.sn;
     const int n = nw + r;
     const float* col = src + n * sn;
@@ -480,6 +487,30 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
     if (!OUT) all += tot;
   };
 
+  // A chunk's rows out are held until the next chunk's rows are in LDS: loads
+  // and stores are waited for in order, and the wait for those rows would
+  // otherwise be one for these stores too.
+  typedef uint32_t Held __attribute__((ext_vector_type(sizeof(OutT))));
+  Held held[OUT && FAST ? QT : 1];
+  int64_t held_low = -1;   // lowest token of the held chunk
+  auto write_held = [&]() {
+    if (!OUT || !FAST || held_low < 0) return;
+    const uint32_t pitch = uint32_t(ost) * uint32_t(sizeof(OutT));
+    const int n = nw + 4 * g, left = p.L - held_low < CT ? int(p.L - held_low) : CT;
+    const uint32_t off =
+        n < p.N ? uint32_t(REV ? 15 - r : r) * pitch + uint32_t(n) * uint32_t(sizeof(OutT)) : kOutside;
+#pragma unroll
+    for (int q = 0; q < (OUT && FAST ? QT : 1); ++q) {
+      const int row = REV ? CT - 16 - 16 * q : 16 * q;
+      const auto win = window(po + (held_low + row) * ost, left - row, pitch, p.N * int(sizeof(OutT)));
+      if constexpr (sizeof(OutT) == 4)
+        __builtin_amdgcn_raw_buffer_store_b128(held[q], win, off, 0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b64(held[q], win, off, 0, 0);
+    }
+    held_low = -1;
+  };
+
   bool have = false;
   for (int k = 0; k < chunks; ++k) {
     const int64_t low = lowest(k);
@@ -507,6 +538,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
     if constexpr (OUT) qa.template store<REV>(sA, kStride);
     qb.template store<REV>(sB, kStride);
     qc.template store<REV>(sC, kStrideC);
+    write_held();
     __syncthreads();
     have = k + 1 < chunks && lowest(k + 1) < live;
     if (have) {
@@ -605,10 +637,8 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
     for (int t = 0; t < KT; ++t) c[t] = LD::down(sC, kStrideC, t, g, r, w * 16 + LD::group_col(r));
 
     if constexpr (OUT) {
-      const uint32_t opitch = uint32_t(ost) * uint32_t(sizeof(OutT));
       const int n = nw + 4 * g;   // the lane's columns n..n + 3
-      const uint32_t off =
-          n < p.N ? uint32_t(REV ? 15 - r : r) * opitch + uint32_t(n) * uint32_t(sizeof(OutT)) : kOutside;
+      held_low = low;
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
 #pragma unroll
@@ -617,19 +647,14 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
 #pragma unroll
           for (int s = 0; s < SP; ++s) acc[q] = mma(c[t], sP[score_at(s, q, t) + lane], acc[q]);
         }
-        const int row0 = REV ? CT - 16 - 16 * q : 16 * q, row = row0 + (REV ? 15 - r : r);   // the lane's query
+        const int row = (REV ? CT - 16 - 16 * q : 16 * q) + (REV ? 15 - r : r);   // the lane's query
         const bool on = row < rows;
-        if (!on) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (rows < CT && !on) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (FAST) {
-          const auto win = window(po + (low + row0) * ost, orows - row0, opitch, p.N * int(sizeof(OutT)));
-          if constexpr (sizeof(OutT) == 4) {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[q]), win, off, 0, 0);
-          } else {
-            Operand<bf16_t> v;
-            v.set(acc[q], acc[q]);
-            const u32x4 u = __builtin_bit_cast(u32x4, v.v);
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{u[0], u[1]}, win, off, 0, 0);
-          }
+          if constexpr (sizeof(OutT) == 4)
+            held[q] = __builtin_bit_cast(Held, acc[q]);
+          else
+            held[q] = Held{round2(acc[q][0], acc[q][1]), round2(acc[q][2], acc[q][3])};
         } else if (row < orows) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -671,8 +696,9 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(T) == 2) {
-          lo[i] = static_cast<float>(c[t].v[i]) * e[0][i];
-          hi[i] = static_cast<float>(c[t].v[4 + i]) * e[1][i];
+          const u32x4 u = __builtin_bit_cast(u32x4, c[t].v);
+          lo[i] = (i & 1 ? high16(u[i >> 1]) : low16(u[i >> 1])) * e[0][i];
+          hi[i] = (i & 1 ? high16(u[2 + (i >> 1)]) : low16(u[2 + (i >> 1)])) * e[1][i];
         } else {
           lo[i] = c[t].v[0][i] * e[0][i];
           hi[i] = c[t].v[1][i] * e[1][i];
@@ -689,6 +715,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
     }
   }
 
+  write_held();
   float* dst = nullptr;
   float f = 1.0f;
   int64_t dm = p.N, dn = 1;
@@ -718,42 +745,60 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, W>())) void k_mix(Mi
 }
 
 // Joins the spans: from each span's end state from zero and its decay, the
-// state entering every span, in place (the first span's slot takes s0).  A lane
-// per element of S; the loads of later spans do not wait for the chain.
+// state entering the span behind it, in place (slot k: the state entering span
+// k + 1).  A lane takes V elements of S through the spans; their reads do not
+// wait for the chain.
 struct JoinParams {
   float* sum;            // (B H, spans, M, N)
   const float* total;    // (B H, spans)
   const float* s0;       // or null
-  int64_t sm, sn, inner; // strides of s0; M x N
-  int32_t N, spans;
+  int64_t sm, sn;        // strides of s0
+  int32_t inner, N, spans;   // M x N
 };
 
-static __global__ __launch_bounds__(256) void k_join_spans(JoinParams p) {
-  const int64_t blocks = (p.inner + 255) / 256, bh = blockIdx.x / blocks;
-  const int64_t e = blockIdx.x % blocks * 256 + threadIdx.x;
-  if (e >= p.inner) return;
-  float* s = p.sum + bh * p.spans * p.inner + e;
-  const float* tot = p.total + bh * p.spans;
-  float run = p.s0 ? p.s0[bh * p.inner + e / p.N * p.sm + e % p.N * p.sn] : 0.0f;
-  constexpr int U = 32;
-  float v[U];
-  for (int k = 0; k < p.spans; k += U) {
+template <int V>
+__global__ __launch_bounds__(256) void k_join_spans(JoinParams p) {
+  typedef float fvec __attribute__((ext_vector_type(V)));
+  const uint32_t blocks = (uint32_t(p.inner) + 256 * V - 1) / (256 * V), bh = blockIdx.x / blocks;
+  const uint32_t e = (blockIdx.x % blocks * 256 + threadIdx.x) * V;
+  if (e >= uint32_t(p.inner)) return;
+  float* s = p.sum + int64_t(bh) * p.spans * p.inner + e;
+  const float* tot = p.total + int64_t(bh) * p.spans;
+  fvec run = fvec(0.0f);
+  if (p.s0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      run[i] = p.s0[int64_t(bh) * p.inner + (e + i) / uint32_t(p.N) * p.sm + (e + i) % uint32_t(p.N) * p.sn];
+  }
+  constexpr int U = V == 1 ? 32 : 8;
+  const int last = p.spans - 2;   // the last span's end joins nothing
+  for (int k = 0; k <= last; k += U) {
+    fvec v[U];
+    float f[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = k + u < last ? k + u : last;
+      v[u] = *reinterpret_cast<const fvec*>(s + int64_t(i) * p.inner);
+      f[u] = tot[i];
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (k + u < p.spans - 1) v[u] = s[(k + u) * p.inner];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (k + u < p.spans) {
-        s[(k + u) * p.inner] = run;
-        if (k + u < p.spans - 1) run = run * tot[k + u] + v[u];
+      if (k + u <= last) {
+        run = run * f[u] + v[u];
+        v[u] = run;
       }
+    // the state entering span k + u + 1: slot k + u of the carries, which start
+    // with the second span
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k + u <= last) *reinterpret_cast<fvec*>(s + int64_t(k + u) * p.inner) = v[u];
   }
 }
 
 struct DecayGradParams {
-  const float* u;        // (slices, B, H, L)
-  const float* w;        // (slices, B, H, L)
-  const float* carry;    // (B, H, spans, inner): states entering the spans (dq's layout)
+  const float* u;        // (slices, B, H, span x spans)
+  const float* w;        // the same
+  const float* carry;    // (B, H, spans, inner): slot k, the state entering span k + 1 (dq's layout)
   const float* rcarry;   // same of their gradients, spans counted from the end
   const float* s_last;   // (B, H, dk, dv), with dh_last; null: no flow through the end
   const float* dh_last;
@@ -768,39 +813,41 @@ struct DecayGradParams {
 __device__ __forceinline__ double partial_dot(const float* a, const float* b, int64_t n) {
   constexpr int U = 8;
   double sum = 0.0;
-  for (int64_t base = threadIdx.x; base < n; base += 256 * U) {
+  int64_t i = threadIdx.x;
+  for (int64_t whole = n / (256 * U); whole > 0; --whole, i += 256 * U) {
     float x[U], y[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = base + 256 * u;
-      x[u] = i < n ? a[i] : 0.0f;
-      y[u] = i < n ? b[i] : 0.0f;
+      x[u] = a[i + 256 * u];
+      y[u] = b[i + 256 * u];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) sum += double(x[u]) * y[u];
   }
+  for (; i < n; i += 256) sum += double(a[i]) * b[i];
   return sum;
 }
 
 // dg over one span: the flow through its end, then suffix sums of u - w within
-// it.  A workgroup per span; sums in 64 bits.
+// it.  A workgroup per span, eight tokens to a lane; sums in 64 bits.
 static __global__ __launch_bounds__(256) void k_decay_grad(DecayGradParams p) {
+  constexpr int E = 8, kBlock = 256 * E;
   __shared__ double part[4];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int span = int(blockIdx.x % p.spans);
-  const int64_t bh = blockIdx.x / p.spans, b = bh / p.H, h = bh % p.H;
-  const int64_t live = live_tokens(p.lengths, b, p.L), n = p.B * p.H * p.L;
+  const int span = int(blockIdx.x % uint32_t(p.spans));
+  const uint32_t bh = blockIdx.x / uint32_t(p.spans);
+  const int64_t b = bh / uint32_t(p.H), h = bh % uint32_t(p.H);
+  const int64_t live = live_tokens(p.lengths, b, p.L), padded = p.span * p.spans, n = p.B * p.H * padded;
   const int64_t t_begin = span * p.span, t_end = t_begin + p.span < p.L ? t_begin + p.span : p.L;
 
   double flow = 0.0;
   if (span + 1 < p.spans) {
-    const float* s = p.carry + (bh * p.spans + span + 1) * p.inner;
-    const float* q = p.rcarry + (bh * p.spans + (p.spans - 1 - span)) * p.inner;
-    flow = partial_dot(s, q, p.inner);
+    flow = partial_dot(p.carry + (int64_t(bh) * p.spans + span) * p.inner,
+                       p.rcarry + (int64_t(bh) * p.spans + (p.spans - 2 - span)) * p.inner, p.inner);
     const int64_t e = t_begin + p.span;   // the decay between the two
     if (e < live) flow *= exp2_fast(log_decay(p.g, b, e, h) * kLog2e);
   } else if (p.s_last) {
-    flow = partial_dot(p.s_last + bh * p.inner, p.dh_last + bh * p.inner, p.inner);
+    flow = partial_dot(p.s_last + int64_t(bh) * p.inner, p.dh_last + int64_t(bh) * p.inner, p.inner);
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) flow += __shfl_xor(flow, d);
@@ -808,35 +855,48 @@ static __global__ __launch_bounds__(256) void k_decay_grad(DecayGradParams p) {
   __syncthreads();
   double run = part[0] + part[1] + part[2] + part[3];
 
-  for (int64_t base = t_begin + (t_end - 1 - t_begin) / 256 * 256; base >= t_begin; base -= 256) {
-    const int64_t t = base + tid;
-    double v = 0.0;
+  for (int64_t base = t_begin + (t_end - 1 - t_begin) / kBlock * kBlock; base >= t_begin; base -= kBlock) {
+    const int64_t t = base + tid * E;
+    double v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.0;
     if (t < t_end && t < live) {
-      const int64_t i = bh * p.L + t;
-      for (int k = 0; k < p.slices; k += 4) {   // a multiple of 4
-        float x[4], y[4];
+      const float* u = p.u + int64_t(bh) * padded + t;   // spans, and so t, are multiples of eight
+      const float* o = p.w + int64_t(bh) * padded + t;
+      for (int k = 0; k < p.slices; k += 2) {   // an even number
+        f32x4 x[2][2], y[2][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = p.u[(k + j) * n + i];
-          y[j] = p.w[(k + j) * n + i];
-        }
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v += double(x[j]) - double(y[j]);
+          for (int q = 0; q < 2; ++q) {
+            x[j][q] = *reinterpret_cast<const f32x4*>(u + (k + j) * n + 4 * q);
+            y[j][q] = *reinterpret_cast<const f32x4*>(o + (k + j) * n + 4 * q);
+          }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (t + e < live) v[e] += double(x[j][e >> 2][e & 3]) - double(y[j][e >> 2][e & 3]);
       }
     }
 #pragma unroll
+    for (int e = E - 2; e >= 0; --e) v[e] += v[e + 1];
+    double behind = v[0];   // of the lanes from this one on, then of the later ones
+#pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_down(v, d);
-      if (lane + d < 64) v += o;
+      const double o = __shfl_down(behind, d);
+      if (lane + d < 64) behind += o;
     }
     __syncthreads();
-    if (lane == 0) part[w] = v;
+    if (lane == 0) part[w] = behind;
     __syncthreads();
-    double behind = run;
+    behind += run - v[0];
     for (int k = w + 1; k < 4; ++k) behind += part[k];
-    if (t < t_end) {
-      const float out = t < live ? float(v + behind) : 0.0f;
-      const int64_t i = (b * p.L + t) * p.H + h;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (t + e >= t_end) continue;
+      const float out = t + e < live ? float(v[e] + behind) : 0.0f;
+      const int64_t i = (b * p.L + t + e) * p.H + h;
       if (p.bf16)
         st(static_cast<bf16_t*>(p.dg) + i, out);
       else
