@@ -361,7 +361,7 @@ ssm_status_t run_mix(MixParams p, hipStream_t s) {
   const int64_t k = int64_t(16 / sizeof(OutT));
   p.tiles = int32_t(tiles_of(p.N));
   p.walked = PART == kState ? p.spans - 1 : p.spans;
-  bool fast = fast_rows(p.b, p.M, e) && fast_rows(p.c, p.N, e);
+  bool fast = fast_rows(p.b, p.M, e) && fast_rows(p.c, p.N, e) && p.g.st < (int64_t(1) << 31) / 64 / 4;
   if (PART != kState)
     fast = fast && fast_rows(p.a, p.M, e) && !misaligned(p.out, 16) && p.N % k == 0 &&
            p.H * p.N < (int64_t(1) << 31) / 64 / int64_t(sizeof(OutT));

@@ -384,16 +384,17 @@ enum Part : int { kState = 0, kOut = 1, kOutDots = 2 };
 // ---------------------------------------------------------------------------
 // Waves a SIMD is to hold: four (128 registers each) where that does not spill,
 // since a chunk's steps wait on each other and other waves fill the gaps.  The
-// parts of the scores and the state (SP = 2) do spill: every reload from scratch
-// also waits for the rows on their way (training step's two such passes, 4 x 4096
-// x 20 heads x 128 x 128: 200 us each with four, 150 with two).
-template <int MP, int SP>
+// parts of the scores and the state (SP = 2) do spill, and so do 128 rows of S
+// with fp32 operands: every reload from scratch also waits for the rows on their
+// way (two passes of 4 x 4096 x 20 heads x 128 x 128 with SP = 2: 200 us each
+// with four, 150 with two; 2048 x 256 heads x 128 x 128 fp32: 453 and 413 us).
+template <typename T, int MP, int SP>
 constexpr int waves_per_simd() {
-  return MP <= 128 && SP == 1 ? 4 : 2;
+  return SP == 1 && MP <= (sizeof(T) == 4 ? 64 : 128) ? 4 : 2;
 }
 
 template <typename T, int MP, int W, int CT, int SP, typename OutT, Part PART, bool REV, bool FAST>
-__global__ __launch_bounds__(64 * W, (waves_per_simd<MP, SP>())) void k_mix(MixParams p) {
+__global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(MixParams p) {
   using LD = Lds<T>;
   constexpr bool OUT = PART != kState;
   constexpr int NW = 16 * W, MT = MP / 16, QT = CT / 16, KT = CT / 32;
@@ -467,9 +468,23 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<MP, SP>())) void k_mix(MixP
   double all = 0.0;   // the state pass: sum of the log decays behind the chunk
   auto fetch_decays = [&](int64_t low) {
     // backward, the decay stands behind the token
-    const int64_t t = low + (REV ? CT - lane : lane);
+    const int64_t first = low + (REV ? 1 : 0);
+    const int row = REV ? CT - 1 - lane : lane, left = live - first < CT ? int(live - first) : CT;
     gl = 0;
-    if (lane < CT && t < live) gl = log_decay_bits(p.g, b, t, h);
+    if (row >= 0 && row < left) {
+      if constexpr (FAST) {
+        const uint32_t es = p.g.bf16 ? 2 : 4, pitch = uint32_t(p.g.st) * es;
+        const auto win = window(static_cast<const char*>(p.g.p) + (b * p.g.sb + first * p.g.st + h * p.g.sh) * es,
+                                left, pitch, int(es));
+        const uint32_t off = uint32_t(row) * pitch;
+        if (p.g.bf16)
+          gl = __builtin_amdgcn_raw_buffer_load_b16(win, off, 0, 0);
+        else
+          gl = __builtin_amdgcn_raw_buffer_load_b32(win, off, 0, 0);
+      } else {
+        gl = log_decay_bits(p.g, b, first + row, h);
+      }
+    }
   };
   auto sum_decays = [&](int buf) {
     const double bs = wave_running_sum(log_decay_of(p.g, gl) * kLog2e), tot = last_lane(bs);
