@@ -332,6 +332,28 @@ struct Stage {
   }
 };
 
+// The other way: rows in LDS that lie as a Stage would have stored them, out to
+// memory.  A lane takes the places that it would store to, so that it can follow
+// with the next rows without another wait.
+template <typename T, int ROWS, int COLS, int THREADS, bool REV>
+__device__ __forceinline__ void write_rows(T* base, int64_t st, int64_t first, int64_t end, int col0, int n, const T* s,
+                                           int stride) {
+  typedef Stage<T, ROWS, COLS, THREADS, true> St;
+  const int row = threadIdx.x / St::kPerRow, col = threadIdx.x % St::kPerRow * Lds<T>::kVec;
+  if (St::kFew && row >= ROWS) return;
+  const T* p = s + (REV ? (St::kFew ? ROWS : St::kStep) - 1 - row : row) * stride + col;
+  const int left = end - first < ROWS ? int(end - first) : ROWS;
+  const uint32_t pitch = uint32_t(st) * uint32_t(sizeof(T));
+  const uint32_t off =
+      col + col0 < n ? uint32_t(row) * pitch + uint32_t(col + col0) * uint32_t(sizeof(T)) : kOutside;
+#pragma unroll
+  for (int k = 0; k < St::kCount; ++k) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(p + (REV ? St::kCount - 1 - k : k) * St::kStep * stride);
+    __builtin_amdgcn_raw_buffer_store_b128(
+        v, window(base + (first + k * St::kStep) * st, left - k * St::kStep, pitch, n * int(sizeof(T))), off, 0, 0);
+  }
+}
+
 // v plus its value in other lanes (0 where there is none), over two registers.
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ double add_lanes(double v) {
@@ -502,26 +524,32 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     if (!OUT) all += tot;
   };
 
-  // A chunk's rows out are held until the next chunk's rows are in LDS: loads
-  // and stores are waited for in order, and the wait for those rows would
-  // otherwise be one for these stores too.
-  typedef uint32_t Held __attribute__((ext_vector_type(sizeof(OutT))));
-  Held held[OUT && FAST ? QT : 1];
+  // A chunk's rows out are held until the next chunk's rows go to LDS: loads and
+  // stores are waited for in order, and the wait for those rows would otherwise
+  // be one for these stores too.  bf16 rows are held in c's place in LDS (a wave
+  // has read its columns of c by then, and no other wave reads them) and leave
+  // as whole rows; fp32 ones in registers, 64 bytes of a row to a wave (2048 x
+  // 512 heads x 64 x 64: bf16 138 us through registers, 130 through LDS; 8 x 2048
+  // x 24 x 64 x 64 fp32 178 and 193).
+  constexpr bool SWAP = OUT && FAST && sizeof(T) == 2 && sizeof(OutT) == 2;
+  constexpr bool HOLD = OUT && FAST && !SWAP;
+  u32x4 held[HOLD ? QT : 1];
   int64_t held_low = -1;   // lowest token of the held chunk
   auto write_held = [&]() {
-    if (!OUT || !FAST || held_low < 0) return;
-    const uint32_t pitch = uint32_t(ost) * uint32_t(sizeof(OutT));
-    const int n = nw + 4 * g, left = p.L - held_low < CT ? int(p.L - held_low) : CT;
-    const uint32_t off =
-        n < p.N ? uint32_t(REV ? 15 - r : r) * pitch + uint32_t(n) * uint32_t(sizeof(OutT)) : kOutside;
+    if (held_low < 0) return;
+    if constexpr (SWAP) {
+      write_rows<T, CT, NW, 64 * W, REV>(reinterpret_cast<T*>(po), ost, held_low, p.L, n0, p.N, sC, kStrideC);
+    } else if constexpr (HOLD) {
+      const uint32_t pitch = uint32_t(ost) * uint32_t(sizeof(OutT));
+      const int n = nw + 4 * g, left = p.L - held_low < CT ? int(p.L - held_low) : CT;
+      const uint32_t off =
+          n < p.N ? uint32_t(REV ? 15 - r : r) * pitch + uint32_t(n) * uint32_t(sizeof(OutT)) : kOutside;
 #pragma unroll
-    for (int q = 0; q < (OUT && FAST ? QT : 1); ++q) {
-      const int row = REV ? CT - 16 - 16 * q : 16 * q;
-      const auto win = window(po + (held_low + row) * ost, left - row, pitch, p.N * int(sizeof(OutT)));
-      if constexpr (sizeof(OutT) == 4)
-        __builtin_amdgcn_raw_buffer_store_b128(held[q], win, off, 0, 0);
-      else
-        __builtin_amdgcn_raw_buffer_store_b64(held[q], win, off, 0, 0);
+      for (int q = 0; q < QT; ++q) {
+        const int row = REV ? CT - 16 - 16 * q : 16 * q;
+        __builtin_amdgcn_raw_buffer_store_b128(
+            held[q], window(po + (held_low + row) * ost, left - row, pitch, p.N * int(sizeof(OutT))), off, 0, 0);
+      }
     }
     held_low = -1;
   };
@@ -552,8 +580,9 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     __syncthreads();
     if constexpr (OUT) qa.template store<REV>(sA, kStride);
     qb.template store<REV>(sB, kStride);
+    if constexpr (SWAP) write_held();   // out of c's place first
     qc.template store<REV>(sC, kStrideC);
-    write_held();
+    if constexpr (HOLD) write_held();
     __syncthreads();
     have = k + 1 < chunks && lowest(k + 1) < live;
     if (have) {
@@ -653,7 +682,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
 
     if constexpr (OUT) {
       const int n = nw + 4 * g;   // the lane's columns n..n + 3
-      held_low = low;
+      if (FAST) held_low = low;
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
 #pragma unroll
@@ -665,11 +694,14 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
         const int row = (REV ? CT - 16 - 16 * q : 16 * q) + (REV ? 15 - r : r);   // the lane's query
         const bool on = row < rows;
         if (rows < CT && !on) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (FAST) {
-          if constexpr (sizeof(OutT) == 4)
-            held[q] = __builtin_bit_cast(Held, acc[q]);
+        if constexpr (SWAP) {
+          T* to = sC + (16 * q + r) * kStrideC + w * 16 + 4 * g;
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<f32x4*>(to) = acc[q];
           else
-            held[q] = Held{round2(acc[q][0], acc[q][1]), round2(acc[q][2], acc[q][3])};
+            *reinterpret_cast<u32x2*>(to) = u32x2{round2(acc[q][0], acc[q][1]), round2(acc[q][2], acc[q][3])};
+        } else if constexpr (HOLD) {
+          held[q] = __builtin_bit_cast(u32x4, acc[q]);
         } else if (row < orows) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -730,6 +762,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     }
   }
 
+  if (SWAP) __syncthreads();
   write_held();
   float* dst = nullptr;
   float f = 1.0f;
