@@ -119,6 +119,10 @@ ssm_status_t check_step(const ssm_decay_attn_step_args_t* a, Sizes* z) {
   return check_alias(outs, 2, ins, 4);
 }
 
+// Columns a workgroup takes, 16 for each of its 4 or 8 waves.
+int64_t tile_width(int64_t N) { return N > 64 ? 128 : 64; }
+int64_t tiles_of(int64_t N) { return (N + tile_width(N) - 1) / tile_width(N); }
+
 // How the time axis is cut: `spans` spans of `span` tokens (a multiple of
 // kSpanAlign), each walked by workgroups of its own.
 struct Cut {
@@ -128,19 +132,19 @@ struct Cut {
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 // The plan's cut, the cheapest by this count.  `walkers` workgroups walk a span
-// of n chunks in n + 1 steps (one to fill), and m of them on a CU take 0.4 +
-// 0.6 m times as long as one (measured, 32 chunks each of 128 x 128 bf16 / 64 x
-// 64 bf16 / 64 x 64 fp32, us for one, two, three on a CU: 163, 278, - / 99, 139,
-// 219 / 201, 320, 424).  More than one span costs the first pass over all but
-// the last (`state`, its share of a step), two launches (two steps), and reading
-// and writing the spans' states five times (16 MB a step); the backward's three
-// passes share two such first passes and joins (a third and two thirds of a
-// pass's).  Measured, us by
-// number of spans: 80 walkers of 128 chunks, 128 x 128 bf16: 3 330, 6 293, 12
-// 307, 24 329; 4 walkers of 2048 chunks: 64 234, 128 213, 256 264; 320 walkers
-// of 32 chunks: 1 246, 3 315; 192 walkers of 32 chunks, 64 x 64 fp32: 1 182, 2
-// 216, 4 157, 8 171.
-Cut cut_time(int64_t L, int64_t walkers, int64_t inner, double state, double join, int32_t span) {
+// of n chunks in n + 1 steps (one to fill).  m workgroups on a CU take 1 + slope
+// (m - 1) times as long as one: slope 0.7 for those of eight waves, 0.6 for those
+// of four (2048 tokens, us for 1, 2, 4 on a CU of 128 x 128 bf16: 163, 278, 540;
+// 1, 2, 3 of 64 x 64 fp32: 201, 320, 424).  More than one span costs the first
+// pass over all but the last (`state`, its share of a step), two launches (two
+// steps), and reading and writing the spans' states (32 MB a step); the backward's
+// three passes share two such first passes and joins (two thirds of a pass's).
+// Measured, us by number of spans, the plan's marked: 80 walkers of 128 chunks,
+// 128 x 128 bf16: 3 298, *6 246, 12 285, 24 325; 4 walkers of 2048 chunks: 64
+// 223, *128 192, 256 231; 320 walkers of 32 chunks: *1 214, 2 259, 3 265; 192
+// walkers of 32 chunks, 64 x 64 fp32: 1 181, 3 170, *4 143, 8 151; bf16 85, 74,
+// *67, 77.
+Cut cut_time(int64_t L, int64_t walkers, int64_t inner, double slope, double state, double join, int32_t span) {
   constexpr int64_t kCus = 256, kMaxSpans = 1024;
   Cut c;
   if (L == 0 || walkers == 0) return c;
@@ -151,14 +155,14 @@ Cut cut_time(int64_t L, int64_t walkers, int64_t inner, double state, double joi
   } else {
     const int64_t most = std::min({chunks, kMaxSpans, 1 + 8 * kCus / walkers});
     double least = 0.0;
-    auto step = [&](int64_t groups) { return 0.4 + 0.6 * double((groups + kCus - 1) / kCus); };
+    auto step = [&](int64_t groups) { return 1.0 + slope * double((groups - 1) / kCus); };
     for (int64_t want = 1; want <= most; ++want) {
       const int64_t per = (chunks + want - 1) / want, n = (chunks + per - 1) / per;
       if (n != want) continue;
       double cost = double(per + 1) * step(walkers * n);
       if (n > 1)
         cost += state * double(per + 1) * step(walkers * (n - 1)) +
-                join * (2.0 + double(n * walkers) * double(inner) / 0.8e6);
+                join * (2.0 + double(n * walkers) * double(inner) / 1.6e6);
       if (want == 1 || cost < least) {
         least = cost;
         best = per;
@@ -170,10 +174,6 @@ Cut cut_time(int64_t L, int64_t walkers, int64_t inner, double state, double joi
   return c;
 }
 
-// Columns a workgroup takes, 16 for each of its 4 or 8 waves.
-int64_t tile_width(int64_t N) { return N > 64 ? 128 : 64; }
-int64_t tiles_of(int64_t N) { return (N + tile_width(N) - 1) / tile_width(N); }
-
 // Workspace of the forward pass: the states entering the spans and their decays.
 struct FwdPlan {
   Cut cut;
@@ -182,7 +182,8 @@ struct FwdPlan {
 
 FwdPlan make_fwd_plan(const Sizes& z, int32_t span) {
   FwdPlan pl;
-  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dv), z.dk * z.dv, 0.5, 1.0, span);
+  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dv), z.dk * z.dv, tile_width(z.dv) == 128 ? 0.7 : 0.6, 0.35, 1.0,
+                    span);
   if (pl.cut.spans > 1) {
     pl.off_total = align256(size_t(z.state) * size_t(pl.cut.spans) * 4);
     pl.total = pl.off_total + align256(size_t(z.B * z.H) * size_t(pl.cut.spans) * 4);
@@ -206,7 +207,8 @@ BwdPlan make_bwd_plan(const Sizes& z, int32_t span) {
     off += align256(bytes);
     return o;
   };
-  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dk), z.dk * z.dv, 1.0 / 3, 2.0 / 3, span);
+  pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dk), z.dk * z.dv, tile_width(z.dk) == 128 ? 0.7 : 0.6, 0.35 * 2 / 3,
+                    2.0 / 3, span);
   pl.slices = tile_width(z.dk) / 16 * tiles_of(z.dk);
   const size_t th = size_t(z.tokens) * size_t(z.H);
   const size_t dots = size_t(z.B * z.H) * size_t(pl.cut.span * pl.cut.spans) * size_t(pl.slices) * 4;

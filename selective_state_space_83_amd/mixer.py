@@ -132,7 +132,11 @@ def _current(stream):
     """The current device's index and the handle of the stream to launch on."""
     torch = _torch()
     dev = torch.cuda.current_device()
-    return dev, torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    if stream is not None:
+        return dev, stream.cuda_stream
+    # the same handle without a Stream object around it, where this PyTorch has it
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return dev, raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _refuse(t, name, shape, dtype, dev):
