@@ -383,12 +383,16 @@ ssm_status_t run_carries(MixParams p, float* carry, float* total, hipStream_t s)
   if (ssm_status_t st = run_mix<T, 1, T, kState, REV>(p, s)) return st;
   const JoinParams j{carry, total, p.s0, p.sm, p.sn, p.M * p.N, p.N, p.spans};
   // four elements to a lane where that leaves enough lanes; few heads with many
-  // spans want the lanes
+  // spans want the lanes, and the reads in flight (4 heads of 128 x 128, 128
+  // spans: 29 us with 8, 17 with 32; 96 heads of 64 x 64, 8 spans: 13 us with 32)
   const int64_t heads = p.B * p.H;
+  const dim3 ones(uint32_t(heads * ((j.inner + 255) / 256)));
   if (j.inner % 4 == 0 && heads * j.inner >= int64_t(1) << 19)
-    hipLaunchKernelGGL((k_join_spans<4>), dim3(uint32_t(heads * ((j.inner + 1023) / 1024))), dim3(256), 0, s, j);
+    hipLaunchKernelGGL((k_join_spans<4, 8>), dim3(uint32_t(heads * ((j.inner + 1023) / 1024))), dim3(256), 0, s, j);
+  else if (p.spans <= 16)
+    hipLaunchKernelGGL((k_join_spans<1, 8>), ones, dim3(256), 0, s, j);
   else
-    hipLaunchKernelGGL((k_join_spans<1>), dim3(uint32_t(heads * ((j.inner + 255) / 256))), dim3(256), 0, s, j);
+    hipLaunchKernelGGL((k_join_spans<1, 32>), ones, dim3(256), 0, s, j);
   return launch_status("k_join_spans");
 }
 

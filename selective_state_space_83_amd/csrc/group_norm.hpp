@@ -200,6 +200,8 @@ __device__ __forceinline__ float normalize(float (&u)[R * V], int lane, const No
 
 // Forward: TG lanes share a group of a row and walk p.per rows of it; a
 // workgroup of 256 holds 256 / TG of them, numbered (block of rows, group).
+// Bound by memory: 32768 x 2560 gated bf16 in 98 us, 5.1 TB/s (122 us with the
+// weights read a channel at a time).
 template <typename T, int V, int TG, int R, bool Z>
 __global__ __launch_bounds__(256) void k_norm(NormParams p) {
   __shared__ float part[8];
@@ -251,7 +253,8 @@ __global__ __launch_bounds__(256) void k_norm(NormParams p) {
 }
 
 // Backward, the same walk: dx (and dz) of every row, and the sums over the
-// block's rows for the gradients of weight and bias.
+// block's rows for the gradients of weight and bias.  Bound by memory: 16384 x
+// 1536 gated fp32 in 93 us, 5.4 TB/s.
 template <typename T, int V, int TG, int R, bool Z>
 __global__ __launch_bounds__(256) void k_norm_bwd(NormParams p) {
   __shared__ float part[8];
