@@ -421,3 +421,45 @@ def test_binding_refuses():
         ssm.decay_attn_step(h.transpose(-1, -2), q[:, 0], k[:, 0], v[:, 0], g[:, 0])
     with pytest.raises(ValueError):
         ssm.decay_attn_step(h, q[:, 0], k[:, 0], v[:, 0], g)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dk,dv", [(8, 128), (24, 96), (32, 256), (64, 160), (128, 200), (200, 128), (256, 72)])
+def test_wide_values_in_spans(dk, dv, dtype):
+    """More columns than a workgroup takes, over several spans, forward and back."""
+    t = make(1, 333, 2, 1, dk, dv, dtype, seed=dk + dv, h0=True, grad=True)
+    check_fwd(t, span=128)
+    check_bwd(t, span=128)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_ragged_lengths_across_spans(dtype):
+    """Rows that end inside a span, on its edge, before it, and not at all."""
+    t = make(6, 1000, 2, 2, 64, 64, dtype, seed=102, h0=True, grad=True)
+    n = _ragged(t, [0, 130, 999, 640, 1000, 64], float("nan"))
+    check_fwd(t, n, span=128)
+    check_bwd(t, n, span=128)
+    check_fwd(t, n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_heads_joined(dtype):
+    """Enough states that a lane joins four elements; and more spans than it reads
+    ahead."""
+    check_fwd(make(2, 256, 16, 16, 128, 128, dtype, seed=103, h0=True), span=64)
+    t = make(1, 64 * 20 + 5, 1, 1, 16, 16, dtype, seed=104, h0=True, grad=True)
+    check_fwd(t, span=64)
+    check_bwd(t, span=64)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_broadcast_over_time(dtype):
+    """A token stride of 0, for rows and decays, and rows that overlap."""
+    t = make(2, 100, 2, 2, 16, 16, dtype, seed=105, h0=True, grad=True)
+    for n in ("q", "k", "v", "g", "dout"):
+        t[n] = t[n][:, :1].expand(t[n].shape)
+    check_fwd(t)
+    check_bwd(t)
+    flat = torch.randn(2 * 200, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+    t["v"] = flat.as_strided((2, 100, 2, 16), (200, 1, 16, 1))
+    check_fwd(t)

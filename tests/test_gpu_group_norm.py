@@ -58,7 +58,7 @@ def test_modes(dtype, mode, rms):
 
 
 SIZES = [(1, 1), (1, 2), (3, 5), (7, 8), (5, 16), (3, 33), (2, 63), (4, 64), (2, 100), (3, 128), (1, 255),
-         (2, 256), (2, 500), (1, 512), (1, 1000), (1, 1024), (2, 2048), (1, 2560), (1, 4097), (1, 5120), (1, 12000),
+         (2, 256), (2, 500), (1, 512), (1, 1000), (1, 1024), (2, 2048), (1, 2560), (1, 4097), (1, 5120), (1, 12000), (1, 2049),
          (1, 20001), (80, 64), (41, 24)]
 
 
