@@ -138,8 +138,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     # system runtime, and launches would not see the device PyTorch uses
     _torch()
     lib = ctypes.CDLL(path)
+    # before any other symbol is looked up: an older build may lack some (entry
+    # points are added without a new version, which counts changes of old ones)
+    missing = [name for name in EXPORTS if not hasattr(lib, name)]
+    if missing:
+        raise RuntimeError("%s lacks %s; rebuild it" % (path, ", ".join(missing)))
     lib.ssm_abi_version.restype = ctypes.c_int
     lib.ssm_abi_version.argtypes = []
+    got = int(lib.ssm_abi_version())
+    if got != ABI_VERSION:
+        raise RuntimeError("%s has ABI version %d, this binding mirrors version %d; rebuild it"
+                           % (path, got, ABI_VERSION))
     lib.ssm_scan_workspace_size.restype = ctypes.c_size_t
     lib.ssm_scan_workspace_size.argtypes = [ctypes.POINTER(ScanArgs)]
     lib.ssm_scan_plan_chunk_len.restype = ctypes.c_int64
@@ -161,10 +170,6 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ssm_last_error_message.restype = ctypes.c_char_p
     lib.ssm_last_error_message.argtypes = []
     mixer.declare(lib)
-    got = int(lib.ssm_abi_version())
-    if got != ABI_VERSION:
-        raise RuntimeError("%s has ABI version %d, this binding mirrors version %d; rebuild it"
-                           % (path, got, ABI_VERSION))
     if path == LIB_PATH:
         _lib = lib
     return lib
