@@ -129,11 +129,12 @@ def _code(t, name):
 
 
 def _current(stream):
-    """The current device's index and the handle of the stream to launch on."""
+    """Index of the device the call runs on, the given stream's or the current one,
+    and the handle of the stream to launch on."""
     torch = _torch()
-    dev = torch.cuda.current_device()
     if stream is not None:
-        return dev, stream.cuda_stream
+        return stream.device.index, stream.cuda_stream
+    dev = torch.cuda.current_device()
     # the same handle without a Stream object around it, where this PyTorch has it
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return dev, raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
