@@ -337,8 +337,11 @@ ssm_status_t ssm_scan_bwd(const ssm_scan_bwd_args_t* args, void* hip_stream);
  *            may hold anything, NaN included): o and every gradient are 0
  *            there, and h_last is the state after the last of the row's tokens
  *            (h0 for a row without any).
- *   Decay    any log_decay is taken; -inf, or a value whose exp is 0, resets
- *            the state.  Values below -128 act as -128 (exp is 0 in fp32).
+ *   Decay    any log_decay is taken, growth (above 0) included: -inf, or a value
+ *            whose exp is 0 in fp32, resets the state, and what is zero stays
+ *            zero however much it grows.  From a block of 64 tokens on whose
+ *            log decays above 0 add up to more than 22, its head is walked token
+ *            by token (4 x 8192 x 20 heads of 128 x 128, bf16: 1.8 ms for 0.24).
  *   Dtypes   q, k, v, o, dout, dq, dk, dv share dtype; log_decay and dlog_decay
  *            have decay_dtype; states and their gradients are fp32, and so are
  *            all sums.  With bf16 inputs the products of decayed scores with

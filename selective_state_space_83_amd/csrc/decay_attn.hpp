@@ -40,6 +40,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // exp of a decay below this is 0 in fp32; clamped there, sums of log decays
 // stay finite and differences of them are defined (a reset is log decay -inf)
 constexpr float kMinLogDecay = -128.0f;
+// The most that the log2 decays of a chunk may grow for its products' form to
+// hold: every exp then stays below 2^32, so that nothing times it overflows that
+// the recurrence keeps, and a clamped reset followed by growth (2^-184 2^32) is
+// still 0.  Chunks that grow more are walked token by token.
+constexpr float kMaxGrowth = 32.0f;
 
 __device__ __forceinline__ float ld(const float* p) { return *p; }
 __device__ __forceinline__ float ld(const bf16_t* p) {
@@ -74,8 +79,7 @@ __device__ __forceinline__ uint32_t log_decay_bits(const Decay& d, int64_t b, in
   return d.bf16 ? static_cast<const bf16_t*>(d.p)[i] : static_cast<const uint32_t*>(d.p)[i];
 }
 __device__ __forceinline__ float log_decay_of(const Decay& d, uint32_t bits) {
-  const float g = __uint_as_float(d.bf16 ? bits << 16 : bits);
-  return g < kMinLogDecay ? kMinLogDecay : g;   // a NaN stays one
+  return __uint_as_float(d.bf16 ? bits << 16 : bits);
 }
 __device__ __forceinline__ float log_decay(const Decay& d, int64_t b, int64_t t, int64_t h) {
   return log_decay_of(d, log_decay_bits(d, b, t, h));
@@ -97,7 +101,7 @@ struct MixParams {
   const float* carry;    // (B, H, spans, M x N): slot k, the state entering span k + 1; null with one span
   int64_t cm, cn;        // strides of S(m, n) within a carry
   float* sum;            // (B, H, spans, M, N): a span's end state from zero (the state pass)
-  float* total;          // (B, H, spans): a span's decay (the state pass)
+  float* total;          // (B, H, spans): the root of a span's decay, exp2_half (the state pass)
   void* out;             // (B, L, H, N)
   float* dots;           // (slices of N, B, H, span x spans): out_t . x_t over a wave's slice
   int64_t B, L, H, span; // span: tokens per span, a multiple of the chunk
@@ -112,6 +116,13 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// 2^(v / 2), at most 2^127: x 2^v is formed as x f f, which keeps a zero zero
+// where 2^v overflows, and what 2^v brings into range or out of it in place
+// (past 2^254 everything but a zero has overflowed).
+__device__ __forceinline__ float exp2_half(float v) {
+  return exp2_fast(0.5f * (v > 254.0f && v < __builtin_inff() ? 254.0f : v));
+}
 
 // A matrix operand over 32 contracted indices.  The 16 x 16 matrix instructions
 // take an operand as 16 rows (lane % 16) by slots of the contracted index
@@ -399,6 +410,11 @@ enum Part : int { kState = 0, kOut = 1, kOutDots = 2 };
 // that differences of long sums stay exact to 2^-24 (a chunk may hold resets);
 // wave 0 does it a chunk ahead.
 //
+// Where the decays of a chunk add up to growth that the exps cannot hold, as they
+// may while the state is zero, the workgroup walks from there on token by token,
+// as the recurrence does (log decays of at most 0, the usual ones, never do; a
+// test of their signs is all they pay).
+//
 // With bf16 rows the products' operands are bf16: scores and the state as read
 // are rounded once (SP = 1), or kept to 16 bits (SP = 2; the gradient of the
 // decay sums differences of what they give).  The state itself is fp32: its
@@ -434,6 +450,10 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
   __shared__ __align__(16) Operand<T> sP[OUT ? SP * kScores * kWave : 1];
   // of the chunk's running sums b: rounded and rest; exp(b), exp(b_CT - b), exp(b_CT)
   __shared__ __align__(16) float sBh[2][CT], sBl[2][CT], sIn[2][CT], sEnd[2][CT], sAll[2];
+  // the log decays themselves (the state pass: their sums to the span's end), and
+  // whether the chunk is walked token by token
+  __shared__ float sG[2][CT];
+  __shared__ int sWalk[2];
   // where query tile q's scores with keys 32 t.. lie: 0 0 | 1 1 2 2 and on
   auto score_at = [](int s, int q, int t) { return (s * kScores + (q < 2 ? q : 2 * q - 2 + t)) * kWave; };
 
@@ -494,11 +514,14 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
   uint32_t gl = 0;    // the lane's log decay (all zeros: none)
   double all = 0.0;   // the state pass: sum of the log decays behind the chunk
   auto fetch_decays = [&](int64_t low) {
-    // backward, the decay stands behind the token
+    // backward, the decay stands behind the token; the state pass takes the last
+    // token's first
     const int64_t first = low + (REV ? 1 : 0);
-    const int row = REV ? CT - 1 - lane : lane, left = live - first < CT ? int(live - first) : CT;
+    int lane = tid & 63;
+    asm volatile("" : "+v"(lane));   // one wave's addresses, not to be held by all through the loop
+    const int row = REV == OUT ? CT - 1 - lane : lane, left = live - first < CT ? int(live - first) : CT;
     gl = 0;
-    if (row >= 0 && row < left) {
+    if (row >= 0 && row < left && lane < CT) {
       if constexpr (FAST) {
         const uint32_t es = p.g.bf16 ? 2 : 4, pitch = uint32_t(p.g.st) * es;
         const auto win = window(static_cast<const char*>(p.g.p) + (b * p.g.sb + first * p.g.st + h * p.g.sh) * es,
@@ -514,19 +537,34 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     }
   };
   auto sum_decays = [&](int buf) {
-    const double bs = wave_running_sum(log_decay_of(p.g, gl) * kLog2e), tot = last_lane(bs);
-    const float hi = float(bs);
-    if (lane < CT) {
-      if constexpr (OUT) {
+    int lane = tid & 63;
+    asm volatile("" : "+v"(lane));
+    const float g = log_decay_of(p.g, gl) * kLog2e;   // -inf and NaN stay what they are
+    bool walk;
+    if constexpr (OUT) {
+      const double bs = wave_running_sum(g < kMinLogDecay * kLog2e ? kMinLogDecay * kLog2e : g), tot = last_lane(bs);
+      const float hi = float(bs);
+      if (lane < CT) {
         sBh[buf][lane] = hi;
         sBl[buf][lane] = float(bs - hi);
         sIn[buf][lane] = exp2_fast(hi);
+        sEnd[buf][lane] = exp2_fast(float(tot - bs));   // to the chunk's end
+        sG[buf][lane] = g;
       }
-      // to the chunk's end; in the state pass to the span's
-      sEnd[buf][lane] = exp2_fast(float(OUT ? tot - bs : all + (tot - bs)));
+      if (lane == 0) sAll[buf] = exp2_fast(float(tot));
+      walk = __any(!(g <= 0.0f));
+      if (walk) walk = !(last_lane(wave_running_sum(g <= 0.0f ? 0.0f : g)) <= kMaxGrowth);
+    } else {
+      // from behind the lane's token to the span's end
+      const double bs = wave_running_sum(g), before = __shfl_up(bs, 1), at = all + (lane > 0 ? before : 0.0);
+      if (lane < CT) {
+        sEnd[buf][CT - 1 - lane] = exp2_fast(float(at));
+        sG[buf][CT - 1 - lane] = float(at);
+      }
+      walk = __any(lane < CT && !(at <= kMaxGrowth));
+      all += last_lane(bs);
     }
-    if (OUT && lane == 0) sAll[buf] = exp2_fast(float(tot));
-    if (!OUT) all += tot;
+    if (lane == 0) sWalk[buf] = walk;
   };
 
   // A chunk's rows out are held until the next chunk's rows go to LDS: loads and
@@ -559,18 +597,23 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     held_low = -1;
   };
 
+  auto write_zeros = [&](int64_t low) {
+    if constexpr (OUT) {
+      for (int i = tid; i < CT * NW; i += 64 * W) {
+        const int64_t t = low + i / NW;
+        const int n = n0 + i % NW;
+        if (t < p.L && n < p.N) st(po + t * ost + n, 0.0f);
+      }
+    }
+  };
+
   bool have = false;
-  for (int k = 0; k < chunks; ++k) {
+  int k = 0;
+  for (; k < chunks; ++k) {
     const int64_t low = lowest(k);
     const int buf = k & 1;
     if (low >= live) {   // no token: zeros
-      if constexpr (OUT) {
-        for (int i = tid; i < CT * NW; i += 64 * W) {
-          const int64_t t = low + i / NW;
-          const int n = n0 + i % NW;
-          if (t < p.L && n < p.N) st(po + t * ost + n, 0.0f);
-        }
-      }
+      write_zeros(low);
       have = false;
       continue;
     }
@@ -590,6 +633,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     if constexpr (HOLD) write_held();
     __syncthreads();
     have = k + 1 < chunks && lowest(k + 1) < live;
+    const int walk = sWalk[buf];   // the same for the whole workgroup
     if (have) {
       if (w == DW) {
         sum_decays(buf ^ 1);
@@ -597,6 +641,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
       }
       fetch(lowest(k + 1));
     }
+    if (__builtin_amdgcn_readfirstlane(walk)) break;
     const int rows = live - low < CT ? int(live - low) : CT;       // of the chunk, with tokens
     const int orows = p.L - low < CT ? int(p.L - low) : CT;        // with a place in out
 
@@ -769,30 +814,87 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
 
   if (SWAP) __syncthreads();
   write_held();
+
+  // token by token from the chunk that needs it to the span's end; a loop of its
+  // own, since what it holds would cost the usual one registers; the lane's place
+  // is hidden for the same reason
+  int lane2 = lane;
+  asm volatile("" : "+v"(lane2));
+  const int g2 = lane2 >> 4, r2 = lane2 & 15;
+  for (const int summed = have ? k + 2 : k + 1; k < chunks; ++k) {
+    const int64_t low = lowest(k);
+    const int buf = k & 1;
+    if (low >= live) {
+      write_zeros(low);
+      continue;
+    }
+    const int rows = live - low < CT ? int(live - low) : CT, orows = p.L - low < CT ? int(p.L - low) : CT;
+    const int n = nw + r2;   // the lane's column; its rows of S as ever
+    __syncthreads();
+    fetch(low);
+    if (w == DW && k >= summed) {
+      fetch_decays(low);
+      sum_decays(buf);
+    }
+    if constexpr (OUT) qa.template store<REV>(sA, kStride);
+    qb.template store<REV>(sB, kStride);
+    qc.template store<REV>(sC, kStrideC);
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < CT; ++i) {
+      const float f = exp2_half(sG[buf][i]), cv = ld(sC + i * kStrideC + w * 16 + r2);
+      float o = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int m = i * kStride + LD::m_of(mt, g2, e);
+          if constexpr (OUT) {
+            S[mt][e] = S[mt][e] * f * f + ld(sB + m) * cv;
+            o += S[mt][e] * ld(sA + m);
+          } else {
+            S[mt][e] += ld(sB + m) * cv * f * f;
+          }
+        }
+        asm volatile("" ::: "memory");   // a few reads at a time
+      }
+      if constexpr (OUT) {
+        o += __shfl_xor(o, 16);
+        o += __shfl_xor(o, 32);
+        const int row = REV ? CT - 1 - i : i;
+        if (g2 == 0 && row < orows && n < p.N) st(po + (low + row) * ost + n, row < rows ? o : 0.0f);
+        if constexpr (PART == kOutDots) {
+          float d = row < rows && n < p.N ? o * ld(px + (low + row) * p.x.st + n) : 0.0f;
+#pragma unroll
+          for (int x = 1; x < 16; x <<= 1) d += __shfl_xor(d, x);
+          if (lane2 == 0 && row < rows) dots[low + row] = d;
+        }
+      }
+    }
+  }
+
   float* dst = nullptr;
-  float f = 1.0f;
+  float f = 1.0f;   // the root of a last decay
   int64_t dm = p.N, dn = 1;
   if (!OUT) {
     dst = p.sum + (bh * p.spans + span) * p.M * p.N;
-    if (w == DW && lane == 0 && tile == 0) p.total[bh * p.spans + span] = exp2_fast(float(all));
+    if (w == DW && lane == 0 && tile == 0) p.total[bh * p.spans + span] = exp2_half(float(all));
   } else if (span == p.spans - 1 && p.s_last) {
     dst = p.s_last + bh * p.M * p.N;
     dm = p.sm;
     dn = p.sn;
     // going backward, the first token's own decay stands between G_0 and h0
-    if (REV && live > 0) f = exp2_fast(log_decay(p.g, b, 0, h) * kLog2e);
+    if (REV && live > 0) f = exp2_half(log_decay(p.g, b, 0, h) * kLog2e);
   }
   if (dst) {
-    int g2 = g;   // kept apart from the loads above: their conditions would be held through the loop
-    asm volatile("" : "+v"(g2));
-    const int n = nw + r;
+    const int n = nw + r2;
     float* col = dst + n * dn;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int m = LD::m_of(mt, g2, i);
-        if (m < p.M && n < p.N) col[m * dm] = S[mt][i] * f;
+        if (m < p.M && n < p.N) col[m * dm] = S[mt][i] * f * f;
       }
   }
 }
@@ -803,7 +905,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
 // of the chain at a time (the last ones again where fewer are left).
 struct JoinParams {
   float* sum;            // (B H, spans, M, N)
-  const float* total;    // (B H, spans)
+  const float* total;    // (B H, spans): roots of the decays
   const float* s0;       // or null
   int64_t sm, sn;        // strides of s0
   int32_t inner, N, spans;   // M x N
@@ -836,7 +938,7 @@ __global__ __launch_bounds__(256) void k_join_spans(JoinParams p) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (k + u <= last) {
-        run = run * f[u] + v[u];
+        run = run * f[u] * f[u] + v[u];
         v[u] = run;
       }
     // the state entering span k + u + 1: slot k + u of the carries, which start
@@ -898,7 +1000,10 @@ static __global__ __launch_bounds__(256) void k_decay_grad(DecayGradParams p) {
     flow = partial_dot(p.carry + (int64_t(bh) * p.spans + span) * p.inner,
                        p.rcarry + (int64_t(bh) * p.spans + (p.spans - 2 - span)) * p.inner, p.inner);
     const int64_t e = t_begin + p.span;   // the decay between the two
-    if (e < live) flow *= exp2_fast(log_decay(p.g, b, e, h) * kLog2e);
+    if (e < live) {
+      const double f = exp2_half(log_decay(p.g, b, e, h) * kLog2e);
+      flow *= f * f;
+    }
   } else if (p.s_last) {
     flow = partial_dot(p.s_last + int64_t(bh) * p.inner, p.dh_last + int64_t(bh) * p.inner, p.inner);
   }
@@ -1039,7 +1144,7 @@ __global__ __launch_bounds__(256) void k_attn_step(AttnStepParams p) {
     for (int i = 0; i < V; ++i) vv[i] = ld(v + n + i);
   }
   const Decay d{p.g, p.gs[0], 0, p.gs[1], p.g_bf16};
-  const float e = exp2_fast(log_decay(d, b, 0, h) * kLog2e);
+  const float f = exp2_half(log_decay(d, b, 0, h) * kLog2e);
   __syncthreads();
   fvec acc = fvec(0.0f);
   for (int m0 = 0; m0 < p.dk; m0 += RG * U) {
@@ -1048,7 +1153,7 @@ __global__ __launch_bounds__(256) void k_attn_step(AttnStepParams p) {
     for (int u = 0; u < U; ++u) {
       const int m = m0 + u * RG + rg;
       if (m < p.dk) {
-        s[u] = s[u] * e + sk[m] * vv;
+        s[u] = s[u] * f * f + sk[m] * vv;
         acc += s[u] * sq[m];
         if (on) __builtin_nontemporal_store(s[u], reinterpret_cast<fvec*>(S + int64_t(m) * p.dv));
       }

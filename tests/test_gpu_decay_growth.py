@@ -1,0 +1,115 @@
+"""Decay attention with log decays above 0: states that grow, and growth of a
+state that is zero, which the recurrence keeps zero however far the decays add
+up.  Against the 64-bit recurrence; the cases keep every result in float32's
+range."""
+import math
+
+import pytest
+import torch
+
+import mixer_ref as R
+import selective_state_space_83_amd as ssm
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def make(L, dtype, seed, B=1, H=2, Hk=1, dk=32, dv=48):
+    gen = torch.Generator().manual_seed(3000 + seed)
+    n = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    return {"q": n(B, L, Hk, dk), "k": n(B, L, Hk, dk) * dk ** -0.5, "v": n(B, L, H, dv), "dout": n(B, L, H, dv),
+            "g": -0.1 * torch.rand(B, L, H, generator=gen), "dtype": dtype}
+
+
+def put(t):
+    dt = t["dtype"]
+    return {n: x.to(dt).cuda() for n, x in t.items() if n != "dtype"}
+
+
+def check_forward(t, **kw):
+    u = put(t)
+    ref = R.attn(u["q"], u["k"], u["v"], u["g"])
+    assert all(bool((m < 1e38).all()) for _, m in ref.values())
+    o, h = ssm.decay_attn(u["q"], u["k"], u["v"], u["g"], **kw)
+    torch.cuda.synchronize()
+    R.check("o", o, ref["o"], t["dtype"] == BF16, norm=False)
+    R.check("h_last", h, ref["h_last"], False, norm=False)
+
+
+def check_gradients(t, **kw):
+    u = put(t)
+    ref = R.attn(u["q"], u["k"], u["v"], u["g"], dout=u["dout"])
+    assert all(bool((m < 1e38).all()) for _, m in ref.values())
+    got = ssm.decay_attn_bwd(u["q"], u["k"], u["v"], u["g"], u["dout"], **kw)
+    torch.cuda.synchronize()
+    for name in ("dq", "dk", "dv", "dh0", "dlog_decay"):
+        R.check(name, got[name], ref[name], t["dtype"] == BF16 and name != "dh0", norm=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_growth_of_a_zero_state(dtype):
+    """exp(100) overflows float32, but what it multiplies is zero."""
+    t = make(4, dtype, 1)
+    t["g"][:] = torch.tensor([50.0, 50.0, -60.0, -1.0])[None, :, None]
+    check_forward(t)
+    u = put(t)
+    h = torch.zeros(1, 2, 32, 48, device="cuda")
+    ref = R.attn(u["q"], u["k"], u["v"], u["g"])
+    for i in range(4):
+        o = ssm.decay_attn_step(h, u["q"][:, i], u["k"][:, i], u["v"][:, i], u["g"][:, i])
+        R.check("o", o, tuple(x[:, i] for x in ref["o"]), dtype == BF16, norm=False)
+    R.check("h", h, ref["h_last"], False, norm=False)
+
+
+def test_one_step_past_the_range():
+    """exp(100) alone: zero stays zero, and a small state comes back in range."""
+    t = put(make(1, F32, 2))
+    h = torch.zeros(1, 2, 32, 48, device="cuda")
+    h[0, 1] = 1e-30
+    g = torch.full((1, 2), 100.0, device="cuda")
+    o = ssm.decay_attn_step(h, t["q"][:, 0], t["k"][:, 0], t["v"][:, 0], g)
+    up = (t["k"][0, 0, 0][:, None].double() * t["v"][0, 0][:, None, :].double())
+    want = up + torch.tensor([0.0, 1e-30 * math.exp(100.0)], dtype=torch.float64, device="cuda")[:, None, None]
+    assert torch.allclose(h[0].double(), want, rtol=1e-5, atol=1e-6)
+    assert torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L", [130, 700])
+def test_growth_and_decay(dtype, L):
+    """A rise by exp(40) in half a chunk, and back: finite everywhere."""
+    t = make(L, dtype, 3 + L)
+    t["g"][:, 10:50] = 1.0
+    t["g"][:, 50:90] = -1.0
+    check_forward(t)
+    check_forward(t, span=64)
+    t["dout"] *= 1e-3
+    check_gradients(t)
+    check_gradients(t, span=64)
+
+
+@pytest.mark.parametrize("span", [0, 64, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_reset_then_growth(dtype, span):
+    """What a reset forgot stays forgotten, however much the decays grow after it:
+    within a chunk, and over several spans."""
+    for at, n, up in ((20, 25, 10.0), (70, 300, 0.7)):
+        t = make(500, dtype, 5 + at)
+        t["g"][:, at] = -math.inf
+        t["g"][:, at + 1:at + 1 + n] = up
+        t["k"][:, at:at + n + 1] = 0
+        check_forward(t, span=span)
+
+
+@pytest.mark.parametrize("span", [0, 64, 192])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_growth_between_nothing_and_nothing(dtype, span):
+    """Nothing is written before the growth ends and nothing is read after it
+    began, so no gradient passes it either."""
+    t = make(600, dtype, 7)
+    t["g"][:, 100:400] = 0.5
+    t["k"][:, :400] = 0
+    t["dout"][:, 100:] = 0
+    check_forward(t, span=span)
+    check_gradients(t, span=span)
