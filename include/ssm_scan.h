@@ -347,9 +347,12 @@ ssm_status_t ssm_scan_bwd(const ssm_scan_bwd_args_t* args, void* hip_stream);
  *            all sums.  With bf16 inputs the products of decayed scores with
  *            values run on operands rounded once to bf16; updates of the state
  *            keep 24 bits.
- *   Non-finite values of a token reach that token and later ones as the
- *            recurrence says, and may reach earlier tokens of the same block of
- *            64 (they share its matrix products); rows past a length reach none.
+ *   Non-finite values of a token reach what the recurrence takes them to: that
+ *            token and later ones, in gradients going backward that token and
+ *            earlier ones.  dlog_decay may take them further within a span.  A
+ *            head is walked token by token from such a token's block on, where
+ *            v (gradients: k, q or dout) holds them.  Rows past a length reach
+ *            none.
  *   Sizes    1 <= key_dim, value_dim <= 256; heads a multiple of key_heads.
  *            Empty problems are valid: with L == 0, h_last = h0, dh0 = dh_last.
  * ------------------------------------------------------------------------- */

@@ -331,6 +331,27 @@ struct Stage {
       }
     }
   }
+  // Whether one of the lane's values is an infinity or a NaN: its exponent, the
+  // bits below the sign, is then the largest there is.
+  __device__ __forceinline__ bool non_finite() const {
+    if constexpr (sizeof(T) == 2) {
+      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 top{0, 0};
+#pragma unroll
+      for (int k = 0; k < kCount; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[k][i] & 0x7fff7fffu));
+      return top[0] >= 0x7f80u || top[1] >= 0x7f80u;
+    } else {
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < kCount; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = v[k][i] << 1 > top ? v[k][i] << 1 : top;
+      return top >= 0xff000000u;
+    }
+  }
   // REV: the last row first
   template <bool REV>
   __device__ __forceinline__ void store(T* s, int stride) const {
@@ -413,7 +434,9 @@ enum Part : int { kState = 0, kOut = 1, kOutDots = 2 };
 // Where the decays of a chunk add up to growth that the exps cannot hold, as they
 // may while the state is zero, the workgroup walks from there on token by token,
 // as the recurrence does (log decays of at most 0, the usual ones, never do; a
-// test of their signs is all they pay).
+// test of their signs is all they pay).  So it does where a row of c holds an
+// infinity or a NaN, which the products would carry, times their zeros above the
+// diagonal, to the rows out before it.
 //
 // With bf16 rows the products' operands are bf16: scores and the state as read
 // are rounded once (SP = 1), or kept to 16 bits (SP = 2; the gradient of the
@@ -630,6 +653,7 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     qb.template store<REV>(sB, kStride);
     if constexpr (SWAP) write_held();   // out of c's place first
     qc.template store<REV>(sC, kStrideC);
+    if (OUT && __any(qc.non_finite())) sWalk[buf] = 1;
     if constexpr (HOLD) write_held();
     __syncthreads();
     have = k + 1 < chunks && lowest(k + 1) < live;
