@@ -349,8 +349,7 @@ ssm_status_t ssm_scan_bwd(const ssm_scan_bwd_args_t* args, void* hip_stream);
  *            keep 24 bits.
  *   Non-finite values of a token reach what the recurrence takes them to: that
  *            token and later ones, in gradients going backward that token and
- *            earlier ones.  dlog_decay may take them further within a span.  A
- *            head is walked token by token from such a token's block on, where
+ *            earlier ones.  A head is walked token by token from such a token's block on, where
  *            v (gradients: k, q or dout) holds them.  Rows past a length reach
  *            none.
  *   Sizes    1 <= key_dim, value_dim <= 256; heads a multiple of key_heads.
@@ -401,6 +400,8 @@ typedef struct {
  *   G_t = q_t dout_t^T + exp(log_decay_{t+1}) G_{t+1},
  *   dq_t = S_t dout_t, dk_t = G_t v_t, dv_t = G_t^T k_t,
  *   dlog_decay_t = exp(log_decay_t) <S_{t-1}, G_t>, dh0 = exp(log_decay_0) G_0;
+ * dlog_decay is formed from the terms that pass token t alone (0 at a reset).
+ * The workspace holds the state at every 64 tokens (fp32 rows: 32);
  * dq and dk are summed over the heads that share a key head, in a fixed
  * order.  All gradients are dense and overwritten. */
 typedef struct {

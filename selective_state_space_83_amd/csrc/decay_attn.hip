@@ -123,6 +123,10 @@ ssm_status_t check_step(const ssm_decay_attn_step_args_t* a, Sizes* z) {
 int64_t tile_width(int64_t N) { return N > 64 ? 128 : 64; }
 int64_t tiles_of(int64_t N) { return (N + tile_width(N) - 1) / tile_width(N); }
 
+// Tokens of a chunk.  fp32 takes 32: its products are the bound, and those of the
+// scores grow with the chunk.
+constexpr int chunk_tokens(int32_t dtype) { return dtype == SSM_BF16 ? 64 : 32; }
+
 // How the time axis is cut: `spans` spans of `span` tokens (a multiple of
 // kSpanAlign), each walked by workgroups of its own.
 struct Cut {
@@ -194,11 +198,12 @@ FwdPlan make_fwd_plan(const Sizes& z, int32_t span) {
 // Workspace of the backward pass.
 struct BwdPlan {
   Cut cut;
-  int64_t slices = 0;   // column slices of key_dim whose dots are kept apart
-  size_t off_carry = 0, off_rcarry = 0, off_total = 0, off_s = 0, off_u = 0, off_w = 0, off_heads = 0, total = 0;
+  int64_t slices = 0, tiles = 0;   // of 16 columns of key_dim, whose dots are kept apart, and of 16 rows of value_dim
+  size_t off_carry = 0, off_rcarry = 0, off_total = 0, off_u = 0, off_w = 0, off_kept = 0, off_flow = 0, off_heads = 0,
+         total = 0;
 };
 
-BwdPlan make_bwd_plan(const Sizes& z, int32_t span) {
+BwdPlan make_bwd_plan(const Sizes& z, int32_t span, int32_t dtype) {
   BwdPlan pl;
   if (z.tokens == 0 || z.H == 0) return pl;
   size_t off = 0;
@@ -209,16 +214,20 @@ BwdPlan make_bwd_plan(const Sizes& z, int32_t span) {
   };
   pl.cut = cut_time(z.L, z.B * z.H * tiles_of(z.dk), z.dk * z.dv, tile_width(z.dk) == 128 ? 0.7 : 0.6, 0.35 * 2 / 3,
                     2.0 / 3, span);
-  pl.slices = tile_width(z.dk) / 16 * tiles_of(z.dk);
+  pl.slices = (z.dk + 15) / 16;
+  pl.tiles = round_up(z.dv, 32) / 16;
+  const int64_t chunks = pl.cut.span * pl.cut.spans / chunk_tokens(dtype);
   const size_t th = size_t(z.tokens) * size_t(z.H);
-  const size_t dots = size_t(z.B * z.H) * size_t(pl.cut.span * pl.cut.spans) * size_t(pl.slices) * 4;
+  const size_t dots = size_t(z.B * z.H) * size_t(pl.cut.span * pl.cut.spans) *
+                      size_t(tile_width(z.dk) / 16 * tiles_of(z.dk)) * 4;
   const size_t spans = pl.cut.spans > 1 ? size_t(pl.cut.spans) : 0;
   pl.off_carry = take(size_t(z.state) * spans * 4);
   pl.off_rcarry = take(size_t(z.state) * spans * 4);
   pl.off_total = take(size_t(z.B * z.H) * spans * 4);
-  pl.off_s = take(size_t(z.state) * 4);
   pl.off_u = take(dots);
   pl.off_w = take(dots);
+  pl.off_kept = take(size_t(z.B * z.H) * size_t(chunks) * size_t(pl.slices * pl.tiles) * 1024);
+  pl.off_flow = take(size_t(z.B * z.H) * size_t(chunks) * size_t(pl.slices) * 4);
   const bool shared = z.H != z.Hk;
   pl.off_heads = take(shared ? th * size_t(z.dk) * 4 : 0);
   pl.total = off;
@@ -282,7 +291,7 @@ ssm_status_t check_bwd(const ssm_decay_attn_bwd_args_t* a, Sizes* z, BwdPlan* pl
   if (a->span < 0 || a->span % kSpanAlign != 0)
     return fail(SSM_ERR_UNSUPPORTED, "span must be a non-negative multiple of %lld", (long long)kSpanAlign);
   if (a->reserved != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved field must be 0");
-  *pl = make_bwd_plan(*z, a->span);
+  *pl = make_bwd_plan(*z, a->span, a->dtype);
   if (ssm_status_t st = check_grid(*z, pl->cut)) return st;
   if (z->B * z->H == 0) return SSM_OK;
   if (z->L > 0 && (!a->q || !a->k || !a->v || !a->log_decay || !a->dout || !a->dq || !a->dk ||
@@ -335,9 +344,7 @@ bool fast_rows(const Rows& r, int64_t n, size_t elem) {
 
 template <typename T, int MP, int W, int SP, typename OutT, Part PART, bool REV, bool FAST>
 ssm_status_t launch_mix(const MixParams& p, hipStream_t s) {
-  // fp32 takes chunks of 32 tokens: its products are the bound, and those of
-  // the scores grow with the chunk
-  constexpr int CT = sizeof(T) == 2 ? 64 : 32;
+  constexpr int CT = chunk_tokens(sizeof(T) == 2 ? SSM_BF16 : SSM_F32);
   hipLaunchKernelGGL((k_mix<T, MP, W, CT, sizeof(T) == 2 ? SP : 1, OutT, PART, REV, FAST>),
                      dim3(uint32_t(p.B * p.H * p.tiles * p.walked)), dim3(64 * W), 0, s, p);
   return launch_status("k_mix");
@@ -518,9 +525,12 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
     dq.carry = carry;
     dk.carry = dv.carry = rcarry;
   }
-  dq.s_last = a->dh_last ? reinterpret_cast<float*>(ws + pl.off_s) : nullptr;
   dq.dots = reinterpret_cast<float*>(ws + pl.off_u);
   dk.dots = reinterpret_cast<float*>(ws + pl.off_w);
+  dq.kept = dk.kept = reinterpret_cast<float*>(ws + pl.off_kept);
+  dk.flow = reinterpret_cast<float*>(ws + pl.off_flow);
+  dq.kept_slices = dk.kept_slices = int32_t(pl.slices);
+  dq.kept_tiles = dk.kept_tiles = int32_t(pl.tiles);
   dq.out = shared ? ws + pl.off_heads : a->dq;
   dk.out = shared ? ws + pl.off_heads : a->dk;
   if (ssm_status_t st = run_mix<T, 1, T, kOut, true>(dv, s)) return st;
@@ -535,24 +545,31 @@ ssm_status_t run_bwd(const ssm_decay_attn_bwd_args_t* a, const Sizes& z, const B
     if (ssm_status_t st = run_mix<T, 2, T, kOutDots, true>(dk, s)) return st;
   }
   DecayGradParams gp{};
-  gp.u = dq.dots;
-  gp.w = dk.dots;
-  gp.carry = carry;
-  gp.rcarry = rcarry;
-  gp.s_last = dq.s_last;
-  gp.dh_last = a->dh_last;
+  gp.q = q;
+  gp.k = k;
+  gp.v = v;
+  gp.dout = d;
   gp.g = p.g;
+  gp.reads = dq.dots;
+  gp.writes = dk.dots;
+  gp.flow = dk.flow;
   gp.lengths = a->lengths;
   gp.dg = a->dlog_decay;
   gp.B = z.B;
   gp.L = z.L;
   gp.H = z.H;
-  gp.inner = z.dk * z.dv;
-  gp.span = pl.cut.span;
-  gp.spans = int32_t(pl.cut.spans);
+  gp.padded = pl.cut.span * pl.cut.spans;
+  gp.dk = int32_t(z.dk);
+  gp.dv = int32_t(z.dv);
   gp.slices = int32_t(pl.slices);
   gp.bf16 = a->decay_dtype == SSM_BF16;
-  hipLaunchKernelGGL(k_decay_grad, dim3(uint32_t(z.B * z.H * gp.spans)), dim3(256), 0, s, gp);
+  constexpr int CT = chunk_tokens(sizeof(T) == 2 ? SSM_BF16 : SSM_F32);
+  const dim3 grid(uint32_t(std::min<int64_t>(z.B * z.H * (gp.padded / CT), kMaxGroups)));
+  if (fast_rows(q, z.dk, sizeof(T)) && fast_rows(k, z.dk, sizeof(T)) && fast_rows(v, z.dv, sizeof(T)) &&
+      fast_rows(d, z.dv, sizeof(T)))
+    hipLaunchKernelGGL((k_decay_grad<T, CT, true>), grid, dim3(256), 0, s, gp);
+  else
+    hipLaunchKernelGGL((k_decay_grad<T, CT, false>), grid, dim3(256), 0, s, gp);
   return launch_status("k_decay_grad");
 }
 
@@ -590,7 +607,7 @@ size_t ssm_decay_attn_bwd_workspace_size(const ssm_decay_attn_bwd_args_t* a) {
   if (!a || a->span < 0 || a->span % kSpanAlign != 0) return 0;
   Sizes z{a->batch, a->seqlen, a->heads, a->key_heads, a->key_dim, a->value_dim, 0, 0};
   if (check_sizes(&z)) return 0;
-  return make_bwd_plan(z, a->span).total;
+  return make_bwd_plan(z, a->span, a->dtype).total;
 }
 
 ssm_status_t ssm_decay_attn_fwd(const ssm_decay_attn_args_t* a, void* hip_stream) {

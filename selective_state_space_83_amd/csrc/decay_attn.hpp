@@ -20,12 +20,21 @@
 // pass forms each span's end state from zero, k_join_spans the states entering
 // the spans.
 //
-// The decay's gradient needs no state per token: dq_i.q_i and dk_i.k_i sum the
-// same pairs (i, j <= i) by reader and by writer, so with u_i = dq_i.q_i,
-// w_i = dk_i.k_i (per value head), any e > t, and P_e the gradient's flow
-// through the boundary before e, P_e = <S_{e-1}, exp(g_e) G_e> (at the
-// sequence's end <S_last, dh_last>),
-//   dg_t = sum_{t <= i < e} (u_i - w_i) + P_e.
+// The decay's gradient dg_t = exp(g_t) <S_{t-1}, G_t> is the sum over all pairs of
+// a token j < t that writes and one i >= t that reads.  Within a chunk, with S the
+// state entering it, G its gradient behind it and b_i as below,
+//
+//   dg_t =   sum_{j < t <= i} exp(b_i - b_j) (q_i . k_j) (v_j . dout_i)    both in it
+//          + sum_{i >= t} exp(b_i) q_i . (S dout_i)                        j before it
+//          + sum_{j < t} exp(b_end - b_j) k_j . (G v_j)                    i behind it
+//          + exp(b_end) <S, G>                                             neither.
+//
+// Every term is one that passes t, with its own decay: no sums cancel (as those of
+// dq_i . q_i - dk_i . k_i would, which also count the pairs that do not pass t),
+// a reset's gradient is 0, and other segments' sizes and non-finite values stay
+// theirs.  The passes for dq and dk leave the second and third terms as dots of
+// the state's part of their rows; the first also leaves the state entering each
+// chunk, for the other to take its product with G; k_decay_grad adds up the rest.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -92,7 +101,7 @@ __device__ __forceinline__ int64_t live_tokens(const int32_t* lengths, int64_t b
 }
 
 struct MixParams {
-  Rows a, b, c, x;       // x: rows like out, for the dots (dots null: unused)
+  Rows a, b, c, x;       // x: rows like out, for the dots
   Decay g;
   const int32_t* lengths;
   const float* s0;       // state before the first token, or null
@@ -103,7 +112,11 @@ struct MixParams {
   float* sum;            // (B, H, spans, M, N): a span's end state from zero (the state pass)
   float* total;          // (B, H, spans): the root of a span's decay, exp2_half (the state pass)
   void* out;             // (B, L, H, N)
-  float* dots;           // (slices of N, B, H, span x spans): out_t . x_t over a wave's slice
+  float* dots;           // (slices of N, B, H, span x spans): over a wave's slice, x_t . the state's part of out_t
+  float* kept;           // (B, H, chunks, slices, tiles of M, lanes, 4): the state entering a chunk as the waves hold
+                         // it; forward in time written, backward read
+  float* flow;           // (slices, B, H, chunks): <kept, S> (backward in time)
+  int32_t kept_slices, kept_tiles;   // those with columns below N, rows below M
   int64_t B, L, H, span; // span: tokens per span, a multiple of the chunk
   int32_t M, N, spans, tiles;
   int32_t walked;        // spans of this launch: all, or (the state pass) all but the last
@@ -413,8 +426,25 @@ __device__ __forceinline__ double last_lane(double v) {
   return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
 }
 
+// Sum over the 16 lanes of a row, in all of them; over the wave.
+template <int CTRL>
+__device__ __forceinline__ float add_lane(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v = add_lane<0xB1>(v);      // lane ^ 1
+  v = add_lane<0x4E>(v);      // lane ^ 2
+  v = add_lane<0x141>(v);     // mirrored within 8
+  return add_lane<0x140>(v);  // mirrored within 16
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row_sum(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
 // What a launch forms: only the state, from zero (the first pass over spans);
-// the rows out; the rows out and their dots with x.
+// the rows out; the rows out and what the decay's gradient takes from them.
 enum Part : int { kState = 0, kOut = 1, kOutDots = 2 };
 
 // ---------------------------------------------------------------------------
@@ -440,7 +470,7 @@ enum Part : int { kState = 0, kOut = 1, kOutDots = 2 };
 //
 // With bf16 rows the products' operands are bf16: scores and the state as read
 // are rounded once (SP = 1), or kept to 16 bits (SP = 2; the gradient of the
-// decay sums differences of what they give).  The state itself is fp32: its
+// decay, which may be fp32, is taken from them).  The state itself is fp32: its
 // update takes the decayed rows in three parts, 24 bits.
 // ---------------------------------------------------------------------------
 // Waves a SIMD is to hold: four (128 registers each) where that does not spill,
@@ -448,7 +478,7 @@ enum Part : int { kState = 0, kOut = 1, kOutDots = 2 };
 // parts of the scores and the state (SP = 2) do spill, and so do 128 rows of S
 // with fp32 operands: every reload from scratch also waits for the rows on their
 // way (two passes of 4 x 4096 x 20 heads x 128 x 128 with SP = 2: 200 us each
-// with four, 150 with two; 2048 x 256 heads x 128 x 128 fp32: 453 and 413 us).
+// with four, 150 with two, both without the states kept for the decay's gradient; 2048 x 256 heads x 128 x 128 fp32: 453 and 413 us).
 template <typename T, int MP, int SP>
 constexpr int waves_per_simd() {
   return SP == 1 && MP <= (sizeof(T) == 4 ? 64 : 128) ? 4 : 2;
@@ -630,6 +660,40 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     }
   };
 
+  // The state entering a chunk, kept for its product with the state of the pass
+  // the other way, which has the same tiles in the same lanes: KG tiles at a time.
+  constexpr int KG = MT < 8 ? MT : 8;
+  const int slice = tile * W + w;
+  auto kept_window = [&](int64_t low) {
+    const int64_t at = ((bh * p.spans * chunks + low / CT) * p.kept_slices + slice) * p.kept_tiles * 256;
+    return window(p.kept + at, slice < p.kept_slices, 0, p.kept_tiles * 1024);
+  };
+  auto write_kept = [&](int64_t low) {
+    const auto win = kept_window(low);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[mt]), win, (mt * 64 + lane) * 16, 0, 0);
+  };
+  auto read_kept = [&](f32x4(&to)[KG], int64_t low, int mt0) {
+    const auto win = kept_window(low);
+#pragma unroll
+    for (int mt = 0; mt < KG; ++mt)
+      to[mt] = __builtin_bit_cast(
+          f32x4, __builtin_amdgcn_raw_buffer_load_b128(win, ((mt0 + mt) * 64 + lane) * 16, 0, 0));
+  };
+  auto write_flow = [&](f32x4(&first)[KG], int64_t low) {
+    f32x4 sum{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int mt0 = 0; mt0 < MT; mt0 += KG) {
+      if (mt0 > 0) read_kept(first, low, mt0);
+#pragma unroll
+      for (int mt = 0; mt < KG; ++mt) sum += first[mt] * S[mt0 + mt];
+    }
+    const float d = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (lane == 0 && slice < p.kept_slices)
+      p.flow[(slice * p.B * p.H + bh) * p.spans * chunks + low / CT] = d;
+  };
+
   bool have = false;
   int k = 0;
   for (; k < chunks; ++k) {
@@ -657,25 +721,14 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     if constexpr (HOLD) write_held();
     __syncthreads();
     have = k + 1 < chunks && lowest(k + 1) < live;
-    const int walk = sWalk[buf];   // the same for the whole workgroup
-    if (have) {
-      if (w == DW) {
-        sum_decays(buf ^ 1);
-        if (k + 2 < chunks) fetch_decays(lowest(k + 2));
-      }
-      fetch(lowest(k + 1));
-    }
-    if (__builtin_amdgcn_readfirstlane(walk)) break;
-    const int rows = live - low < CT ? int(live - low) : CT;       // of the chunk, with tokens
-    const int orows = p.L - low < CT ? int(p.L - low) : CT;        // with a place in out
-
-    f32x4 acc[OUT ? QT : 1];
     u32x4 xr[PART == kOutDots ? QT : 1];
-    if constexpr (OUT) {
-      if constexpr (PART == kOutDots && FAST) {
+    f32x4 kept[PART == kOutDots && REV ? KG : 1];
+    // ahead of the next chunk's rows: waits are in order
+    if constexpr (PART == kOutDots) {
+      if constexpr (FAST) {
         // the rows the dots are taken with: the lane's query, its 4 columns
         const uint32_t pitch = uint32_t(p.x.st) * uint32_t(sizeof(T));
-        const int n = nw + 4 * g;
+        const int n = nw + 4 * g, rows = live - low < CT ? int(live - low) : CT;
         const uint32_t off =
             n < p.N ? uint32_t(REV ? 15 - r : r) * pitch + uint32_t(n) * uint32_t(sizeof(T)) : kOutside;
 #pragma unroll
@@ -690,6 +743,23 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
           }
         }
       }
+      if constexpr (REV) read_kept(kept, low, 0);
+    }
+    const int walk = sWalk[buf];   // the same for the whole workgroup
+    if (have) {
+      if (w == DW) {
+        sum_decays(buf ^ 1);
+        if (k + 2 < chunks) fetch_decays(lowest(k + 2));
+      }
+      fetch(lowest(k + 1));
+    }
+    if (__builtin_amdgcn_readfirstlane(walk)) break;
+    if constexpr (PART == kOutDots && !REV) write_kept(low);
+    const int rows = live - low < CT ? int(live - low) : CT;       // of the chunk, with tokens
+    const int orows = p.L - low < CT ? int(p.L - low) : CT;        // with a place in out
+
+    f32x4 acc[OUT ? QT : 1];
+    if constexpr (OUT) {
       // scores: the keys kt0.. of query tile qt that the wave takes
       constexpr int PER = CT == 32 ? 1 : W == 8 ? 2 : 4;   // key tiles of a wave
       const int qt = CT == 32 ? w & 1 : W == 8 ? w >> 1 : w;
@@ -747,6 +817,31 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
       }
 #pragma unroll
       for (int q = 0; q < QT; ++q) acc[q] *= sIn[buf][16 * q + r];
+      if constexpr (PART == kOutDots) {
+#pragma unroll
+        for (int q = 0; q < QT; ++q) {
+          const int row = (REV ? CT - 16 - 16 * q : 16 * q) + (REV ? 15 - r : r);
+          const int n = nw + 4 * g;
+          float d = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = 0.0f;
+            if constexpr (!FAST) {
+              if (row < rows && n + i < p.N) x = ld(px + (low + row) * p.x.st + n + i);
+            } else if constexpr (sizeof(T) == 4) {
+              x = __uint_as_float(xr[q][i]);
+            } else {
+              const uint32_t u = xr[q][i >> 1];
+              x = __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
+            }
+            d += acc[q][i] * x;
+          }
+          d += __shfl_xor(d, 16);
+          d += __shfl_xor(d, 32);
+          if (g == 0 && row < rows) dots[low + row] = d;
+        }
+        if constexpr (REV) write_flow(kept, low);
+      }
       __syncthreads();
     }
 
@@ -780,25 +875,6 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (n + i < p.N) st(po + (low + row) * ost + n + i, acc[q][i]);
-        }
-        if constexpr (PART == kOutDots) {
-          float d = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = 0.0f;
-            if constexpr (!FAST) {
-              if (on && n + i < p.N) x = ld(px + (low + row) * p.x.st + n + i);
-            } else if constexpr (sizeof(T) == 4) {
-              x = __uint_as_float(xr[q][i]);
-            } else {
-              const uint32_t u = xr[q][i >> 1];
-              x = __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
-            }
-            d += acc[q][i] * x;
-          }
-          d += __shfl_xor(d, 16);
-          d += __shfl_xor(d, 32);
-          if (g == 0 && on) dots[low + row] = d;
         }
       }
     }
@@ -864,6 +940,32 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
     qb.template store<REV>(sB, kStride);
     qc.template store<REV>(sC, kStrideC);
     __syncthreads();
+    if constexpr (PART == kOutDots) {
+      if constexpr (REV) {
+        f32x4 kept[KG];
+        read_kept(kept, low, 0);
+        write_flow(kept, low);
+      } else {
+        write_kept(low);
+      }
+      double sum = 0.0;   // of the log decays
+#pragma unroll 1
+      for (int i = 0; i < CT; ++i) {
+        float d = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d += S[mt][e] * ld(sA + i * kStride + LD::m_of(mt, g2, e));
+          asm volatile("" ::: "memory");
+        }
+        sum += sG[buf][i];
+        const float f = exp2_half(float(sum));
+        const int row = REV ? CT - 1 - i : i;
+        const bool on = row < rows;
+        d = wave_sum(on && n < p.N ? d * f * f * ld(px + (low + row) * p.x.st + n) : 0.0f);
+        if (lane2 == 0 && on) dots[low + row] = d;
+      }
+    }
 #pragma unroll 1
     for (int i = 0; i < CT; ++i) {
       const float f = exp2_half(sG[buf][i]), cv = ld(sC + i * kStrideC + w * 16 + r2);
@@ -887,12 +989,6 @@ __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(M
         o += __shfl_xor(o, 32);
         const int row = REV ? CT - 1 - i : i;
         if (g2 == 0 && row < orows && n < p.N) st(po + (low + row) * ost + n, row < rows ? o : 0.0f);
-        if constexpr (PART == kOutDots) {
-          float d = row < rows && n < p.N ? o * ld(px + (low + row) * p.x.st + n) : 0.0f;
-#pragma unroll
-          for (int x = 1; x < 16; x <<= 1) d += __shfl_xor(d, x);
-          if (lane2 == 0 && row < rows) dots[low + row] = d;
-        }
       }
     }
   }
@@ -974,117 +1070,168 @@ __global__ __launch_bounds__(256) void k_join_spans(JoinParams p) {
 }
 
 struct DecayGradParams {
-  const float* u;        // (slices, B, H, span x spans)
-  const float* w;        // the same
-  const float* carry;    // (B, H, spans, inner): slot k, the state entering span k + 1 (dq's layout)
-  const float* rcarry;   // same of their gradients, spans counted from the end
-  const float* s_last;   // (B, H, dk, dv), with dh_last; null: no flow through the end
-  const float* dh_last;
+  Rows q, k, v, dout;
   Decay g;
+  const float* reads;    // (slices, B, H, padded): exp(b_i) q_i . (S dout_i)
+  const float* writes;   // the same: exp(b_end - b_j) k_j . (G v_j), with the decay behind the chunk
+  const float* flow;     // (slices, B, H, padded / CT): <S, G>
   const int32_t* lengths;
   void* dg;              // (B, L, H)
-  int64_t B, L, H, inner, span;
-  int32_t slices, spans, bf16;
+  int64_t B, L, H, padded;
+  int32_t dk, dv, slices, bf16;
 };
 
-// A thread's share of a dot product, eight loads of each at a time.
-__device__ __forceinline__ double partial_dot(const float* a, const float* b, int64_t n) {
-  constexpr int U = 8;
-  double sum = 0.0;
-  int64_t i = threadIdx.x;
-  for (int64_t whole = n / (256 * U); whole > 0; --whole, i += 256 * U) {
-    float x[U], y[U];
+// The decay's gradient, a workgroup to a chunk of CT tokens of a head: the two
+// score matrices, a query tile to a wave, their product with the decays, its sums
+// over keys before and queries from each token, and the sums that the passes left.
+// Decays are summed without the resets, which are counted instead: what passes one
+// is 0 whatever grows.  Sums over tokens run forward or back from their own end, so
+// that no value reaches a token it does not pass.  Bound by the waits of a chunk's
+// few steps on each other: 4 x 4096 x 20 heads of 128 x 128 bf16 in 76 us (four
+// workgroups to a CU; 90 with three), 4 x 1024 x 24 of 64 x 64 fp32 in 33 us.
+template <typename T, int CT, bool FAST>
+__global__ __launch_bounds__(256, (FAST ? 4 : 3)) void k_decay_grad(DecayGradParams p) {
+  using LD = Lds<T>;
+  constexpr int QT = CT / 16, COLS = sizeof(T) == 2 ? 128 : 64, kStride = COLS + LD::kPad;
+  __shared__ __align__(16) T sQ[CT * kStride];
+  __shared__ __align__(16) T sK[CT * kStride];
+  __shared__ __align__(16) float sBh[CT], sBl[CT];
+  __shared__ __align__(16) int sResets[CT];
+  __shared__ float sPairs[QT][CT], sReads[CT], sWrites[CT], sFlow;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t chunks = p.padded / CT;
+  for (int64_t id = blockIdx.x; id < p.B * p.H * chunks; id += gridDim.x) {
+    const int64_t bh = id / chunks, b = bh / p.H, h = bh % p.H;
+    const int64_t low = id % chunks * CT, live = live_tokens(p.lengths, b, p.L);
+    if (low >= p.L) continue;
+    const int rows = live - low < CT ? int(live - low) : CT;   // with tokens; at most 0: none
+    const int orows = p.L - low < CT ? int(p.L - low) : CT;
+    float out = 0.0f;   // token tid's
+    if (rows > 0) {
+      const T* pq[2] = {row_base<T>(p.q, b, h), row_base<T>(p.dout, b, h)};
+      const T* pk[2] = {row_base<T>(p.k, b, h), row_base<T>(p.v, b, h)};
+      const int64_t sq[2] = {p.q.st, p.dout.st}, sk[2] = {p.k.st, p.v.st};
+      Stage<T, CT, COLS, 256, FAST> rq, rk;
+      const int width[2] = {p.dk, p.dv};
+      auto fetch = [&](int m, int c0) {
+        rq.load(pq[m], sq[m], low, live, c0, width[m]);
+        rk.load(pk[m], sk[m], low, live, c0, width[m]);
+      };
+      fetch(0, 0);
+      // what the passes left: a sum each to a wave
+      const int64_t n = p.B * p.H * p.padded, at = bh * p.padded + low;
+      if (w == 0) {
+        const float gr = lane < rows ? log_decay(p.g, b, low + lane, h) : 0.0f;
+        const float gn = low + CT < live ? log_decay(p.g, b, low + CT, h) : 0.0f;
+        const bool reset = gr < kMinLogDecay;
+        const uint64_t resets = __ballot(reset);
+        const double bs = wave_running_sum(reset ? 0.0f : gr * kLog2e), tot = last_lane(bs) + gn * kLog2e;
+        if (lane < CT) {
+          const float hi = float(bs);
+          sBh[lane] = hi;
+          sBl[lane] = float(bs - hi);
+          sResets[lane] = __popcll(resets & (2ull << lane) - 1);
+        }
+        // at most 16 slices: the first lanes
+        const float f = row_sum(lane < p.slices ? p.flow[(lane * p.B * p.H + bh) * chunks + low / CT] : 0.0f);
+        const float e = exp2_half(float(tot));
+        if (lane == 0) sFlow = resets || gn < kMinLogDecay ? 0.0f : f * e * e;
+      } else if (w < 3) {
+        // reads: of the lane's token and those behind it; writes: of those before it
+        const int t = w == 1 ? CT - 1 - lane : lane;
+        const float* from = (w == 1 ? p.reads : p.writes) + at + t;
+        float x = 0.0f;
+        if (t >= 0 && t < rows)
+          for (int k0 = 0; k0 < p.slices; k0 += 8) {   // eight reads in flight, the last again where fewer are left
+            float v[8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      x[u] = a[i + 256 * u];
-      y[u] = b[i + 256 * u];
-    }
+            for (int k = 0; k < 8; ++k) v[k] = from[(k0 + k < p.slices ? k0 + k : p.slices - 1) * n];
 #pragma unroll
-    for (int u = 0; u < U; ++u) sum += double(x[u]) * y[u];
-  }
-  for (; i < n; i += 256) sum += double(a[i]) * b[i];
-  return sum;
-}
-
-// dg over one span: the flow through its end, then suffix sums of u - w within
-// it.  A workgroup per span, eight tokens to a lane; sums in 64 bits.  Bound by the
-// latency of its few reads (80 heads of 128 x 128, 3 spans of 1408 tokens: 16 us).
-static __global__ __launch_bounds__(256) void k_decay_grad(DecayGradParams p) {
-  constexpr int E = 8, kBlock = 256 * E;
-  __shared__ double part[4];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int span = int(blockIdx.x % uint32_t(p.spans));
-  const uint32_t bh = blockIdx.x / uint32_t(p.spans);
-  const int64_t b = bh / uint32_t(p.H), h = bh % uint32_t(p.H);
-  const int64_t live = live_tokens(p.lengths, b, p.L), padded = p.span * p.spans, n = p.B * p.H * padded;
-  const int64_t t_begin = span * p.span, t_end = t_begin + p.span < p.L ? t_begin + p.span : p.L;
-
-  double flow = 0.0;
-  if (span + 1 < p.spans) {
-    flow = partial_dot(p.carry + (int64_t(bh) * p.spans + span) * p.inner,
-                       p.rcarry + (int64_t(bh) * p.spans + (p.spans - 2 - span)) * p.inner, p.inner);
-    const int64_t e = t_begin + p.span;   // the decay between the two
-    if (e < live) {
-      const double f = exp2_half(log_decay(p.g, b, e, h) * kLog2e);
-      flow *= f * f;
-    }
-  } else if (p.s_last) {
-    flow = partial_dot(p.s_last + int64_t(bh) * p.inner, p.dh_last + int64_t(bh) * p.inner, p.inner);
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) flow += __shfl_xor(flow, d);
-  if (lane == 0) part[w] = flow;
-  __syncthreads();
-  double run = part[0] + part[1] + part[2] + part[3];
-
-  for (int64_t base = t_begin + (t_end - 1 - t_begin) / kBlock * kBlock; base >= t_begin; base -= kBlock) {
-    const int64_t t = base + tid * E;
-    double v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = 0.0;
-    if (t < t_end && t < live) {
-      const float* u = p.u + int64_t(bh) * padded + t;   // spans, and so t, are multiples of eight
-      const float* o = p.w + int64_t(bh) * padded + t;
-      for (int k = 0; k < p.slices; k += 2) {   // an even number
-        f32x4 x[2][2], y[2][2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            x[j][q] = *reinterpret_cast<const f32x4*>(u + (k + j) * n + 4 * q);
-            y[j][q] = *reinterpret_cast<const f32x4*>(o + (k + j) * n + 4 * q);
+            for (int k = 0; k < 8; ++k) x += k0 + k < p.slices ? v[k] : 0.0f;
           }
+        const double sum = wave_running_sum(x), before = __shfl_up(sum, 1);
+        if (lane < CT) {
+          if (w == 1)
+            sReads[t] = float(sum);
+          else
+            sWrites[t] = lane > 0 ? float(before) : 0.0f;
+        }
+      }
+      f32x4 score[2][QT];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int m = 0; m < 2; ++m) {
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (t + e < live) v[e] += double(x[j][e >> 2][e & 3]) - double(y[j][e >> 2][e & 3]);
+        for (int kt = 0; kt < QT; ++kt) score[m][kt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int c0 = 0; c0 < width[m]; c0 += COLS) {
+          __syncthreads();
+          rq.template store<false>(sQ, kStride);
+          rk.template store<false>(sK, kStride);
+          __syncthreads();
+          if (c0 + COLS < width[m])
+            fetch(m, c0 + COLS);
+          else if (m == 0)
+            fetch(1, 0);
+          const int blocks = (width[m] - c0 < COLS ? width[m] - c0 + 31 : COLS) / 32;
+          if (w < QT)
+            for (int t = 0; t < blocks; ++t) {
+              const Operand<T> a = LD::along(sQ + (16 * w + r) * kStride, t, g);
+#pragma unroll
+              for (int kt = 0; kt < QT; ++kt)
+                if (kt <= w) score[m][kt] = mma(LD::along(sK + (16 * kt + r) * kStride, t, g), a, score[m][kt]);
+            }
+        }
+      }
+      if (w < QT) {
+        const int query = 16 * w + r;
+        const float qh = sBh[query], ql = sBl[query];
+        const int qr = sResets[query];
+        float run = 0.0f;   // of the tiles of keys before
+#pragma unroll
+        for (int kt = 0; kt < QT; ++kt) {
+          if (kt > w) continue;
+          float m[4], sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = 16 * kt + 4 * g + i;
+            const float f = exp2_half((qh - sBh[key]) + (ql - sBl[key]));
+            const float x = score[0][kt][i] * score[1][kt][i] * f * f;
+            m[i] = sum;   // of the lane's keys before
+            sum += key < query && query < rows && sResets[key] == qr ? x : 0.0f;
+          }
+          // of the lanes with keys before, then of all four
+          float ahead = sum;
+          float o = __shfl_up(ahead, 16);
+          ahead += g >= 1 ? o : 0.0f;
+          o = __shfl_up(ahead, 32);
+          ahead += g >= 2 ? o : 0.0f;
+          o = __shfl_up(ahead, 16);
+          const float all = __shfl(ahead, 48 + r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = 16 * kt + 4 * g + i;
+            const float x = row_sum(t <= query ? run + ((g >= 1 ? o : 0.0f) + m[i]) : 0.0f);
+            if (r == 0) sPairs[w][t] = x;
+          }
+          run += all;
+        }
+      }
+      __syncthreads();
+      if (tid < rows) {
+        out = sFlow + (sReads[tid] + sWrites[tid]);
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+          if (q >= tid >> 4) out += sPairs[q][tid];
       }
     }
-#pragma unroll
-    for (int e = E - 2; e >= 0; --e) v[e] += v[e + 1];
-    double behind = v[0];   // of the lanes from this one on, then of the later ones
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_down(behind, d);
-      if (lane + d < 64) behind += o;
-    }
-    __syncthreads();
-    if (lane == 0) part[w] = behind;
-    __syncthreads();
-    behind += run - v[0];
-    for (int k = w + 1; k < 4; ++k) behind += part[k];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (t + e >= t_end) continue;
-      const float out = t + e < live ? float(v[e] + behind) : 0.0f;
-      const int64_t i = (b * p.L + t + e) * p.H + h;
+    if (tid < orows) {
+      const int64_t i = (b * p.L + low + tid) * p.H + h;
       if (p.bf16)
         st(static_cast<bf16_t*>(p.dg) + i, out);
       else
         static_cast<float*>(p.dg)[i] = out;
     }
-    run += part[0] + part[1] + part[2] + part[3];
+    __syncthreads();   // the sums are read before the next chunk writes its own
   }
 }
 
