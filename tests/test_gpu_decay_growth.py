@@ -113,3 +113,41 @@ def test_growth_between_nothing_and_nothing(dtype, span):
     t["dout"][:, 100:] = 0
     check_forward(t, span=span)
     check_gradients(t, span=span)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dk,dv", [(1, 1), (17, 33), (130, 70), (64, 256), (256, 64), (256, 256)])
+def test_growth_at_other_widths(dk, dv, dtype):
+    """Narrow, odd and wide heads (odd ones are read element by element), forward
+    and with gradients, in one span and in several."""
+    t = make(200, dtype, 11 + dk, dk=dk, dv=dv)
+    t["g"][:, 60:90] = 1.0
+    t["g"][:, 90:120] = -1.0
+    t["dout"] *= 1e-3
+    for span in (0, 64):
+        check_forward(t, span=span)
+        check_gradients(t, span=span)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_growth_with_lengths(dtype):
+    """Rows that end in the growing chunk, before it and behind it; what lies past
+    a length grows by any amount."""
+    t = make(260, dtype, 13, B=4)
+    t["g"][:, 70:100] = 1.0
+    t["g"][:, 100:130] = -1.0
+    n = [260, 20, 85, 200]
+    for b, m in enumerate(n):
+        t["g"][b, m:] = 1e30
+        for name in ("q", "k", "v", "dout"):
+            t[name][b, m:] = float("nan")
+    t["dout"] *= 1e-3
+    u, lengths = put(t), torch.tensor(n, dtype=torch.int32, device="cuda")
+    ref = R.attn(u["q"], u["k"], u["v"], u["g"], lengths=lengths, dout=u["dout"])
+    for span in (0, 64):
+        o, h = ssm.decay_attn(u["q"], u["k"], u["v"], u["g"], lengths=lengths, span=span)
+        got = ssm.decay_attn_bwd(u["q"], u["k"], u["v"], u["g"], u["dout"], lengths=lengths, span=span)
+        torch.cuda.synchronize()
+        got.update(o=o, h_last=h)
+        for name in ("o", "h_last", "dq", "dk", "dv", "dh0", "dlog_decay"):
+            R.check(name, got[name], ref[name], dtype == BF16 and name not in ("h_last", "dh0"), norm=False)

@@ -193,3 +193,12 @@ def test_against_differences():
         # the loss is a sum of exponentials of g: the difference's error is e^2 / 6 of it
         want = (loss(up) - loss(down)) / (2 * e)
         assert abs(float(got[0, i, 0]) - want) <= (2 * R.EPS32 + e * e) * float(mag[0, i, 0]) + 1e-7
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dk,dv", [(1, 1), (17, 33), (130, 70), (256, 256)])
+def test_growth_at_other_widths(dk, dv, dtype):
+    t = make(1, 200, 2, 1, dk, dv, dtype, seed=37 + dk)
+    t["g"][:, 70:110] = 1.0
+    t["g"][:, 110:150] = -1.0
+    check(t, span=64)
