@@ -345,8 +345,11 @@ ssm_status_t ssm_scan_bwd(const ssm_scan_bwd_args_t* args, void* hip_stream);
  *   Dtypes   q, k, v, o, dout, dq, dk, dv share dtype; log_decay and dlog_decay
  *            have decay_dtype; states and their gradients are fp32, and so are
  *            all sums.  With bf16 inputs the products of decayed scores with
- *            values run on operands rounded once to bf16; updates of the state
- *            keep 24 bits.
+ *            values, and of the state as it is read with q, run on operands
+ *            rounded once to bf16 (in dq and dk kept to 16 bits): o has 1.4 times
+ *            the error of its own rounding, where the single-token form, which
+ *            reads the state in full, has once.  Updates of the state keep 24
+ *            bits.
  *   Non-finite values of a token reach what the recurrence takes them to: that
  *            token and later ones, in gradients going backward that token and
  *            earlier ones.  A head is walked token by token from such a token's block on, where

@@ -143,11 +143,16 @@ int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // pass over all but the last (`state`, its share of a step), two launches (two
 // steps), and reading and writing the spans' states (32 MB a step); the backward's
 // three passes share two such first passes and joins (two thirds of a pass's).
+// The shares are counted from the chunk's products and bytes, one for both types.
 // Measured, us by number of spans, the plan's marked: 80 walkers of 128 chunks,
 // 128 x 128 bf16: 3 298, *6 246, 12 285, 24 325; 4 walkers of 2048 chunks: 64
 // 223, *128 192, 256 231; 320 walkers of 32 chunks: *1 214, 2 259, 3 265; 192
 // walkers of 32 chunks, 64 x 64 fp32: 1 181, 3 170, *4 143, 8 151; bf16 85, 74,
-// *67, 77.
+// *67, 77.  Backward, all its launches: 80 walkers of 64 chunks, 128 x 128 bf16: 1
+// 1322, 3 723, 4 856, 5 795, *6 728, 11 832, 16 834; 320 walkers of 32 chunks: 1
+// 1372, 2 1298, 3 1310, *4 1325, 8 1542; 8 walkers of 256 chunks, 64 x 64: 8 431, 32
+// 169, *64 149; 96 walkers of 16 chunks, 64 x 64 fp32: 1 373, 2 276, 4 227, *8 189,
+// 16 215; 192 walkers of 32 chunks: 1 822, 3 706, *4 624, 8 661, 16 687.
 Cut cut_time(int64_t L, int64_t walkers, int64_t inner, double slope, double state, double join, int32_t span) {
   constexpr int64_t kCus = 256, kMaxSpans = 1024;
   Cut c;

@@ -478,17 +478,19 @@ enum Part : int { kState = 0, kOut = 1, kOutDots = 2 };
 // parts of the scores and the state (SP = 2) do spill, and so do 128 rows of S
 // with fp32 operands: every reload from scratch also waits for the rows on their
 // way (two passes of 4 x 4096 x 20 heads x 128 x 128 with SP = 2: 200 us each
-// with four, 150 with two, both without the states kept for the decay's gradient; 2048 x 256 heads x 128 x 128 fp32: 453 and 413 us).
+// with four, 150 with two, both without the states kept for the decay's gradient;
+// 2048 x 256 heads x 128 x 128 fp32: 453 and 413 us).
 template <typename T, int MP, int SP>
 constexpr int waves_per_simd() {
   return SP == 1 && MP <= (sizeof(T) == 4 ? 64 : 128) ? 4 : 2;
 }
 
-// Measured (one walk over 2048 tokens a head): 512 heads of 128 x 128 bf16 290 us
-// (3.7 TB/s), 512 of 64 x 64 bf16 131 us (4.1 TB/s), 512 of 64 x 64 fp32 305 us.
-// bf16 is near memory's rate once two workgroups share a CU, alone on a CU (169 to
-// 185 us for 256 heads) it is bound by a chunk's steps waiting on each other; fp32
-// by its matrix products, half of their rate.
+// Measured (one walk over 2048 tokens a head, calls back to back): 512 heads of
+// 128 x 128 bf16 288 us (3.7 TB/s), 512 of 64 x 64 bf16 127 us (4.2 TB/s), 512 of
+// 64 x 64 fp32 316 us.  bf16 is bound by a chunk's steps waiting on each other and
+// on memory (waves wait 48% of the time, the matrix units are busy 29%), more so
+// alone on a CU (176 to 184 us for 256 heads); fp32 by its matrix products, which
+// are busy half of the time.
 template <typename T, int MP, int W, int CT, int SP, typename OutT, Part PART, bool REV, bool FAST>
 __global__ __launch_bounds__(64 * W, (waves_per_simd<T, MP, SP>())) void k_mix(MixParams p) {
   using LD = Lds<T>;
@@ -1237,8 +1239,8 @@ __global__ __launch_bounds__(256, (FAST ? 4 : 3)) void k_decay_grad(DecayGradPar
 
 // Sum over the value heads of a key head: (rows, heads, n) fp32 to (rows, key
 // heads, n), in the heads' order.  V = 4 where n is a multiple of it.  Bound by
-// memory (16384 tokens, 20 heads to 4, n = 128: 27 us, 7 TB/s, partly from the
-// caches that the pass before it filled).
+// memory (16384 tokens, 20 heads to 4, n = 128: 31 to 41 us, 4.9 to 6.5 TB/s,
+// partly from the caches that the pass before it filled).
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_sum_heads(T* out, const float* in, int64_t total, int32_t n, int32_t per) {
   typedef float fvec __attribute__((ext_vector_type(V)));
