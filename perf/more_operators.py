@@ -1,0 +1,598 @@
+"""The operators of a selective-scan layer for sequences of unequal lengths, measured case by case: the scan and the
+short causal convolution over packed sequences whose states lie in slots of a cache, both for one token per sequence
+and with their gradients, and the residual's addition with the root-mean-square norm, to 16, 32 or 8 bits.
+
+With ``own`` false, ``run`` computes a case in its plain form, elementary torch operations in float32 rounded once
+at the end; with ``own`` true it makes the library's calls on the same inputs.
+
+    packed scan   h_t = exp(delta_t A) h_{t-1} + Bbar_t x_t,  y_t = (sum_n C_t h_t + D x_t) silu(z_t)
+    short conv    y_t = act(bias + sum_k w_k x_{t-K+1+k})       both never look past their sequence's first token
+    add + norm    s = x + residual,  y = s / sqrt(mean(s^2) + eps) w,  or e4m3 values of y / scale with their scales
+
+Shapes: x, delta, z, y (tokens, dim); B, C (tokens, N); sequence s holds tokens offsets[s] to offsets[s + 1] - 1; states
+(slots, dim, N) and windows (slots, channels, K - 1), the one of sequence s at slots[s], taken up where resume[s].
+"""
+import math
+
+import torch
+
+own = False
+
+EPS = 1e-5
+E4M3 = torch.float8_e4m3fn
+E4M3_MAX = 448.0
+
+
+# ---------------------------------------------------------------------------
+# cases
+# ---------------------------------------------------------------------------
+
+def _scan(kind, tokens, seqs, dim, N, dtype, zoh=False, fused=False, states=False, sliced=False):
+    return {"kind": kind, "tokens": tokens, "seqs": seqs, "dim": dim, "N": N, "dtype": dtype, "zoh": zoh,
+            "fused": fused, "states": states, "sliced": sliced}
+
+
+def _conv(kind, tokens, seqs, channels, K, dtype, act="silu", states=False, sliced=False):
+    return {"kind": kind, "tokens": tokens, "seqs": seqs, "channels": channels, "K": K, "dtype": dtype, "act": act,
+            "states": states, "sliced": sliced}
+
+
+def _norm(kind, rows, channels, dtype, residual, out="same", block=0):
+    """residual: "none", "same" (x's type) or "f32"; out: "same" or "e4m3", with a scale per `block` channels (0: per row)."""
+    return {"kind": kind, "rows": rows, "channels": channels, "dtype": dtype, "residual": residual, "out": out,
+            "block": block}
+
+
+def listed():
+    """Widths are the repository's workloads' (32, 512, 1536, 2560, 5120 channels, 16 states, 4 taps)."""
+    named = [
+        # the tiny workload's width, a few short prompts of a small model: latency counts
+        ("scan tiny", _scan("scan", 128, 3, 32, 16, "f32")),
+        # a serving engine's prefill: prompts of unequal lengths, half of them continued, step size and gate fused
+        ("scan prompts", _scan("scan", 16384, 48, 2560, 16, "bf16", fused=True, states=True, sliced=True)),
+        # two long documents on the long workload's width
+        ("scan long", _scan("scan", 131072, 2, 512, 16, "bf16", zoh=True)),
+        # one token for each of the decode workload's sequences, states wherever their slots lie
+        ("scan step", _scan("scan_step", 256, 256, 5120, 16, "bf16", fused=True, states=True, sliced=True)),
+        # documents packed into a training batch of the fp32 workload's size
+        ("scan train", _scan("scan_train", 16384, 20, 1536, 16, "f32", states=True)),
+        # the convolution in front of the prompts, on a slice of the layer's first projection
+        ("conv prompts", _conv("conv", 32768, 48, 2560, 4, "bf16", states=True, sliced=True)),
+        # its single token
+        ("conv step", _conv("conv_step", 256, 256, 5120, 4, "bf16", states=True, sliced=True)),
+        # its training step
+        ("conv train", _conv("conv_train", 16384, 20, 1536, 4, "f32")),
+        # the norm of a serving step: 256 tokens, 8-bit rows for the next projection
+        ("norm step", _norm("norm", 256, 2560, "bf16", "same", "e4m3")),
+        # the norm over the large prompt batch, a scale for each 128 channels
+        ("norm prompts 8 bit", _norm("norm", 32768, 2560, "bf16", "f32", "e4m3", 128)),
+        # the same to bf16
+        ("norm prompts", _norm("norm", 32768, 2560, "bf16", "same")),
+        # the norm in a training step, forward and backward, the residual stream in float32
+        ("norm train", _norm("norm_train", 16384, 1536, "bf16", "f32")),
+    ]
+    return [dict(case, name=name) for name, case in named]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.5)))))))
+
+
+def draw(rng):
+    """One more case of the listed ones' ranges."""
+    kind = rng.choice(["scan", "scan", "scan_step", "scan_train", "conv", "conv_step", "conv_train", "norm", "norm",
+                       "norm_train"])
+    dtype = rng.choice(["f32", "bf16"])
+    flip = lambda: rng.random() < 0.5  # noqa: E731
+    width = rng.choice([_log_int(rng, 8, 5120), 64 * rng.randrange(1, 81), 8 * rng.randrange(1, 321)])
+    if kind.startswith("norm"):
+        width = rng.choice([width, _log_int(rng, 16, 16384)])
+        most = (24 << 20) if kind == "norm_train" else (64 << 20)
+        rows = _log_int(rng, 1, max(1, min(32768, most // width)))
+        out = rng.choice(["same", "e4m3"]) if kind == "norm" else "same"
+        return _norm(kind, rows, width, dtype, rng.choice(["none", "same", "f32"]), out,
+                     rng.choice([0, 32, 64, 128, 256]) if out == "e4m3" else 0)
+    if kind.endswith("step"):
+        tokens = _log_int(rng, 1, max(1, min(256, (1280 << 10) // width)))
+        if kind == "conv_step":
+            return _conv(kind, tokens, tokens, width, rng.choice([2, 3, 4]), dtype, rng.choice(["silu", "none"]), True,
+                         flip())
+        return _scan(kind, tokens, tokens, width, rng.choice([1, 2, 4, 8, 16]), dtype, flip(), flip(), True, flip())
+    if kind.startswith("conv"):
+        tokens = _log_int(rng, 1, max(1, min(32768, ((24 if kind == "conv_train" else 64) << 20) // width)))
+        return _conv(kind, tokens, _log_int(rng, 1, min(256, tokens)), width, rng.choice([2, 3, 4, 4]), dtype,
+                     rng.choice(["silu", "none"]), kind == "conv" and flip(), flip())
+    N = rng.choice([1, 2, 4, 8, 16, 16])
+    tokens = _log_int(rng, 1, max(1, min(131072 if kind == "scan" else 16384,
+                                         ((16 if kind == "scan_train" else 32) << 20) // width)))
+    return _scan(kind, tokens, _log_int(rng, 1, min(256, tokens)), width, N, dtype, flip(), kind == "scan" and flip(),
+                 flip(), flip())
+
+
+# ---------------------------------------------------------------------------
+# inputs
+# ---------------------------------------------------------------------------
+
+def _dtype(case):
+    return torch.bfloat16 if case["dtype"] == "bf16" else torch.float32
+
+
+class _Random:
+    def __init__(self, seed):
+        self.gen = torch.Generator(device="cuda").manual_seed(int(seed))
+
+    def normal(self, *shape):
+        return torch.randn(*shape, generator=self.gen, device="cuda", dtype=torch.float32)
+
+    def uniform(self, *shape):
+        return torch.rand(*shape, generator=self.gen, device="cuda", dtype=torch.float32)
+
+    def order(self, n):
+        return torch.randperm(n, generator=self.gen, device="cuda").to(torch.int32)
+
+
+def _sequences(s, rng, tokens, seqs):
+    """Offsets at random cuts, one sequence without tokens among four or more; slots in any order; half resumed."""
+    cuts = (rng.uniform(seqs - 1) * (tokens + 1)).to(torch.int32).clamp_(0, tokens).sort().values
+    if seqs >= 4:
+        cuts[seqs // 2] = cuts[seqs // 2 - 1]
+    ends = torch.tensor([0, tokens], dtype=torch.int32, device="cuda")
+    s["offsets"] = torch.cat([ends[:1], cuts, ends[1:]])
+    s["slots"] = rng.order(seqs + 8)[:seqs].contiguous()
+    s["resume"] = rng.uniform(seqs) < 0.5
+
+
+def prepare(case, seed):
+    rng, dt = _Random(seed), _dtype(case)
+    s = {"case": case}
+    if case["kind"].startswith("norm"):
+        rows, channels = case["rows"], case["channels"]
+        s["x"] = (rng.normal(rows, channels) * (0.5 + rng.uniform(rows, 1))).to(dt)
+        s["residual"] = None
+        if case["residual"] != "none":
+            s["residual"] = (2 * rng.normal(rows, channels)).to(torch.float32 if case["residual"] == "f32" else dt)
+        s["weight"] = 1 + 0.1 * rng.normal(channels)
+        if case["kind"] == "norm_train":
+            s["dy"] = rng.normal(rows, channels).to(dt)
+            wide = torch.float32 if case["residual"] == "f32" else dt
+            s["dsum"] = None if case["residual"] == "none" else rng.normal(rows, channels).to(wide)
+        return s
+    T, S = case["tokens"], case["seqs"]
+    _sequences(s, rng, T, S)
+    if case["kind"].startswith("conv"):
+        C, K = case["channels"], case["K"]
+        # sliced: the first half of a projection's rows
+        s["x"] = rng.normal(T, 2 * C).to(dt)[:, :C] if case["sliced"] else rng.normal(T, C).to(dt)
+        s["weight"], s["bias"] = rng.normal(C, K) * K ** -0.5, 0.1 * rng.normal(C)
+        s["state"] = rng.normal(S + 8, C, K - 1) if case["states"] else None
+        if case["kind"] == "conv_train":
+            s["dy"] = rng.normal(T, C).to(dt)
+        return s
+    D, N = case["dim"], case["N"]
+    s["x"] = rng.normal(T, D).to(dt)
+    # step sizes log-uniform in [1e-3, 0.1]
+    step = torch.exp(math.log(1e-3) + math.log(100.0) * rng.uniform(1 if case["fused"] else T, D))
+    s["delta_bias"] = torch.log(torch.expm1(step[0])).contiguous() if case["fused"] else None
+    s["delta"] = (0.5 * rng.normal(T, D)).to(dt) if case["fused"] else step.to(dt)
+    s["z"] = None
+    if case["fused"]:
+        s["z"] = rng.normal(T, 2 * D).to(dt)[:, D:] if case["sliced"] else rng.normal(T, D).to(dt)
+    if case["sliced"]:
+        # one projection of the scan's input: the low-rank step size, B and C side by side
+        rank = -(-D // 16)
+        row = rng.normal(T, rank + 2 * N).to(dt)
+        s["B"], s["C"] = row[:, rank:rank + N], row[:, rank + N:]
+    else:
+        s["B"], s["C"] = rng.normal(T, N).to(dt), rng.normal(T, N).to(dt)
+    s["A"] = -torch.arange(1, N + 1, device="cuda", dtype=torch.float32).expand(D, N) * (0.9 + 0.2 * rng.uniform(D, N))
+    s["D"] = 1 + 0.1 * rng.normal(D)
+    train = case["kind"] == "scan_train"
+    s["h"] = rng.normal(S if train else S + 8, D, N) if case["states"] else None
+    if train:
+        s["dy"] = rng.normal(T, D).to(dt)
+        s["dh_last"] = rng.normal(S, D, N) if case["states"] else None
+    return s
+
+
+# ---------------------------------------------------------------------------
+# plain forms
+# ---------------------------------------------------------------------------
+
+def _up(t):
+    return None if t is None else t.float()
+
+
+def _silu(t):
+    return t * torch.sigmoid(t)
+
+
+def _leaf(t):
+    return None if t is None else t.detach().float().clone().requires_grad_(True)
+
+
+def _of_token(offsets, T):
+    """The sequence of every token, and whether the token is its first."""
+    at = torch.arange(T, device=offsets.device, dtype=torch.int32)
+    seq = torch.searchsorted(offsets[1:].contiguous(), at, right=True)
+    return seq, at == offsets[seq], at - offsets[seq]
+
+
+def _recurrence(a, b):
+    """h_t = a_t h_{t-1} + b_t from a zero state, neighbours paired and the halves solved first."""
+    n = a.shape[0]
+    if n == 1:
+        return b
+    if n % 2:
+        head = _recurrence(a[:-1], b[:-1])
+        return torch.cat([head, torch.addcmul(b[-1:], a[-1:], head[-1:])])
+    odd = _recurrence(a[1::2] * a[0::2], torch.addcmul(b[1::2], a[1::2], b[0::2]))
+    before = torch.cat([torch.zeros_like(odd[:1]), odd[:-1]])
+    return torch.stack([torch.addcmul(b[0::2], a[0::2], before), odd], 1).flatten(0, 1)
+
+
+def _input_factor(z, A, delta, zoh):
+    # in 64 bits: the derivative by A is a difference of nearly equal numbers where z is small
+    return (torch.expm1(z.double()) / A.double()).float() if zoh else delta.unsqueeze(-1)
+
+
+def _plain_scan(x, delta, A, B, C, D, h0, offsets, zoh):
+    """h0: one state per sequence, or None.  Returns y without the gate and the state after every sequence."""
+    T = x.shape[0]
+    _, first, _ = _of_token(offsets, T)
+    z = delta.unsqueeze(-1) * A
+    a = torch.exp(z)
+    b = _input_factor(z, A, delta, zoh) * B.unsqueeze(1) * x.unsqueeze(-1)
+    some = (offsets[1:] > offsets[:-1])[:, None, None]
+    if h0 is not None:
+        at = offsets[:-1].long().clamp(max=T - 1)
+        b = b.index_add(0, at, torch.where(some, a[at] * h0, 0.0))
+    h = _recurrence(a.masked_fill(first[:, None, None], 0.0), b)
+    y = (h * C.unsqueeze(1)).sum(-1) + D * x
+    before = torch.zeros_like(h[:1]) if h0 is None else h0
+    return y, torch.where(some, h[(offsets[1:].long() - 1).clamp(min=0)], before)
+
+
+def _plain_step(s):
+    case, slots = s["case"], s["slots"].long()
+    x, delta, z = _up(s["x"]), _up(s["delta"]), _up(s["z"])
+    if case["fused"]:
+        delta = torch.log1p(torch.exp(delta + s["delta_bias"]))
+    e = delta.unsqueeze(-1) * s["A"]
+    h = s["h"][slots] * torch.exp(e) + _input_factor(e, s["A"], delta, case["zoh"]) * _up(s["B"]).unsqueeze(1) * x.unsqueeze(-1)
+    s["h"][slots] = h
+    y = (h * _up(s["C"]).unsqueeze(1)).sum(-1) + s["D"] * x
+    return (y if z is None else y * _silu(z)).to(_dtype(case)), s["h"]
+
+
+def _window(state, slots, resume):
+    return torch.where(resume[:, None, None], state[slots.long()], 0.0)
+
+
+def _plain_conv(x, weight, bias, window, offsets, act):
+    """window: the inputs before each sequence (seqs, channels, K - 1), or None."""
+    T, K = x.shape[0], weight.shape[1]
+    seq, _, rank = _of_token(offsets, T)
+    back = torch.arange(K - 1, -1, -1, device=x.device)
+    at = torch.arange(T, device=x.device)[:, None] - back            # the token each tap reads
+    inside = rank[:, None] >= back
+    taps = torch.where(inside.unsqueeze(-1), x[at.clamp(min=0)], 0.0)
+    if window is not None:
+        early = window.transpose(1, 2)[seq[:, None], (rank[:, None] + K - 1 - back).clamp(max=K - 2)]
+        taps = torch.where(inside.unsqueeze(-1), taps, early)
+    y = (taps * weight.t()).sum(1) + bias
+    return _silu(y) if act == "silu" else y
+
+
+def _moved_window(x, window, offsets):
+    """The last K - 1 inputs of each sequence, reaching into its window."""
+    S, C, W = window.shape
+    length = (offsets[1:] - offsets[:-1]).long()
+    j = length[:, None] - W + torch.arange(W, device=x.device)       # within the sequence; below 0: of the window
+    new = x[(offsets[:-1, None] + j).clamp(0, x.shape[0] - 1)].transpose(1, 2)
+    old = window.gather(2, (j + W).clamp(0, W - 1)[:, None].expand(S, C, W))
+    return torch.where((j >= 0)[:, None], new, old)
+
+
+def _plain_norm(x, residual, weight):
+    s = x if residual is None else x + residual
+    return s * torch.rsqrt((s * s).mean(-1, keepdim=True) + EPS) * weight, s
+
+
+def _to_8_bits(y, block):
+    """e4m3 values and their scales: the largest magnitude of a row, or of a block of it, becomes 448."""
+    rows, channels = y.shape
+    block = block or channels
+    pad = -channels % block
+    cut = torch.cat([y, y.new_zeros(rows, pad)], 1).view(rows, -1, block) if pad else y.view(rows, -1, block)
+    top = cut.abs().amax(-1, keepdim=True)
+    scale = torch.where(top > 0, top / E4M3_MAX, 1.0)
+    q = (cut / scale).clamp(-E4M3_MAX, E4M3_MAX).view(rows, -1)[:, :channels]
+    return q, scale.squeeze(-1)
+
+
+def _run_plain(s):
+    case, dt, kind = s["case"], _dtype(s["case"]), s["case"]["kind"]
+    if kind == "scan":
+        delta = _up(s["delta"])
+        if case["fused"]:
+            delta = torch.log1p(torch.exp(delta + s["delta_bias"]))
+        h0 = None if s["h"] is None else _window(s["h"], s["slots"], s["resume"])
+        y, h = _plain_scan(_up(s["x"]), delta, s["A"], _up(s["B"]), _up(s["C"]), s["D"], h0, s["offsets"], case["zoh"])
+        y = (y if s["z"] is None else y * _silu(_up(s["z"]))).to(dt)
+        if s["h"] is None:
+            return y
+        s["h"][s["slots"].long()] = h
+        return y, s["h"]
+    if kind == "scan_step":
+        return _plain_step(s)
+    if kind == "conv_step" or kind == "conv":
+        # one token per sequence: sequences of one token, all resumed
+        step = kind == "conv_step"
+        offsets = torch.arange(case["tokens"] + 1, device="cuda", dtype=torch.int32) if step else s["offsets"]
+        resume = torch.ones_like(s["resume"]) if step else s["resume"]
+        window = None if s["state"] is None else _window(s["state"], s["slots"], resume)
+        x = _up(s["x"])
+        y = _plain_conv(x, s["weight"], s["bias"], window, offsets, case["act"]).to(dt)
+        if window is None:
+            return y
+        s["state"][s["slots"].long()] = _moved_window(x, window, offsets)
+        return y, s["state"]
+    if kind == "norm":
+        y, total = _plain_norm(_up(s["x"]), _up(s["residual"]), s["weight"])
+        out = [y.to(dt)]
+        if case["out"] == "e4m3":
+            q, scale = _to_8_bits(y, case["block"])
+            out = [q.to(E4M3), scale]
+        return out if s["residual"] is None else out + [total.to(s["residual"].dtype)]
+    with torch.enable_grad():
+        if kind == "norm_train":
+            x, residual, weight = (_leaf(s[n]) for n in ("x", "residual", "weight"))
+            y, total = _plain_norm(x, residual, weight)
+            ends = [(y, _up(s["dy"]))] + ([] if residual is None else [(total, _up(s["dsum"]))])
+            dx, dw = torch.autograd.grad([e for e, _ in ends], [x, weight], [d for _, d in ends])
+            out = {"y": y.detach().to(dt), "dx": dx.to(dt), "dweight": dw}
+            if residual is not None:
+                out["sum"] = total.detach().to(s["residual"].dtype)
+                if s["residual"].dtype != dt:
+                    out["dresidual"] = dx
+            return out
+        if kind == "conv_train":
+            x, weight, bias = (_leaf(s[n]) for n in ("x", "weight", "bias"))
+            y = _plain_conv(x, weight, bias, None, s["offsets"], case["act"])
+            dx, dw, db = torch.autograd.grad(y, [x, weight, bias], _up(s["dy"]))
+            return {"y": y.detach().to(dt), "dx": dx.to(dt), "dweight": dw, "dbias": db}
+        names = ["x", "delta", "A", "B", "C", "D"] + (["h"] if s["h"] is not None else [])
+        leaves = [_leaf(s[n]) for n in names]
+        y, h = _plain_scan(*leaves[:6], leaves[6] if s["h"] is not None else None, s["offsets"], case["zoh"])
+        ends = [(y, _up(s["dy"]))] + ([(h, s["dh_last"])] if s["dh_last"] is not None else [])
+        grads = torch.autograd.grad([e for e, _ in ends], leaves, [d for _, d in ends])
+    out = dict(zip(["dx", "ddelta", "dA", "dB", "dC", "dD", "dh0"], grads))
+    return dict(out, y=y.detach().to(dt), h_last=h.detach())
+
+
+# ---------------------------------------------------------------------------
+# one pass
+# ---------------------------------------------------------------------------
+
+def _run_own(s):
+    import selective_state_space_83_amd as ssm
+
+    case, kind = s["case"], s["case"]["kind"]
+    act = "silu" if case.get("act") == "silu" else None
+    if kind == "scan":
+        y, h = ssm.packed_scan(s["x"], s["delta"], s["A"], s["B"], s["C"], s["offsets"], D=s["D"], h0=s["h"],
+                               h_last=s["h"], slots=s["slots"] if s["h"] is not None else None,
+                               resume=s["resume"] if s["h"] is not None else None, zoh=case["zoh"],
+                               delta_bias=s["delta_bias"], delta_softplus=case["fused"], z=s["z"])
+        return y if h is None else (y, h)
+    if kind == "scan_step":
+        y = ssm.packed_step(s["h"], s["x"], s["delta"], s["A"], s["B"], s["C"], D=s["D"], slots=s["slots"],
+                            zoh=case["zoh"], delta_bias=s["delta_bias"], delta_softplus=case["fused"], z=s["z"])
+        return y, s["h"]
+    if kind == "scan_train":
+        hs = torch.empty(ssm.packed_states_shape(case["tokens"], case["dim"], case["N"]), device="cuda")
+        y, h = ssm.packed_scan(s["x"], s["delta"], s["A"], s["B"], s["C"], s["offsets"], D=s["D"], h0=s["h"],
+                               want_h_last=True, zoh=case["zoh"], h_saved=hs)
+        g = ssm.packed_scan_bwd(s["x"], s["delta"], s["A"], s["B"], s["C"], s["offsets"], s["dy"], hs, D=s["D"],
+                                h0=s["h"], dh_last=s["dh_last"], zoh=case["zoh"], want_dh0=s["h"] is not None)
+        return dict(g, y=y, h_last=h)
+    if kind == "conv":
+        y = ssm.short_conv(s["x"], s["weight"], s["bias"], offsets=s["offsets"], act=act, state=s["state"],
+                           slots=s["slots"] if s["state"] is not None else None,
+                           resume=s["resume"] if s["state"] is not None else None)
+        return y if s["state"] is None else (y, s["state"])
+    if kind == "conv_step":
+        return ssm.short_conv_step(s["state"], s["x"], s["weight"], s["bias"], act=act, slots=s["slots"]), s["state"]
+    if kind == "conv_train":
+        y = ssm.short_conv(s["x"], s["weight"], s["bias"], offsets=s["offsets"], act=act)
+        return dict(ssm.short_conv_bwd(s["x"], s["weight"], s["dy"], s["bias"], offsets=s["offsets"], act=act), y=y)
+    if kind == "norm":
+        if case["out"] == "e4m3":
+            out = ssm.add_rms_norm_8bit(s["x"], s["residual"], s["weight"], eps=EPS, block=case["block"])
+        else:
+            out = ssm.add_rms_norm(s["x"], s["residual"], s["weight"], eps=EPS)
+        return list(out if s["residual"] is not None else out[:-1])
+    y, total = ssm.add_rms_norm(s["x"], s["residual"], s["weight"], eps=EPS)
+    g = ssm.add_rms_norm_bwd(total, s["dy"], s["weight"], dsum=s["dsum"], eps=EPS)
+    return dict(g, y=y) if s["residual"] is None else dict(g, y=y, sum=total)
+
+
+def run(state):
+    with torch.no_grad():
+        return _run_own(state) if own else _run_plain(state)
+
+
+# ---------------------------------------------------------------------------
+# what a pass cannot do without
+# ---------------------------------------------------------------------------
+
+def work(case):
+    size, kind = 2 if case["dtype"] == "bf16" else 4, case["kind"]
+    if kind.startswith("norm"):
+        n = case["rows"] * case["channels"]
+        wide = {"none": 0, "same": size, "f32": 4}[case["residual"]]
+        if kind == "norm":
+            out = size if case["out"] == "same" else 1
+            scales = 0 if case["out"] == "same" else case["rows"] * -(-case["channels"] // (case["block"] or case["channels"]))
+            return {"bytes": n * (size + 2 * wide + out) + 4 * scales, "flops": 6 * n}
+        # x, residual, dy and the sum's gradient in; y, the sum, dx (and the residual's in its own type) out
+        own_type = wide if case["residual"] == "f32" and case["dtype"] == "bf16" else 0
+        return {"bytes": n * (4 * size + 3 * wide + own_type) + 8 * case["channels"], "flops": 16 * n}
+    T, S = case["tokens"], case["seqs"]
+    if kind.startswith("conv"):
+        n, K = T * case["channels"], case["K"]
+        states = 8 * S * case["channels"] * (K - 1) if case["states"] else 0
+        if kind == "conv_train":
+            return {"bytes": 4 * n * size, "flops": n * (6 * K + 12)}
+        return {"bytes": 2 * n * size + states, "flops": n * (2 * K + 4)}
+    n, N = T * case["dim"], case["N"]
+    states = 8 * S * case["dim"] * N if case["states"] else 0
+    if kind == "scan_train":
+        # x, delta, dy, B, C in; y, dx, ddelta (float32), dB, dC out
+        return {"bytes": n * (4 * size + 8) + T * N * (2 * size + 8) + 2 * states, "flops": 26 * n * N}
+    return {"bytes": n * size * (4 if case["fused"] else 3) + 2 * T * N * size + states, "flops": 6 * n * N}
+
+
+# ---------------------------------------------------------------------------
+# the definition in 64 bits
+# ---------------------------------------------------------------------------
+
+def _spans(s):
+    cut = s["offsets"].tolist()
+    return list(zip(cut[:-1], cut[1:]))
+
+
+def _exact_scan(s, train):
+    """Token by token, sequence by sequence; the gradients token by token backward from the states kept."""
+    case = s["case"]
+    f = lambda n: None if s.get(n) is None else s[n].double()  # noqa: E731
+    x, dl, A, B, C, D, z = (f(n) for n in ("x", "delta", "A", "B", "C", "D", "z"))
+    T, N = x.shape[0], A.shape[1]
+    if case["fused"]:
+        v = dl + f("delta_bias")
+        dl = v.clamp(min=0) + torch.log1p(torch.exp(-v.abs()))
+    states = f("h")
+    # the sequence's own slot; training states are in the sequences' order
+    place = list(range(case["seqs"])) if train else s["slots"].tolist()
+    taken = [True] * case["seqs"] if train else s["resume"].tolist()
+    out_states = None if states is None else states.clone()
+    h_last = torch.zeros(case["seqs"], *A.shape, dtype=torch.float64, device=x.device)
+    y = torch.zeros_like(x)
+    kept = torch.empty(T, *A.shape, dtype=torch.float64, device=x.device) if train else None
+    factor = (lambda e, d: torch.expm1(e) / A) if case["zoh"] else (lambda e, d: d[:, None].expand_as(e))
+    for i, (lo, hi) in enumerate(_spans(s)):
+        h = states[place[i]].clone() if states is not None and taken[i] else torch.zeros_like(h_last[i])
+        for t in range(lo, hi):
+            if train:
+                kept[t] = h
+            e = dl[t][:, None] * A
+            h = torch.exp(e) * h + factor(e, dl[t]) * B[t] * x[t][:, None]
+            y[t] = h @ C[t]
+        h_last[i] = h
+        if out_states is not None:
+            out_states[place[i]] = h
+    y += D * x
+    if not train:
+        y = y if z is None else y * z / (1 + torch.exp(-z))
+        return y if states is None else (y, out_states)
+    dy = f("dy")
+    g = {"y": y, "h_last": h_last, "dx": D * dy, "ddelta": torch.zeros_like(dl), "dA": torch.zeros_like(A),
+         "dB": torch.zeros_like(B), "dC": torch.zeros_like(C), "dD": (dy * x).sum(0), "dh0": torch.zeros_like(h_last)}
+    for i, (lo, hi) in enumerate(_spans(s)):
+        p = torch.zeros_like(A) if s["dh_last"] is None else s["dh_last"][i].double()
+        for t in range(hi - 1, lo - 1, -1):
+            d = dl[t][:, None]
+            e = d * A
+            a, k, Bx = torch.exp(e), factor(e, dl[t]), B[t] * x[t][:, None]
+            g["dC"][t] = dy[t] @ (a * kept[t] + k * Bx)
+            p = p + dy[t][:, None] * C[t]
+            ah, pB = p * a * kept[t], p * Bx
+            g["dx"][t] += (p * k) @ B[t]
+            g["dB"][t] = x[t] @ (p * k)
+            g["ddelta"][t] = (ah * A).sum(1) + (pB * (a if case["zoh"] else 1)).sum(1)
+            g["dA"] += ah * d + (pB * (d * a - k) / A if case["zoh"] else 0)
+            p = p * a
+        g["dh0"][i] = p
+    if states is None:
+        del g["dh0"]
+    return g
+
+
+def _exact_conv(s):
+    case = s["case"]
+    x, w, b = s["x"].double(), s["weight"].double(), s["bias"].double()
+    C, K = w.shape
+    step = case["kind"] == "conv_step"
+    spans = [(t, t + 1) for t in range(case["tokens"])] if step else _spans(s)
+    state = None if s["state"] is None else s["state"].double()
+    place, taken = s["slots"].tolist(), s["resume"].tolist()
+    y, dx, dw = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(w)
+    db = torch.zeros_like(b)
+    for i, (lo, hi) in enumerate(spans):
+        old = torch.zeros(K - 1, C, dtype=torch.float64, device=x.device)
+        if state is not None and (step or taken[i]):
+            old = state[place[i]].t()
+        line, n = torch.cat([old, x[lo:hi]]), hi - lo
+        a = b + sum(w[:, k] * line[k:k + n] for k in range(K))
+        sig = 1 / (1 + torch.exp(-a))
+        y[lo:hi] = a * sig if case["act"] == "silu" else a
+        if state is not None:
+            state[place[i]] = line[n:].t()
+        if case["kind"] == "conv_train":
+            da = s["dy"][lo:hi].double()
+            da = da * sig * (1 + a * (1 - sig)) if case["act"] == "silu" else da
+            db += da.sum(0)
+            dline = torch.zeros_like(line)
+            for k in range(K):
+                dline[k:k + n] += w[:, k] * da
+                dw[:, k] += (da * line[k:k + n]).sum(0)
+            dx[lo:hi] = dline[K - 1:]
+    if case["kind"] == "conv_train":
+        return {"y": y, "dx": dx, "dweight": dw, "dbias": db}
+    return y if state is None else (y, state)
+
+
+def _exact_norm(s):
+    case = s["case"]
+    x, w = s["x"].double(), s["weight"].double()
+    total = x if s["residual"] is None else x + s["residual"].double()
+    r = (total.square().sum(-1, keepdim=True) / total.shape[1] + EPS).pow(-0.5)
+    n = total * r
+    y = n * w
+    if case["kind"] == "norm":
+        out = [y]
+        if case["out"] == "e4m3":
+            size = case["block"] or y.shape[1]
+            parts = y.split(size, 1)
+            scale = torch.stack([p.abs().max(1).values for p in parts], 1) / E4M3_MAX
+            scale = torch.where(scale > 0, scale, torch.ones_like(scale))
+            q = torch.cat([p / scale[:, i:i + 1] for i, p in enumerate(parts)], 1)
+            # to the nearest of e4m3's values: three bits behind the leading one, steps of 2^-9 below 2^-6
+            unit = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 3)
+            out = [torch.round(q / unit) * unit, scale]
+        return out if s["residual"] is None else out + [total]
+    dy = s["dy"].double()
+    dn = dy * w
+    ds = r * (dn - n * (dn * n).sum(-1, keepdim=True) / n.shape[1])
+    if s["dsum"] is not None:
+        ds = ds + s["dsum"].double()
+    got = {"y": y, "dx": ds, "dweight": (dy * n).sum(0)}
+    if s["residual"] is not None:
+        got["sum"] = total
+        if s["residual"].dtype != s["x"].dtype:
+            got["dresidual"] = ds
+    return got
+
+
+def exact(case, seed):
+    with torch.no_grad():
+        s = prepare(case, seed)
+        if case["kind"].startswith("norm"):
+            return _exact_norm(s)
+        if case["kind"].startswith("conv"):
+            return _exact_conv(s)
+        if case["kind"] == "scan_step":
+            # sequences of one token, all resumed
+            s["offsets"] = torch.arange(case["tokens"] + 1, device="cuda")
+            s["resume"] = torch.ones_like(s["resume"])
+        return _exact_scan(s, case["kind"] == "scan_train")
