@@ -517,6 +517,255 @@ size_t ssm_group_norm_bwd_workspace_size(const ssm_group_norm_bwd_args_t* args);
  * dweight and dbias are summed over the rows in a fixed order. */
 ssm_status_t ssm_group_norm_bwd(const ssm_group_norm_bwd_args_t* args, void* hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the scan in a layer, for sequences of unequal lengths laid one behind
+ * the other: the packed scan, the short convolution by itself (its output is
+ * what a layer projects to Delta, B and C, which the convolution fused into
+ * ssm_scan_fwd comes too late for), and the residual's addition with the
+ * root-mean-square norm.
+ *
+ * Conventions, where they differ from the scan's:
+ *   Packed     rows are tokens; sequence s holds the tokens offsets[s] ..
+ *              offsets[s + 1] - 1 (device, int32, seqs + 1 of them, not
+ *              falling, within 0 .. tokens; values outside are taken as clamped,
+ *              falling ones give unspecified outputs).  Sequences may be empty.
+ *              Tokens before offsets[0] and from offsets[seqs] on belong to
+ *              none: they are not read for any output (they may hold anything),
+ *              and their rows of y are left as they were; gradients are 0 there.
+ *   Slots      states and windows lie in a cache of `slots` entries; sequence s
+ *              uses entry slot[s] (device, int32), or entry s where slot is
+ *              NULL.  A sequence whose slot is not within 0 .. slots - 1 (a padding row's
+ *              -1) starts from zero and keeps nothing.  Two sequences of a call
+ *              with one slot: it ends up with parts of either's state.
+ *   Resume     resume[s] (device, one byte; NULL = all 1) says whether sequence
+ *              s takes up its slot's entry (nonzero) or starts from zero.
+ *   Strides    inputs have contiguous channels and the row strides given (in
+ *              elements, not negative), so slices of a projection need no copy;
+ *              outputs, states and weights are dense.
+ *   Dtypes     x and the other inputs of a row share dtype (fp32 or bf16), and so
+ *              does y; A, weights, biases, states and windows are fp32, sums too.
+ * ------------------------------------------------------------------------- */
+
+/* The scan of ssm_scan_args_t over packed sequences:
+ *   h_t = Abar_t h_{t-1} + Bbar_t x_t,  y_t = (sum_n C_t h_t + Dskip x_t) silu(z_t)
+ * with h before a sequence's first token from h0 (zero when h0 is NULL or the
+ * sequence is not resumed), and its last state to h_last.  An empty sequence's
+ * last state is its first.  h_last may be h0 itself (a cache updated in place);
+ * otherwise the two do not overlap. */
+typedef struct {
+  int64_t tokens, seqs, slots, dim, dstate;
+  int64_t x_stride, delta_stride, z_stride, b_stride, c_stride;
+  int32_t dtype;                      /* ssm_dtype_t of x, delta, z, Bm, Cm, y */
+  int32_t disc;                       /* ssm_disc_t */
+  int32_t delta_softplus;             /* 1: Delta = softplus(delta + delta_bias) */
+  int32_t chunk_len;                  /* tokens per chunk, a multiple of 4; 0 = plan */
+  const void* x;                      /* (tokens, dim) */
+  const void* delta;                  /* (tokens, dim) */
+  const float* A;                     /* (dim, dstate) */
+  const void* Bm;                     /* (tokens, dstate) */
+  const void* Cm;                     /* (tokens, dstate) */
+  const float* Dskip;                 /* (dim) or NULL */
+  const float* delta_bias;            /* (dim) or NULL, added to delta */
+  const void* z;                      /* (tokens, dim) or NULL = no gate */
+  const int32_t* offsets;             /* (seqs + 1) */
+  const int32_t* slot;                /* (seqs) or NULL (slots = seqs) */
+  const uint8_t* resume;              /* (seqs) or NULL */
+  const float* h0;                    /* (slots, dim, dstate) or NULL */
+  float* h_last;                      /* (slots, dim, dstate) or NULL */
+  float* h_saved;                     /* (ceil(tokens / 16) - 1, dim, dstate) or NULL: receives the state
+                                         before tokens 16, 32, ..., for ssm_packed_scan_bwd (left as
+                                         it was at tokens of no sequence) */
+  void* y;                            /* (tokens, dim) */
+  void* workspace;                    /* >= ssm_packed_scan_workspace_size() bytes */
+  size_t workspace_bytes;
+} ssm_packed_scan_args_t;
+
+/* One token for each row of a batch, row b's state in entry slot[b] of h (NULL:
+ * entry b; slots = batch), updated in place; a row whose slot is out of range
+ * reads a zero state and keeps nothing. */
+typedef struct {
+  int64_t batch, slots, dim, dstate;
+  int64_t x_stride, delta_stride, z_stride, b_stride, c_stride;
+  int32_t dtype;
+  int32_t disc;
+  int32_t delta_softplus;
+  int32_t reserved;                   /* must be 0 */
+  const void* x;                      /* (batch, dim) */
+  const void* delta;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* Dskip;
+  const float* delta_bias;
+  const void* z;
+  const int32_t* slot;                /* (batch) or NULL */
+  float* h;                           /* (slots, dim, dstate) */
+  void* y;                            /* (batch, dim) */
+} ssm_packed_step_args_t;
+
+/* Gradients of  sum(dy * y) + sum(dh_last * h_last)  of the packed scan without
+ * softplus, bias and gate, every sequence's state in entry s of h0 (NULL = all
+ * from zero), dh_last (NULL = 0) and dh0 (seqs of them).  h_saved is what the
+ * forward call of the same inputs kept.  Gradients are fp32 and overwritten. */
+typedef struct {
+  int64_t tokens, seqs, dim, dstate;
+  int64_t x_stride, delta_stride, b_stride, c_stride, dy_stride;
+  int32_t dtype;                      /* ssm_dtype_t of x, delta, Bm, Cm, dy */
+  int32_t disc;
+  int32_t super_chunk;                /* tokens per adjoint chunk, a multiple of 16; 0 = plan */
+  int32_t reserved;                   /* must be 0 */
+  const void* x;
+  const void* delta;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* Dskip;
+  const int32_t* offsets;             /* (seqs + 1) */
+  const float* h0;                    /* (seqs, dim, dstate) or NULL */
+  const float* h_saved;               /* (ceil(tokens / 16) - 1, dim, dstate) */
+  const void* dy;                     /* (tokens, dim) gradient of y */
+  const float* dh_last;               /* (seqs, dim, dstate) or NULL */
+  float* dx;                          /* (tokens, dim) */
+  float* ddelta;                      /* (tokens, dim) */
+  float* dA;                          /* (dim, dstate) */
+  float* dB;                          /* (tokens, dstate) */
+  float* dC;                          /* (tokens, dstate) */
+  float* dD;                          /* (dim) or NULL */
+  float* dh0;                         /* (seqs, dim, dstate) or NULL */
+  void* workspace;                    /* >= ssm_packed_scan_bwd_workspace_size() bytes */
+  size_t workspace_bytes;
+} ssm_packed_scan_bwd_args_t;
+
+/* Workspace sizes: pure host functions of the sizes, chunk_len or super_chunk and
+ * whether h0 and h_last are given; 0 for invalid sizes. */
+size_t ssm_packed_scan_workspace_size(const ssm_packed_scan_args_t* args);
+size_t ssm_packed_scan_bwd_workspace_size(const ssm_packed_scan_bwd_args_t* args);
+ssm_status_t ssm_packed_scan_fwd(const ssm_packed_scan_args_t* args, void* hip_stream);
+ssm_status_t ssm_packed_step(const ssm_packed_step_args_t* args, void* hip_stream);
+ssm_status_t ssm_packed_scan_bwd(const ssm_packed_scan_bwd_args_t* args, void* hip_stream);
+
+/* Short causal convolution, depthwise, over packed sequences:
+ *   y[t,c] = act(bias[c] + sum_{k<K} weight[c,k] x[t-K+1+k, c])
+ * where inputs before a sequence's first token come from its window, the last
+ * K - 1 inputs before it, oldest first (zero when state is NULL or it is not
+ * resumed), and the window moves on in place.  Without offsets the sequences
+ * have seqlen tokens each (tokens = seqs * seqlen). */
+typedef enum { SSM_ACT_NONE = 0, SSM_ACT_SILU = 1 } ssm_act_t;
+
+typedef struct {
+  int64_t tokens, seqs, seqlen, slots, channels;
+  int64_t x_stride;
+  int32_t dtype;                      /* ssm_dtype_t of x, y */
+  int32_t taps;                       /* K, 1..4 */
+  int32_t act;                        /* ssm_act_t */
+  int32_t reserved;                   /* must be 0 */
+  const void* x;                      /* (tokens, channels) */
+  const float* weight;                /* (channels, K), the newest input's tap last */
+  const float* bias;                  /* (channels) or NULL */
+  const int32_t* offsets;             /* (seqs + 1) or NULL */
+  const int32_t* slot;                /* (seqs) or NULL (slots = seqs) */
+  const uint8_t* resume;              /* (seqs) or NULL */
+  float* state;                       /* (slots, channels, K - 1) or NULL */
+  void* y;                            /* (tokens, channels) */
+} ssm_short_conv_args_t;
+
+typedef struct {
+  int64_t batch, slots, channels;
+  int64_t x_stride;
+  int32_t dtype;
+  int32_t taps;
+  int32_t act;
+  int32_t reserved;
+  const void* x;                      /* (batch, channels) */
+  const float* weight;
+  const float* bias;
+  const int32_t* slot;                /* (batch) or NULL (slots = batch) */
+  float* state;                       /* (slots, channels, K - 1); may be NULL with K = 1 */
+  void* y;                            /* (batch, channels) */
+} ssm_short_conv_step_args_t;
+
+/* Gradients of sum(dy * y) with every sequence from an empty window:
+ *   da = dy act'(a);  dx[t] = sum_k weight[k] da[t+K-1-k] within t's sequence;
+ *   dweight[k] = sum_t da[t] x[t-K+1+k];  dbias = sum_t da[t],
+ * the sums in a fixed order.  dx has dtype; dweight and dbias are fp32. */
+typedef struct {
+  int64_t tokens, seqs, seqlen, channels;
+  int64_t x_stride, dy_stride;
+  int32_t dtype;                      /* ssm_dtype_t of x, dy, dx */
+  int32_t taps;
+  int32_t act;
+  int32_t reserved;
+  const void* x;
+  const float* weight;
+  const float* bias;
+  const int32_t* offsets;
+  const void* dy;                     /* (tokens, channels) */
+  void* dx;                           /* (tokens, channels) */
+  float* dweight;                     /* (channels, K) or NULL */
+  float* dbias;                       /* (channels) or NULL */
+  void* workspace;                    /* >= ssm_short_conv_bwd_workspace_size() bytes */
+  size_t workspace_bytes;
+} ssm_short_conv_bwd_args_t;
+
+/* (0 without dweight and dbias, or for invalid sizes; a pure host function) */
+size_t ssm_short_conv_bwd_workspace_size(const ssm_short_conv_bwd_args_t* args);
+ssm_status_t ssm_short_conv_fwd(const ssm_short_conv_args_t* args, void* hip_stream);
+ssm_status_t ssm_short_conv_step(const ssm_short_conv_step_args_t* args, void* hip_stream);
+ssm_status_t ssm_short_conv_bwd(const ssm_short_conv_bwd_args_t* args, void* hip_stream);
+
+/* The residual's addition and the root-mean-square norm of the sum, row by row:
+ *   s = x + residual (x when residual is NULL)
+ *   y = s / sqrt(mean(s^2) + eps) * weight
+ * s is kept in the residual's type in `sum` (which may be the residual itself,
+ * updated in place); y is formed from the unrounded s, in x's type, or in 8 bits:
+ * values of e4m3 (the OCP format: largest 448, NaN, no infinities) and a scale
+ * for each `block` neighbouring channels of a row (the last block may be short;
+ * 0: one for the row), y ~ q scale, scale = max|y| / 448 of its block, at least 2^-126,
+ * and 1 where that maximum is 0 (or no number).  q is rounded once, to nearest even. */
+#define SSM_E4M3 2                    /* a y_dtype of ssm_add_norm_args_t only */
+
+typedef struct {
+  int64_t rows, channels, block;
+  int64_t x_stride, residual_stride;
+  int32_t dtype;                      /* ssm_dtype_t of x */
+  int32_t residual_dtype;             /* dtype or SSM_F32 */
+  int32_t y_dtype;                    /* dtype or SSM_E4M3 */
+  float eps;                          /* >= 0 */
+  const void* x;                      /* (rows, channels) */
+  const void* residual;               /* (rows, channels) or NULL */
+  const float* weight;                /* (channels) or NULL = 1 */
+  void* sum;                          /* (rows, channels) in residual_dtype; NULL: not kept */
+  void* y;                            /* (rows, channels) */
+  float* scale;                       /* (rows, ceil(channels / block)), with SSM_E4M3 only */
+} ssm_add_norm_args_t;
+
+/* Its gradients, from the sum:  with n = s r, r = 1 / sqrt(mean(s^2) + eps),
+ *   ds = dsum + r (dy weight - n mean(dy weight n)),  dweight = sum_rows dy n.
+ * dx and dresidual are both ds: dx in dtype, dresidual in sum_dtype where that is
+ * another type (NULL: not wanted). */
+typedef struct {
+  int64_t rows, channels;
+  int64_t sum_stride, dy_stride, dsum_stride;
+  int32_t dtype;                      /* ssm_dtype_t of dy, dx */
+  int32_t sum_dtype;                  /* dtype or SSM_F32: of sum, dsum, dresidual */
+  int32_t reserved;                   /* must be 0 */
+  float eps;
+  const void* sum;                    /* (rows, channels) */
+  const void* dy;                     /* (rows, channels) gradient of y */
+  const void* dsum;                   /* (rows, channels) gradient of the kept sum, or NULL = 0 */
+  const float* weight;                /* (channels) or NULL = 1 */
+  void* dx;                           /* (rows, channels) */
+  void* dresidual;                    /* (rows, channels) or NULL */
+  float* dweight;                     /* (channels) or NULL */
+  void* workspace;                    /* >= ssm_add_norm_bwd_workspace_size() bytes */
+  size_t workspace_bytes;
+} ssm_add_norm_bwd_args_t;
+
+/* (0 without dweight, or for invalid sizes; a pure host function) */
+size_t ssm_add_norm_bwd_workspace_size(const ssm_add_norm_bwd_args_t* args);
+ssm_status_t ssm_add_norm_fwd(const ssm_add_norm_args_t* args, void* hip_stream);
+ssm_status_t ssm_add_norm_bwd(const ssm_add_norm_bwd_args_t* args, void* hip_stream);
+
 /* Static description of a status code. */
 const char* ssm_status_string(ssm_status_t status);
 

@@ -20,6 +20,10 @@ calls (conv_state_in / conv_state_out for the scan, conv_state for step).
 Beside the scan, for models with one decay per head, ``mixer`` binds decay
 attention and the group norm that follows it (``decay_attn``,
 ``decay_attn_step``, ``decay_attn_bwd``, ``group_norm``, ``group_norm_bwd``).
+``layer`` binds what stands around the scan where sequences of unequal lengths lie
+one behind the other and their states in a cache: ``packed_scan``, ``packed_step``,
+``packed_scan_bwd``, ``short_conv``, ``short_conv_step``, ``short_conv_bwd``,
+``add_rms_norm``, ``add_rms_norm_8bit``, ``add_rms_norm_bwd``.
 
 If the library is not built, importing works but every call raises: there is
 no CPU fallback.
@@ -117,7 +121,12 @@ EXPORTS = ["ssm_abi_version", "ssm_scan_workspace_size", "ssm_scan_plan_chunk_le
            "ssm_scan_bwd", "ssm_status_string", "ssm_last_error_message",
            "ssm_decay_attn_workspace_size", "ssm_decay_attn_bwd_workspace_size",
            "ssm_decay_attn_fwd", "ssm_decay_attn_step", "ssm_decay_attn_bwd",
-           "ssm_group_norm_fwd", "ssm_group_norm_bwd_workspace_size", "ssm_group_norm_bwd"]
+           "ssm_group_norm_fwd", "ssm_group_norm_bwd_workspace_size", "ssm_group_norm_bwd",
+           "ssm_packed_scan_workspace_size", "ssm_packed_scan_fwd", "ssm_packed_step",
+           "ssm_packed_scan_bwd_workspace_size", "ssm_packed_scan_bwd",
+           "ssm_short_conv_fwd", "ssm_short_conv_step", "ssm_short_conv_bwd_workspace_size",
+           "ssm_short_conv_bwd",
+           "ssm_add_norm_fwd", "ssm_add_norm_bwd_workspace_size", "ssm_add_norm_bwd"]
 
 # bytes of device scratch ssm_scan_fwd_noalloc keeps per GPU (SSM_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -170,6 +179,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ssm_last_error_message.restype = ctypes.c_char_p
     lib.ssm_last_error_message.argtypes = []
     mixer.declare(lib)
+    layer.declare(lib)
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -649,7 +659,11 @@ def scan_bwd(x, delta, A, B, C, dy, D=None, h0=None, dh_last=None, zoh=False, wa
     return {k: v for k, v in g.items() if v is not None}
 
 
-# the head-decay mixer's part of the binding (it uses the helpers above)
+# the head-decay mixer's part of the binding, and the layer's (they use the helpers above)
 from . import mixer  # noqa: E402
 from .mixer import (decay_attn, decay_attn_bwd, decay_attn_step, group_norm,  # noqa: E402,F401
                     group_norm_bwd)
+from . import layer  # noqa: E402
+from .layer import (add_rms_norm, add_rms_norm_8bit, add_rms_norm_bwd, packed_scan,  # noqa: E402,F401
+                    packed_scan_bwd, packed_states_shape, packed_step, short_conv, short_conv_bwd,
+                    short_conv_step)

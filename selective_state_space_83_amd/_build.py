@@ -12,7 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libssmscan.so")
 
-SOURCES = [os.path.join(CSRC, n) for n in ("ssm_scan.hip", "decay_attn.hip", "group_norm.hip")]
+SOURCES = [os.path.join(CSRC, n) for n in ("ssm_scan.hip", "decay_attn.hip", "group_norm.hip",
+                                            "packed_scan.hip", "short_conv.hip", "add_norm.hip")]
 
 # Packed-FP32 instructions are switched off for all device code.
 HIPCC_FLAGS = [
@@ -42,7 +43,7 @@ def build(out: str = LIB_PATH, verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory() as d:
         objs = [os.path.join(d, os.path.basename(src) + ".o") for src in SOURCES]
         cmds = [[hipcc()] + flags + ["-c", src, "-o", obj] for src, obj in zip(SOURCES, objs)]
-        with concurrent.futures.ThreadPoolExecutor(max_workers=4) as ex:
+        with concurrent.futures.ThreadPoolExecutor(max_workers=6) as ex:
             list(ex.map(run, cmds))
         run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + ["-o", tmp])
     os.replace(tmp, out)
