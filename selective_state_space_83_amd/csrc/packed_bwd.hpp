@@ -3,15 +3,13 @@
 // carries, and a main pass that recomputes 16 tokens at a time from the states the
 // forward kept and walks them back) over a token axis cut wherever it falls, with
 //
-//   * the state replaced at a sequence's first token in the recompute, and the
-//     adjoint replaced behind it (by dh_last of the sequence before, or 0) on the
-//     way back; what it was there is that sequence's dh0;
+//   * the state replaced at a sequence's first token in the recompute (what is kept in
+//     registers before it is the state after the step before), and the adjoint
+//     replaced behind it (by dh_last of the sequence before, or 0) on the way back;
+//     what it was there is that sequence's dh0;
 //   * summaries walked only from the end of the sequence that reaches back past a
 //     super-chunk's first token, where that end lies in it (reset);
 //   * tokens of no sequence left unread, their gradients 0.
-//
-// The recomputed states before and after a step are neighbours in registers, except
-// before a sequence's first token, where the state after the step is formed again.
 #pragma once
 
 #include "packed_scan.hpp"
@@ -41,22 +39,21 @@ struct PackedBwdParams {
   int32_t* reset;        // (nc - 1)
   float* dAp;            // (nc, D, N) and
   float* dDp;            // (nc, D): the super-chunks' sums
-  float* dBp;            // (tokens, dtiles, N) and
-  float* dCp;            // (tokens, dtiles, N): the channel tiles' sums
-  int64_t xs, dls, bs, cs, ys;   // row strides; ys: of dy
+  float* dBCp;           // (tokens, dtiles, 2, N): the channel tiles' sums for dB, then dC
+  int64_t xs, dls, ys;   // row strides; ys: of dy
+  uint32_t bs, cs;
   int64_t D;
   Seqs q;
   int32_t T, nc;         // tokens per super-chunk (a multiple of 16), super-chunks
   int32_t dtiles, nwg;
   float exact_thr;
-  int32_t rows_ok;
 };
 
 // The sequence that holds token t (of those with its first token, the one with any).
 __device__ __forceinline__ int32_t seq_at(const Seqs& q, int32_t t) { return seqs_before(q, t + 1) - 1; }
 
 // Reverse summary of super-chunks 1 .. nc - 1.
-template <int N, typename InT, int DISC>
+template <int N, typename InT, int DISC, bool ODD>
 __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) k_packed_bwd_summary(const PackedBwdParams p) {
   constexpr int kU = 8;
   const int wg = xcd_remap(blockIdx.x, p.nwg);
@@ -90,14 +87,16 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
   const uint32_t lane = lo_ch * sizeof(InT);
   constexpr InT* kIn = nullptr;
   const InT* Crow = static_cast<const InT*>(p.Cm) + int64_t(to - 1) * p.cs;
-  const bool ok = p.rows_ok != 0;
   float dacc = 0.0f, dcomp = 0.0f;
-  float Cb0[N], Cb1[N];
-  row_of<N>(Cb0, Crow, ok);
-  auto one_step = [&](float dv, float dyv, bool has_next, float (&Ccur)[N], float (&Cnext)[N]) {
-    const InT* nc = Crow - (has_next ? p.cs : 0);
-    if constexpr (N >= 2) asm volatile("" : "+s"(nc) : "s"(Ccur[0]));
-    row_of<N>(Cnext, nc, ok);
+  using R = Row<N, InT, ODD>;
+  R Cb0, Cb1;
+  Cb0.load(Crow);
+  auto one_step = [&](float dv, float dyv, uint32_t behind, const R& Cthis, R& Cnext) {
+    const InT* nc = Crow - behind;
+    asm volatile("" : "+s"(nc) : "s"(Cthis.w[0]));
+    Cnext.load(nc);
+    float Ccur[N];
+    Cthis.widen(Ccur);
     if (any_exact<N, DISC>(cc, dv)) {   // wave-uniform
 #pragma unroll
       for (int n = 0; n < N; ++n) {
@@ -123,23 +122,30 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
     dc[j] = ldb(wd.r, lane, at(j) * wd.row, kIn);
     yc[j] = ldb(wy.r, lane, at(j) * wy.row, kIn);
   }
-  for (int32_t tb = 0; tb < steps; tb += kU) {
+  int32_t t = 0;
+  for (; t + kU < steps; t += kU) {
     float dn[kU], yn[kU];
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
-      dn[j] = ldb(wd.r, lane, at(tb + kU + j) * wd.row, kIn);
-      yn[j] = ldb(wy.r, lane, at(tb + kU + j) * wy.row, kIn);
+      dn[j] = ldb(wd.r, lane, at(t + kU + j) * wd.row, kIn);
+      yn[j] = ldb(wy.r, lane, at(t + kU + j) * wy.row, kIn);
     }
 #pragma unroll
     for (int j = 0; j < kU; j += 2) {
-      if (tb + j < steps) one_step(dc[j], yc[j], tb + j + 1 < steps, Cb0, Cb1);
-      if (tb + j + 1 < steps) one_step(dc[j + 1], yc[j + 1], tb + j + 2 < steps, Cb1, Cb0);
+      one_step(dc[j], yc[j], p.cs, Cb0, Cb1);
+      one_step(dc[j + 1], yc[j + 1], p.cs, Cb1, Cb0);
     }
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
       dc[j] = dn[j];
       yc[j] = yn[j];
     }
+  }
+#pragma unroll 1
+  for (; t < steps; ++t) {
+    const float dv = ldb(wd.r, lane, at(t) * wd.row, kIn), dyv = ldb(wy.r, lane, at(t) * wy.row, kIn);
+    one_step(dv, dyv, t + 1 < steps ? p.cs : 0u, Cb0, Cb1);
+    Cb0 = Cb1;
   }
   store_n(p.gsum + (int64_t(slot) * p.D + d) * N, g);
   p.dsum[int64_t(slot) * p.D + d] = dacc - dcomp;
@@ -148,38 +154,13 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
 // Carries, from the last super-chunk down: gsum[c - 1] becomes the adjoint that
 // enters super-chunk c - 1 from behind.
 template <int N>
-__global__ void __launch_bounds__(kWave) k_packed_bwd_carry(const PackedBwdParams p) {
-  constexpr int U = 8;
-  const int64_t i = int64_t(blockIdx.x) * kWave + threadIdx.x, DN = p.D * N;
-  if (i >= DN) return;
-  const float a2 = p.A[i] * kLog2e;
-  const float* ds = p.dsum + i / N;
-  float* gs = p.gsum + i;
-  float carry = 0.0f;
-  int32_t c = p.nc - 2;
-  for (; c >= U - 1; c -= U) {
-    float sv[U], gv[U];
-    int32_t rv[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      sv[j] = ds[(c - j) * p.D];
-      gv[j] = gs[(c - j) * DN];
-      rv[j] = p.reset[c - j];
-    }
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      carry = rv[j] ? gv[j] : decay_add(a2 * sv[j], carry, gv[j]);
-      gs[(c - j) * DN] = carry;
-    }
-  }
-  for (; c >= 0; --c) {
-    const float gv = gs[c * DN];
-    carry = p.reset[c] ? gv : decay_add(a2 * ds[c * p.D], carry, gv);
-    gs[c * DN] = carry;
-  }
+__global__ void __launch_bounds__(kWave * kCarryWaves) k_packed_bwd_carry(const PackedBwdParams p) {
+  carry_walk<N, true>(p.A, p.dsum, p.gsum, p.reset, p.D, p.nc - 1);
 }
 
-// Main pass; lanes, waves and LDS as in k_bwd_main.
+// Main pass; lanes, waves and LDS as in k_bwd_main.  What only some of the steps need is
+// read again from the arguments (args_again) every 16 tokens: kept in scalar registers,
+// it spilled 276 of them (16384 x 1536 x 16 fp32: %OLD% us, this %NEW%).
 template <int N, typename InT, int DISC>
 __global__ void __launch_bounds__(kWave * BwdLayout<N>::NG) __attribute__((amdgpu_waves_per_eu(4)))
 k_packed_bwd(const PackedBwdParams p) {
@@ -189,17 +170,20 @@ k_packed_bwd(const PackedBwdParams p) {
   constexpr int LPR = kWave / RR;      // lanes per row; each sums RR floats
   __shared__ __attribute__((aligned(16))) float red[NG][RR][kRedPitch];
   __shared__ float xch[2][2][NG][K][kWave];
+  // of the sequences that begin among 16 tokens, at the place of their first token:
+  // which one it is, and which one ends before it (each wave its own)
+  __shared__ int32_t ids[NG][2][F];
   // bf16 rows of B and C, widened once, double-buffered by 16 tokens; fp32 rows go
   // through scalar loads
   constexpr bool kRowsLds = !std::is_same<InT, float>::value;
   __shared__ __attribute__((aligned(16))) float rows[kRowsLds ? 2 : 1][2][kRowsLds ? F : 1][N];
 
   const int wg = xcd_remap(blockIdx.x, p.nwg);
-  const int64_t dtile = wg % p.dtiles;
+  const int32_t dtile = wg % p.dtiles;
   const int32_t chunk = wg / p.dtiles;
   const int w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int lane = threadIdx.x % kWave;
-  const int64_t dbase = dtile * kWave;
+  const int64_t dbase = int64_t(dtile) * kWave;
   const int64_t d = dbase + lane_offset(dbase, p.D, static_cast<uint32_t>(lane));
   const bool valid = dbase + lane < p.D;   // lanes past D duplicate D - 1 and add nothing
   if (!valid) {
@@ -208,7 +192,7 @@ k_packed_bwd(const PackedBwdParams p) {
   }
   int xb = 0;
   const int n0 = w * NS;
-  const int64_t dn = d * N + n0, DN = p.D * N;   // this lane's states in a (D, N) array
+  const int64_t dn = d * N + n0;   // this lane's states in a (D, N) array
 
   ChanConst<NS, DISC> cc;
   load_chan<NS, DISC>(cc, p.A + dn, p.exact_thr);
@@ -223,76 +207,90 @@ k_packed_bwd(const PackedBwdParams p) {
   }
 
   const int32_t t0 = chunk * p.T, t1 = p.q.tokens - t0 > p.T ? t0 + p.T : p.q.tokens;
-  const int32_t lo = seq_start(p.q, 0), hi = seq_start(p.q, p.q.S);
-  const int32_t from = t0 > lo ? t0 : lo, to = t1 < hi ? t1 : hi;   // tokens of sequences
-  // the first token of the sequence whose tokens are walked next
-  int32_t first = INT32_MIN;
+  const int32_t lo = seq_start(p.q, 0), hi = seq_start(p.q, p.q.S);   // tokens of sequences
+  // the sequence whose tokens are walked next, and its first token
+  int32_t seq = -1, first = INT32_MIN;
   float g[NS];
   zero_n(g);
-  if (from < to) {
-    const int32_t s = seq_at(p.q, to - 1);
-    first = seq_start(p.q, s);
-    if (first > to - 1) first = to - 1;
-    if (seq_start(p.q, s + 1) > t1) {
-      load_n(g, p.gsum + int64_t(chunk) * DN + dn);
-    } else if (p.dh_last) {
-      load_n(g, p.dh_last + int64_t(s) * DN + dn);
+  {
+    const int32_t from = t0 > lo ? t0 : lo, to = t1 < hi ? t1 : hi;
+    if (from < to) {
+      seq = seq_at(p.q, to - 1);
+      first = seq_start(p.q, seq);
+      if (first > to - 1) first = to - 1;
+      if (seq_start(p.q, seq + 1) > t1) {
+        load_n(g, p.gsum + int64_t(chunk) * p.D * N + dn);
+      } else if (p.dh_last) {
+        load_n(g, p.dh_last + int64_t(seq) * p.D * N + dn);
+      }
     }
   }
   float dAacc[NS];
   zero_n(dAacc);
   float dDacc = 0.0f;
 
-  const InT* Bp = static_cast<const InT*>(p.Bm);
-  const InT* Cp = static_cast<const InT*>(p.Cm);
   const uint32_t lane_in = uint32_t(d - dbase) * sizeof(InT), lane_f = uint32_t(d - dbase) * 4u;
-  const uint32_t row_f = uint32_t(p.D * 4);
   constexpr InT* kIn = nullptr;
   constexpr float* kF = nullptr;
-  const bool ok = p.rows_ok != 0;
+  // where a lane's sums of two steps go, in a token's (dtiles, 2, N) rows: lane's row is
+  // [step of the pair][dB or dC][state]; one lane of each LPR stores (the others past
+  // the window's end)
+  const int rr_ = lane / LPR;
+  const uint32_t sums_row = uint32_t(p.dtiles) * (2 * N * 4);
+  const uint32_t sums_at = lane % LPR == 0 ? uint32_t(((rr_ / NS) & 1) * N + n0 + rr_ % NS) * 4u + uint32_t(rr_ / (2 * NS)) * sums_row
+                                           : 0x80000000u;
 
   // the rows each thread moves into LDS, loaded 16 tokens ahead (rows of tokens of no
   // sequence as 0)
   constexpr int kRowVals = kRowsLds ? 2 * F * N : 1;
   constexpr int RV = (kRowVals + kWave * NG - 1) / (kWave * NG);
   float rpre[RV];
-  auto rows_load = [&](int32_t f0) {
+  auto rows_load = [&](const PackedBwdParams& a, int32_t f0) {
+    const InT* Bp = static_cast<const InT*>(a.Bm);
+    const InT* Cp = static_cast<const InT*>(a.Cm);
 #pragma unroll
     for (int i = 0; i < RV; ++i) {
       const int e = static_cast<int>(threadIdx.x) + i * kWave * NG;
       const int kind = (e / (F * N)) & 1, j = (e / N) % F, n = e % N;
       const bool in = e < kRowVals && f0 + j >= lo && f0 + j < hi;
-      rpre[i] = in ? ld((kind == 0 ? Bp + int64_t(f0 + j) * p.bs : Cp + int64_t(f0 + j) * p.cs) + n) : 0.0f;
+      rpre[i] = in ? ld((kind == 0 ? Bp + int64_t(f0 + j) * a.bs : Cp + int64_t(f0 + j) * a.cs) + n) : 0.0f;
     }
   };
   const int32_t f_top = (t1 - 1) / F * F;
-  if constexpr (kRowsLds) rows_load(f_top);
+  if constexpr (kRowsLds) rows_load(p, f_top);
   int rb = 0;
 
   for (int32_t f0 = f_top; f0 >= t0; f0 -= F) {
-    const int len = p.q.tokens - f0 < F ? p.q.tokens - f0 : F;
-    // tokens jlo .. jhi - 1 of them belong to sequences; bit j of begins: token j is a first one
+    const PackedBwdParams& a = args_again<PackedBwdParams>();
+    const int len = a.q.tokens - f0 < F ? a.q.tokens - f0 : F;
+    // bit j of live: token j belongs to a sequence; of begins: it is a first one
     const int jlo = lo > f0 ? (lo - f0 < len ? lo - f0 : len) : 0;
     const int jhi = hi - f0 < len ? (hi > f0 ? hi - f0 : 0) : len;
-    const bool some = jlo < jhi;
+    const uint32_t live = jlo < jhi ? (1u << jhi) - (1u << jlo) : 0u;
     uint32_t begins = 0;
     while (first >= f0) {
+      const int32_t before = first > lo ? seq_at(a.q, first - 1) : -1;
       begins |= 1u << (first - f0);
-      const int32_t before = first > lo ? seq_start(p.q, seq_at(p.q, first - 1)) : INT32_MIN;
-      first = before < first ? before : INT32_MIN;   // (falling offsets end the walk too)
+      if (lane < 2) ids[w][lane][first - f0] = lane == 0 ? seq : before;
+      const int32_t start = before >= 0 ? seq_start(a.q, before) : INT32_MIN;
+      seq = before;
+      first = start < first ? start : INT32_MIN;   // (falling offsets end the walk too)
     }
-    if (!some) {   // wave-uniform, and the workgroup's
+    // gradients of this channel tile's rows, and its sums for dB and dC
+    const __amdgpu_buffer_rsrc_t rdx = make_rsrc(a.dx + int64_t(f0) * a.D + dbase, uint32_t(len * a.D * 4));
+    const __amdgpu_buffer_rsrc_t rdd = make_rsrc(a.ddelta + int64_t(f0) * a.D + dbase, uint32_t(len * a.D * 4));
+    const uint32_t row_f = uint32_t(a.D * 4);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.dBCp + (int64_t(f0) * a.dtiles + dtile) * (2 * N),
+                                                uint32_t(len - 1) * sums_row + 2 * N * 4);
+    if (live == 0) {   // the whole workgroup
       for (int j = w; j < len; j += NG) {
-        p.dx[int64_t(f0 + j) * p.D + d] = 0.0f;
-        p.ddelta[int64_t(f0 + j) * p.D + d] = 0.0f;
+        stb(rdx, lane_f, uint32_t(j) * row_f, 0.0f, kF);
+        stb(rdd, lane_f, uint32_t(j) * row_f, 0.0f, kF);
       }
-      for (int e = threadIdx.x; e < len * N; e += kWave * NG) {
-        const int64_t i = (int64_t(f0 + e / N) * p.dtiles + dtile) * N + e % N;
-        p.dBp[i] = 0.0f;
-        p.dCp[i] = 0.0f;
-      }
+      for (int e = threadIdx.x; e < len * 2 * N; e += kWave * NG)
+        stb(rs, uint32_t(e / (2 * N)) * sums_row + uint32_t(e % (2 * N)) * 4u, 0, 0.0f, kF);
       if constexpr (kRowsLds) {
-        if (f0 > t0) rows_load(f0 - F);
+        if (f0 > t0) rows_load(a, f0 - F);
       }
       continue;
     }
@@ -303,24 +301,23 @@ k_packed_bwd(const PackedBwdParams p) {
         if (e < kRowVals) (&rows[rb][0][0][0])[e] = rpre[i];
       }
       __syncthreads();
-      if (f0 > t0) rows_load(f0 - F);
+      if (f0 > t0) rows_load(a, f0 - F);
     }
     const float* Brow = &rows[kRowsLds ? rb : 0][0][0][n0];
     const float* Crow = &rows[kRowsLds ? rb : 0][1][0][n0];
-    // every row is read at a token of a sequence: those of others repeat the nearest
-    auto near = [&](int j) { return j < jlo ? jlo : j < jhi ? j : jhi - 1; };
-    const RowWindow wx = window<InT>(p.x, p.xs, p.D, dbase, f0, jhi);
-    const RowWindow wd = window<InT>(p.delta, p.dls, p.D, dbase, f0, jhi);
-    const RowWindow wy = window<InT>(p.dy, p.ys, p.D, dbase, f0, jhi);
-    const __amdgpu_buffer_rsrc_t rdx = make_rsrc(p.dx + int64_t(f0) * p.D + dbase, uint32_t(len) * row_f);
-    const __amdgpu_buffer_rsrc_t rdd = make_rsrc(p.ddelta + int64_t(f0) * p.D + dbase, uint32_t(len) * row_f);
-    const InT* Bc = Bp + int64_t(f0) * p.bs + n0;
-    const InT* Cc = Cp + int64_t(f0) * p.cs + n0;
-    const float* hin = f0 > 0 ? p.hsave + (int64_t(f0 / F) - 1) * DN + dn : nullptr;
+    const RowWindow wx = window<InT>(a.x, a.xs, a.D, dbase, f0, len);
+    const RowWindow wd = window<InT>(a.delta, a.dls, a.D, dbase, f0, len);
+    const RowWindow wy = window<InT>(a.dy, a.ys, a.D, dbase, f0, len);
+    const InT* Bc = static_cast<const InT*>(a.Bm) + int64_t(f0) * a.bs + n0;
+    const InT* Cc = static_cast<const InT*>(a.Cm) + int64_t(f0) * a.cs + n0;
+    const uint32_t bs = a.bs, cs = a.cs;
+    auto in = [&](int j) { return uint32_t(j < len ? j : len - 1); };   // a row of the tensors
+    const float* hin = f0 > 0 ? a.hsave + (int64_t(f0 / F) - 1) * a.D * N + dn : nullptr;
     // the state before the first token of a sequence
-    auto initial = [&](float (&h)[NS], int32_t t) {
+    auto initial = [&](float (&h)[NS], int j) {
+      const PackedBwdParams& b = args_again<PackedBwdParams>();
       zero_n(h);
-      if (p.h0) load_n(h, p.h0 + int64_t(seq_at(p.q, t)) * DN + dn);
+      if (b.h0) load_n(h, b.h0 + int64_t(__builtin_amdgcn_readfirstlane(ids[w][0][j])) * b.D * N + dn);
     };
 #pragma unroll
     for (int half = F / H - 1; half >= 0; --half) {
@@ -329,12 +326,13 @@ k_packed_bwd(const PackedBwdParams p) {
       float h[NS];
       zero_n(h);
       if (hin) load_n(h, hin);
+      // the state after the step before each step of the half
       float stash[H][NS];
       float xa[K], da[K];
 #pragma unroll
       for (int jj = 0; jj < K; ++jj) {
-        xa[jj] = ldb(wx.r, lane_in, uint32_t(near(jj)) * wx.row, kIn);
-        da[jj] = ldb(wd.r, lane_in, uint32_t(near(jj)) * wd.row, kIn);
+        xa[jj] = ldb(wx.r, lane_in, in(jj) * wx.row, kIn);
+        da[jj] = ldb(wd.r, lane_in, in(jj) * wd.row, kIn);
       }
 #pragma unroll
       for (int jb = 0; jb < (j0 + H) / K; ++jb) {
@@ -342,13 +340,13 @@ k_packed_bwd(const PackedBwdParams p) {
         const int nb = (jb + 1 < (j0 + H) / K) ? jb + 1 : jb;
 #pragma unroll
         for (int jj = 0; jj < K; ++jj) {
-          xn[jj] = ldb(wx.r, lane_in, uint32_t(near(nb * K + jj)) * wx.row, kIn);
-          dn_[jj] = ldb(wd.r, lane_in, uint32_t(near(nb * K + jj)) * wd.row, kIn);
+          xn[jj] = ldb(wx.r, lane_in, in(nb * K + jj) * wx.row, kIn);
+          dn_[jj] = ldb(wd.r, lane_in, in(nb * K + jj) * wd.row, kIn);
         }
         float Bb[K][NS];
         if constexpr (!kRowsLds) {
 #pragma unroll
-          for (int jj = 0; jj < K; ++jj) row_of<NS>(Bb[jj], Bc + near(jb * K + jj) * p.bs, ok);
+          for (int jj = 0; jj < K; ++jj) load_row<NS>(Bb[jj], Bc + in(jb * K + jj) * bs);
         }
 #pragma unroll
         for (int jj = 0; jj < K; ++jj) {
@@ -360,12 +358,12 @@ k_packed_bwd(const PackedBwdParams p) {
 #pragma unroll
             for (int n = 0; n < NS; ++n) Bv[n] = Bb[jj][n];
           }
-          if (begins >> j & 1) initial(h, f0 + j);
           if (j >= j0) {
 #pragma unroll
             for (int n = 0; n < NS; ++n) stash[j - j0][n] = h[n];
           }
-          if (j >= jlo && j < jhi) {
+          if (begins >> j & 1) initial(h, j);
+          if (live >> j & 1) {
             if (any_exact<NS, DISC>(cc, da[jj]))
               ssm_step_lane<NS, DISC, false, true, true>(h, cc, Bv, Bv, xa[jj], da[jj]);
             else
@@ -384,14 +382,21 @@ k_packed_bwd(const PackedBwdParams p) {
         float ub[K], db[K], yb[K], Bb[K][NS], Cb[K][NS];
 #pragma unroll
         for (int jj = 0; jj < K; ++jj) {
-          const int j = near(jb * K + jj);
-          ub[jj] = ldb(wx.r, lane_in, uint32_t(j) * wx.row, kIn);
-          db[jj] = ldb(wd.r, lane_in, uint32_t(j) * wd.row, kIn);
-          yb[jj] = ldb(wy.r, lane_in, uint32_t(j) * wy.row, kIn);
+          const uint32_t j = in(jb * K + jj);
+          ub[jj] = ldb(wx.r, lane_in, j * wx.row, kIn);
+          db[jj] = ldb(wd.r, lane_in, j * wd.row, kIn);
+          yb[jj] = ldb(wy.r, lane_in, j * wy.row, kIn);
           if constexpr (!kRowsLds) {
-            row_of<NS>(Bb[jj], Bc + j * p.bs, ok);
-            row_of<NS>(Cb[jj], Cc + j * p.cs, ok);
+            load_row<NS>(Bb[jj], Bc + j * bs);
+            load_row<NS>(Cb[jj], Cc + j * cs);
           }
+        }
+        // keep the scalar row loads here, together
+        if constexpr (!kRowsLds && NS == 4) {
+#pragma unroll
+          for (int jj = 0; jj < K; ++jj)
+            asm volatile("" ::"s"(Bb[jj][0]), "s"(Bb[jj][1]), "s"(Bb[jj][2]), "s"(Bb[jj][3]),
+                         "s"(Cb[jj][0]), "s"(Cb[jj][1]), "s"(Cb[jj][2]), "s"(Cb[jj][3]));
         }
 #pragma unroll
         for (int jj = K - 1; jj >= 0; --jj) {
@@ -411,36 +416,32 @@ k_packed_bwd(const PackedBwdParams p) {
               Cv[n] = Cb[jj][n];
             }
           }
-          if (j >= jlo && j < jhi) {
+          if (live >> j & 1) {
             const int js = j - j0;
-            const bool exact = any_exact<NS, DISC>(cc, dv);
-            // the state after the step: the one before the next, or, before a sequence's
-            // first token, formed again
-            float hn[NS];
+            float hp[NS], hn[NS];   // the states before and after the step
 #pragma unroll
-            for (int n = 0; n < NS; ++n) hn[n] = (js + 1 < H) ? stash[js + 1 < H ? js + 1 : js][n] : h[n];
-            if (js + 1 < H && (begins >> (j + 1) & 1)) {
-#pragma unroll
-              for (int n = 0; n < NS; ++n) hn[n] = stash[js][n];
-              if (exact)
-                ssm_step_lane<NS, DISC, false, true, true>(hn, cc, Bv, Bv, u, dv);
-              else
-                ssm_step_lane<NS, DISC, false, false>(hn, cc, Bv, Bv, u, dv);
+            for (int n = 0; n < NS; ++n) {
+              hp[n] = stash[js][n];
+              hn[n] = (js + 1 < H) ? stash[js + 1 < H ? js + 1 : js][n] : h[n];
             }
+            if (begins >> j & 1) initial(hp, j);
+            const bool exact = any_exact<NS, DISC>(cc, dv);
             const bool series = DISC == kZoh && __builtin_amdgcn_ballot_w64(dv < zoh_thr) != 0;
             if (series)
-              bwd_lane_step<NS, DISC, true, kShortSeries>(g, dAacc, cc, Bv, Cv, stash[js], hn, u, dv, dyv, exact, pB,
-                                                          pC, du, ddt);
+              bwd_lane_step<NS, DISC, true, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, exact, pB, pC, du,
+                                                          ddt);
             else
-              bwd_lane_step<NS, DISC, false, kShortSeries>(g, dAacc, cc, Bv, Cv, stash[js], hn, u, dv, dyv, exact, pB,
-                                                           pC, du, ddt);
+              bwd_lane_step<NS, DISC, false, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, exact, pB, pC, du,
+                                                           ddt);
             dDacc = fmaf(dyv, u, dDacc);
             if (begins >> j & 1) {
-              const int32_t t = f0 + j;
-              if (p.dh0) store_n(p.dh0 + int64_t(seq_at(p.q, t)) * DN + dn, g);
+              const PackedBwdParams& b = args_again<PackedBwdParams>();
+              const int32_t s = __builtin_amdgcn_readfirstlane(ids[w][0][j]);
+              const int32_t before = __builtin_amdgcn_readfirstlane(ids[w][1][j]);
+              if (b.dh0) store_n(b.dh0 + int64_t(s) * b.D * N + dn, g);
               zero_n(g);
-              if (t > lo && p.dh_last) load_n(g, p.dh_last + int64_t(seq_at(p.q, t - 1)) * DN + dn);
-              // (where the sequence before ends before this super-chunk, that is another's to take)
+              // (of a sequence that ends before this super-chunk, g goes no further)
+              if (before >= 0 && b.dh_last) load_n(g, b.dh_last + int64_t(before) * b.D * N + dn);
             }
           }
           const int sp = jj & 1;
@@ -474,13 +475,9 @@ k_packed_bwd(const PackedBwdParams p) {
               acc += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc), 0x141, 0xF, 0xF, false));
             if constexpr (LPR >= 16)
               acc += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc), 0x140, 0xF, 0xF, false));
-            const int jr = jj + rr / (2 * NS);
-            const int kind = (rr / NS) & 1;
-            const int n = rr % NS;
-            if (c == 0 && jb * K + jr < len) {
-              float* dst = kind == 0 ? p.dBp : p.dCp;
-              dst[(int64_t(f0 + jb * K + jr) * p.dtiles + dtile) * N + n0 + n] = acc;
-            }
+            // rows of tokens past the last end behind the window (the row's offset goes
+            // with the lane's, which is what the window is checked against)
+            stb(rs, sums_at + uint32_t(j) * sums_row, 0, acc, kF);
             __builtin_amdgcn_wave_barrier();
           }
         }
@@ -495,7 +492,7 @@ k_packed_bwd(const PackedBwdParams p) {
               su += xch[xb][0][v][jj][lane];
               sd += xch[xb][1][v][jj][lane];
             }
-            if (j >= jlo && j < jhi) su = fmaf(dsk, ldb(wy.r, lane_in, uint32_t(j) * wy.row, kIn), su);
+            if (live >> j & 1) su = fmaf(dsk, ldb(wy.r, lane_in, uint32_t(j) * wy.row, kIn), su);
             stb(rdx, lane_f, uint32_t(j) * row_f, su, kF);
             stb(rdd, lane_f, uint32_t(j) * row_f, sd, kF);
           }
@@ -505,42 +502,40 @@ k_packed_bwd(const PackedBwdParams p) {
     }
     rb ^= 1;
   }
-  store_n(p.dAp + int64_t(chunk) * DN + dn, dAacc);
-  if (w == 0) p.dDp[int64_t(chunk) * p.D + d] = dDacc;
+  const PackedBwdParams& a = args_again<PackedBwdParams>();
+  const int64_t DN = a.D * N;
+  store_n(a.dAp + int64_t(chunk) * DN + dn, dAacc);
+  if (w == 0) a.dDp[int64_t(chunk) * a.D + d] = dDacc;
   // sequences without tokens: their last state is their first
-  if (chunk == 0 && p.dh0) {
-    for (int32_t s0 = 0; s0 < p.q.S; s0 += kWave) {
+  if (chunk == 0 && a.dh0) {
+    for (int32_t s0 = 0; s0 < a.q.S; s0 += kWave) {
       const int32_t s = s0 + lane;
       bool empty = false;
-      if (s < p.q.S) empty = ssmq::in_tokens(p.q, p.q.offsets[s]) >= ssmq::in_tokens(p.q, p.q.offsets[s + 1]);
+      if (s < a.q.S) empty = ssmq::in_tokens(a.q, a.q.offsets[s]) >= ssmq::in_tokens(a.q, a.q.offsets[s + 1]);
       uint64_t todo = __builtin_amdgcn_ballot_w64(empty);
       while (todo) {
         const int64_t e = s0 + __builtin_ctzll(todo);
         todo &= todo - 1;
         float v[NS];
         zero_n(v);
-        if (p.dh_last) load_n(v, p.dh_last + e * DN + dn);
-        store_n(p.dh0 + e * DN + dn, v);
+        if (a.dh_last) load_n(v, a.dh_last + e * DN + dn);
+        store_n(a.dh0 + e * DN + dn, v);
       }
     }
   }
 }
 
-// dB, dC: the channel tiles' sums of a (token, state).
+// dB, dC: the channel tiles' sums of a (token, dB or dC, state).
 template <int N>
 __global__ void __launch_bounds__(256) k_packed_bwd_bc(const PackedBwdParams p) {
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= int64_t(p.q.tokens) * N) return;
-  const int64_t t = i / N, n = i - t * N;
-  const float* sb = p.dBp + t * p.dtiles * N + n;
-  const float* sc = p.dCp + t * p.dtiles * N + n;
-  float ab = 0.0f, ac = 0.0f;
-  for (int k = 0; k < p.dtiles; ++k) {
-    ab += sb[k * N];
-    ac += sc[k * N];
-  }
-  p.dB[i] = ab;
-  p.dC[i] = ac;
+  if (i >= int64_t(p.q.tokens) * (2 * N)) return;
+  const int64_t t = i / (2 * N);
+  const int n = int(i % (2 * N));
+  const float* src = p.dBCp + t * p.dtiles * (2 * N) + n;
+  float sum = 0.0f;
+  for (int k = 0; k < p.dtiles; ++k) sum += src[k * (2 * N)];
+  (n < N ? p.dB + t * N + n : p.dC + t * N + n - N)[0] = sum;
 }
 
 // dA (D, N), then dD (D): the super-chunks' sums in a fixed order; a workgroup covers

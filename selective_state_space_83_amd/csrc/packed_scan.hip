@@ -103,7 +103,7 @@ ssm_status_t check_sizes(const Args* a, int64_t rows, int64_t seqs, int64_t slot
     return fail(SSM_ERR_SHAPE, "problem too large (tokens, sequences and slots are counted in 32 bits)");
   int64_t n;
   // per-token sums of every channel tile, and states, in bytes
-  if (a->dim > (int64_t(1) << 26) || !mul_ok(std::max({rows, seqs, slots}), std::max<int64_t>(a->dim, 1) * 16, &n) ||
+  if (a->dim > (int64_t(1) << 24) || !mul_ok(std::max({rows, seqs, slots}), std::max<int64_t>(a->dim, 1) * 16, &n) ||
       n > INT64_MAX / 64)
     return fail(SSM_ERR_SHAPE, "sizes overflow");
   for (int64_t s : strides)
@@ -223,32 +223,39 @@ float exact_threshold(int32_t disc, int32_t dtype) {
 
 int dt_mode_of(const float* bias, int32_t softplus) { return softplus ? kDtSoftplus : bias ? kDtBias : kDtRaw; }
 
-// bf16 rows of B and C are read two elements at a time where all of them start on 4 bytes
-bool rows_ok(const void* b, const void* c, int64_t bs, int64_t cs, int32_t dtype) {
-  return dtype == SSM_F32 || (!misaligned(b, 4) && !misaligned(c, 4) && bs % 2 == 0 && cs % 2 == 0);
-}
+// bf16 rows that do not all start on 4 bytes
+bool odd_rows(const void* p, uint32_t stride) { return misaligned(p, 4) || stride % 2 != 0; }
 
 ssm_status_t grid_ok(int64_t n) {
   return n > kMaxGrid / 1024 ? fail(SSM_ERR_SHAPE, "problem too large for one launch") : SSM_OK;
 }
 
-template <int N, typename InT, int DISC>
-ssm_status_t run_fwd(PackedParams p, hipStream_t s) {
+template <int N, typename InT, int DISC, bool ODD>
+ssm_status_t run_chunks(PackedParams p, hipStream_t s) {
   const int64_t out = int64_t(p.nc) * p.dtiles;
   if (ssm_status_t st = grid_ok(out)) return st;
   if (p.nc > 1) {
     p.nwg = (p.nc - 1) * p.dtiles;
-    hipLaunchKernelGGL((k_packed_summary<N, InT, DISC>), dim3(uint32_t(p.nwg)), dim3(kWave), 0, s, p);
+    hipLaunchKernelGGL((k_packed_summary<N, InT, DISC, ODD>), dim3(uint32_t(p.nwg)), dim3(kWave), 0, s, p);
     if (ssm_status_t st = launch_status("k_packed_summary")) return st;
-    hipLaunchKernelGGL((k_packed_carry<N>), dim3(uint32_t((p.D * N + kWave - 1) / kWave)), dim3(kWave), 0, s, p);
+    hipLaunchKernelGGL((k_packed_carry<N>), dim3(uint32_t((p.D * N + kWave - 1) / kWave)), dim3(kWave * kCarryWaves), 0,
+                       s, p);
     if (ssm_status_t st = launch_status("k_packed_carry")) return st;
   }
   p.nwg = int32_t(out);
   if (p.z)
-    hipLaunchKernelGGL((k_packed_out<N, InT, DISC, true>), dim3(uint32_t(out)), dim3(kWave), 0, s, p);
+    hipLaunchKernelGGL((k_packed_out<N, InT, DISC, true, ODD>), dim3(uint32_t(out)), dim3(kWave), 0, s, p);
   else
-    hipLaunchKernelGGL((k_packed_out<N, InT, DISC, false>), dim3(uint32_t(out)), dim3(kWave), 0, s, p);
+    hipLaunchKernelGGL((k_packed_out<N, InT, DISC, false, ODD>), dim3(uint32_t(out)), dim3(kWave), 0, s, p);
   return launch_status("k_packed_out");
+}
+
+template <int N, typename InT, int DISC>
+ssm_status_t run_fwd(const PackedParams& p, hipStream_t s) {
+  if constexpr (!std::is_same<InT, float>::value && N > 1) {
+    if (odd_rows(p.Bm, p.bs) || odd_rows(p.Cm, p.cs)) return run_chunks<N, InT, DISC, true>(p, s);
+  }
+  return run_chunks<N, InT, DISC, false>(p, s);
 }
 
 template <int N, typename InT, int DISC>
@@ -264,7 +271,7 @@ ssm_status_t run_step(PackedStepParams p, hipStream_t s) {
 
 struct BwdPlan {
   int64_t T = 16, nc = 1, dtiles = 0;
-  size_t off_dsum = 0, off_reset = 0, off_dAp = 0, off_dDp = 0, off_dBp = 0, off_dCp = 0, total = 0;
+  size_t off_dsum = 0, off_reset = 0, off_dAp = 0, off_dDp = 0, off_dBCp = 0, total = 0;
 };
 
 // Super-chunks: enough for the reverse summary's waves, at most kBwdLong tokens each
@@ -299,8 +306,7 @@ BwdPlan bwd_plan(const ssm_packed_scan_bwd_args_t* a) {
   pl.off_reset = take((n - 1) * 4);
   pl.off_dAp = take(n * d * N * 4);
   pl.off_dDp = take(n * d * 4);
-  pl.off_dBp = take(t * size_t(pl.dtiles) * N * 4);
-  pl.off_dCp = take(t * size_t(pl.dtiles) * N * 4);
+  pl.off_dBCp = take(t * size_t(pl.dtiles) * 2 * N * 4);
   pl.total = off;
   return pl;
 }
@@ -372,16 +378,24 @@ ssm_status_t run_bwd(PackedBwdParams p, hipStream_t s) {
   if (ssm_status_t st = grid_ok(int64_t(p.nc) * p.dtiles)) return st;
   if (p.nc > 1) {
     p.nwg = (p.nc - 1) * p.dtiles;
-    hipLaunchKernelGGL((k_packed_bwd_summary<N, InT, DISC>), dim3(uint32_t(p.nwg)), dim3(kWave), 0, s, p);
+    bool odd = false;
+    if constexpr (!std::is_same<InT, float>::value && N > 1) {
+      odd = odd_rows(p.Cm, p.cs);
+      if (odd)
+        hipLaunchKernelGGL((k_packed_bwd_summary<N, InT, DISC, true>), dim3(uint32_t(p.nwg)), dim3(kWave), 0, s, p);
+    }
+    if (!odd)
+      hipLaunchKernelGGL((k_packed_bwd_summary<N, InT, DISC, false>), dim3(uint32_t(p.nwg)), dim3(kWave), 0, s, p);
     if (ssm_status_t st = launch_status("k_packed_bwd_summary")) return st;
-    hipLaunchKernelGGL((k_packed_bwd_carry<N>), dim3(uint32_t((DN + kWave - 1) / kWave)), dim3(kWave), 0, s, p);
+    hipLaunchKernelGGL((k_packed_bwd_carry<N>), dim3(uint32_t((DN + kWave - 1) / kWave)), dim3(kWave * kCarryWaves), 0, s,
+                       p);
     if (ssm_status_t st = launch_status("k_packed_bwd_carry")) return st;
   }
   p.nwg = p.nc * p.dtiles;
   hipLaunchKernelGGL((k_packed_bwd<N, InT, DISC>), dim3(uint32_t(p.nwg)), dim3(kWave * BwdLayout<N>::NG), 0, s, p);
   if (ssm_status_t st = launch_status("k_packed_bwd")) return st;
   if (p.q.tokens > 0) {
-    const int64_t n = (int64_t(p.q.tokens) * N + 255) / 256;
+    const int64_t n = (int64_t(p.q.tokens) * 2 * N + 255) / 256;
     hipLaunchKernelGGL((k_packed_bwd_bc<N>), dim3(uint32_t(n)), dim3(256), 0, s, p);
     if (ssm_status_t st = launch_status("k_packed_bwd_bc")) return st;
   }
@@ -458,8 +472,8 @@ ssm_status_t ssm_packed_scan_fwd(const ssm_packed_scan_args_t* a, void* hip_stre
   p.xs = a->x_stride;
   p.dls = a->delta_stride;
   p.zs = a->z ? a->z_stride : 0;
-  p.bs = a->b_stride;
-  p.cs = a->c_stride;
+  p.bs = uint32_t(a->b_stride);
+  p.cs = uint32_t(a->c_stride);
   p.D = a->dim;
   p.q = Seqs{a->offsets, a->slot, a->resume, int32_t(a->tokens), int32_t(a->seqs), 0, int32_t(a->slots)};
   p.T = int32_t(pl.T);
@@ -467,7 +481,6 @@ ssm_status_t ssm_packed_scan_fwd(const ssm_packed_scan_args_t* a, void* hip_stre
   p.dtiles = int32_t(pl.dtiles);
   p.exact_thr = exact_threshold(a->disc, a->dtype);
   p.dt_mode = dt_mode_of(a->delta_bias, a->delta_softplus);
-  p.rows_ok = rows_ok(a->Bm, a->Cm, a->b_stride, a->c_stride, a->dtype);
   return dispatch<kFwd>(p, a->dstate, a->dtype, a->disc, static_cast<hipStream_t>(hip_stream));
 }
 
@@ -535,12 +548,11 @@ ssm_status_t ssm_packed_scan_bwd(const ssm_packed_scan_bwd_args_t* a, void* hip_
   p.reset = reinterpret_cast<int32_t*>(ws + pl.off_reset);
   p.dAp = reinterpret_cast<float*>(ws + pl.off_dAp);
   p.dDp = reinterpret_cast<float*>(ws + pl.off_dDp);
-  p.dBp = reinterpret_cast<float*>(ws + pl.off_dBp);
-  p.dCp = reinterpret_cast<float*>(ws + pl.off_dCp);
+  p.dBCp = reinterpret_cast<float*>(ws + pl.off_dBCp);
   p.xs = a->x_stride;
   p.dls = a->delta_stride;
-  p.bs = a->b_stride;
-  p.cs = a->c_stride;
+  p.bs = uint32_t(a->b_stride);
+  p.cs = uint32_t(a->c_stride);
   p.ys = a->dy_stride;
   p.D = a->dim;
   p.q = Seqs{a->offsets, nullptr, nullptr, int32_t(a->tokens), int32_t(a->seqs), 0, int32_t(a->seqs)};
@@ -548,7 +560,6 @@ ssm_status_t ssm_packed_scan_bwd(const ssm_packed_scan_bwd_args_t* a, void* hip_
   p.nc = int32_t(pl.nc);
   p.dtiles = int32_t(pl.dtiles);
   p.exact_thr = exact_threshold(a->disc, a->dtype);
-  p.rows_ok = rows_ok(a->Bm, a->Cm, a->b_stride, a->c_stride, a->dtype);
   return dispatch<kBwd>(p, a->dstate, a->dtype, a->disc, static_cast<hipStream_t>(hip_stream));
 }
 

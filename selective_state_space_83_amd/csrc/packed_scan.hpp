@@ -47,30 +47,48 @@ struct PackedParams {
   float* hsum;           // (nc - 1, D, N)  states the chunks reach, then carries
   float* hstart;         // (nc - 1, D, N)  initial states kept for the output pass, or null
   int32_t* reset;        // (nc - 1)        1: nothing from before the chunk leaves it
-  int64_t xs, dls, zs, bs, cs;   // row strides
+  int64_t xs, dls, zs;   // row strides
+  uint32_t bs, cs;
   int64_t D;
   Seqs q;
   int32_t T, nc;         // tokens per chunk, chunks
   int32_t dtiles, nwg;
   float exact_thr;
   int32_t dt_mode;
-  int32_t rows_ok;       // bf16 rows of B and C start on 4 bytes
 };
 
-// A row of B or C into scalar registers.  bf16 rows that start on an odd element
-// are read by elements.
-template <int N, typename InT>
-__device__ __forceinline__ void row_of(float (&r)[N], const InT* p, bool ok) {
-  if constexpr (std::is_same<InT, float>::value || N == 1) {
-    load_row<N>(r, p);
-  } else if (ok) {
-    load_row<N>(r, p);
-  } else {
+// A row of B or C in scalar registers, as it lies in memory; bf16 rows are widened
+// when their step comes, so that the row requested ahead takes half the registers
+// (the steps of 16 states have none to spare).  ODD: bf16 rows may start on an odd
+// element; they are read by elements, which waits for each row.
+template <int N, typename InT, bool ODD>
+struct Row {
+  static constexpr bool kWide = std::is_same<InT, float>::value;
+  static constexpr int W = kWide || N == 1 ? N : N / 2;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const InT* p) {
+    if constexpr (kWide) {
+      const_u32_ptr q = (const_u32_ptr)(p);
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k] = q[k];
+    } else if constexpr (N == 1 || ODD) {
+      uint32_t v[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] = __builtin_amdgcn_readfirstlane(uint32_t(p[n]));
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k] = N == 1 ? v[0] : v[2 * k % N] | v[(2 * k + 1) % N] << 16;
+    } else {
+      const_u32_ptr q = (const_u32_ptr)(p);
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k] = q[k];
+    }
+  }
+  __device__ __forceinline__ void widen(float (&r)[N]) const {
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      r[n] = __uint_as_float(__builtin_amdgcn_readfirstlane(uint32_t(__builtin_bit_cast(uint16_t, p[n])) << 16));
+      r[n] = __uint_as_float(kWide ? w[n] : N == 1 || n % 2 == 0 ? w[n / 2] << 16 : w[n / 2] & 0xffff0000u);
   }
-}
+};
 
 // Rows of one array in a chunk: a buffer window at the wave's channels.
 struct RowWindow {
@@ -86,6 +104,16 @@ __device__ __forceinline__ RowWindow window(const void* p, int64_t stride, int64
   const int64_t wide = (D - dbase < kWave ? D - dbase : kWave) * int64_t(sizeof(InT));
   w.r = make_rsrc(base, steps > 0 ? uint32_t((steps - 1) * int64_t(w.row) + wide) : 0u);
   return w;
+}
+
+// The kernel's arguments, read again: what only the ends of sequences need would
+// otherwise stay in scalar registers through the steps, which have none to spare.
+template <typename P>
+__device__ __forceinline__ const P& args_again() {
+  typedef const P __attribute__((address_space(4)))* arg_ptr;
+  arg_ptr p = (arg_ptr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const P*)p;
 }
 
 template <int N>
@@ -105,7 +133,7 @@ __device__ __forceinline__ void zero_n(float (&h)[N]) {
 }
 
 // Pass 1: what each chunk but the last hands on.
-template <int N, typename InT, int DISC>
+template <int N, typename InT, int DISC, bool ODD>
 __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) k_packed_summary(const PackedParams p) {
   constexpr int kU = kUnrollSum;
   constexpr bool kScaled = DISC == kZoh;   // carries A h (see ssm_step_lane)
@@ -154,9 +182,8 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
   const uint32_t lane = lo_ch * sizeof(InT);
   constexpr InT* kIn = nullptr;
   const InT* Brow = static_cast<const InT*>(p.Bm) + int64_t(from) * p.bs;
-  const bool ok = p.rows_ok != 0;
-  float Bb0[N], Bb1[N];
-  row_of<N>(Bb0, Brow, ok);
+  Row<N, InT, ODD> Bb0, Bb1;
+  Bb0.load(Brow);
 
   float dacc = 0.0f, dcomp = 0.0f;   // Kahan sum of Delta, as in the scan's summaries
   auto sum_add = [&](float v) {
@@ -165,11 +192,13 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
     dacc = tv;
   };
   // the next row is requested after this step's has been waited for (see chunk_loop)
-  auto one_step = [&](float xv, float dv, bool has_next, float (&Bcur)[N], float (&Bnext)[N]) {
-    const InT* nb = Brow + (has_next ? p.bs : 0);
-    if constexpr (N >= 2) asm volatile("" : "+s"(nb) : "s"(Bcur[0]));
-    row_of<N>(Bnext, nb, ok);
-    ssm_step_any<N, DISC, false, kScaled>(h, cc, Bcur, Bcur, xv, dv);
+  auto one_step = [&](float xv, float dv, const Row<N, InT, ODD>& Bcur, Row<N, InT, ODD>& Bnext) {
+    const InT* nb = Brow + p.bs;
+    asm volatile("" : "+s"(nb) : "s"(Bcur.w[0]));
+    Bnext.load(nb);
+    float Bv[N];
+    Bcur.widen(Bv);
+    ssm_step_any<N, DISC, false, kScaled>(h, cc, Bv, Bv, xv, dv);
     Brow = nb;
   };
   float xc[kU], dc[kU];
@@ -179,44 +208,44 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
     xc[j] = ldb(wx.r, lane, at(j) * wx.row, kIn);
     dc[j] = ldb(wd.r, lane, at(j) * wd.row, kIn);
   }
-  for (int32_t tb = 0; tb < steps; tb += kU) {
+  int32_t t = 0;
+  for (; t + kU < steps; t += kU) {
     float xn[kU], dn[kU];
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
-      xn[j] = ldb(wx.r, lane, at(tb + kU + j) * wx.row, kIn);
-      dn[j] = ldb(wd.r, lane, at(tb + kU + j) * wd.row, kIn);
+      xn[j] = ldb(wx.r, lane, at(t + kU + j) * wx.row, kIn);
+      dn[j] = ldb(wd.r, lane, at(t + kU + j) * wd.row, kIn);
     }
     if (dtm != kDtRaw) {
 #pragma unroll
       for (int j = 0; j < kU; ++j) dc[j] = dt_transform(dc[j], dtb, dtm);
     }
-    if (tb + kU <= steps) {
-      float bs = 0.0f;
+    float bs = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kU; j += 2) {
-        one_step(xc[j], dc[j], true, Bb0, Bb1);
-        one_step(xc[j + 1], dc[j + 1], tb + j + 2 < steps, Bb1, Bb0);
-        bs += dc[j] + dc[j + 1];
-      }
-      sum_add(bs);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kU; j += 2) {
-        if (tb + j < steps) {
-          one_step(xc[j], dc[j], tb + j + 1 < steps, Bb0, Bb1);
-          sum_add(dc[j]);
-        }
-        if (tb + j + 1 < steps) {
-          one_step(xc[j + 1], dc[j + 1], tb + j + 2 < steps, Bb1, Bb0);
-          sum_add(dc[j + 1]);
-        }
-      }
+    for (int j = 0; j < kU; j += 2) {
+      one_step(xc[j], dc[j], Bb0, Bb1);
+      one_step(xc[j + 1], dc[j + 1], Bb1, Bb0);
+      bs += dc[j] + dc[j + 1];
     }
+    sum_add(bs);
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
       xc[j] = xn[j];
       dc[j] = dn[j];
     }
+  }
+  // the last block, step by step; no row behind its last is read
+#pragma unroll 1
+  for (; t < steps; ++t) {
+    const float xv = ldb(wx.r, lane, uint32_t(t) * wx.row, kIn);
+    float dv = ldb(wd.r, lane, uint32_t(t) * wd.row, kIn);
+    if (dtm != kDtRaw) dv = dt_transform(dv, dtb, dtm);
+    float Bv[N];
+    Bb0.widen(Bv);
+    ssm_step_any<N, DISC, false, kScaled>(h, cc, Bv, Bv, xv, dv);
+    sum_add(dv);
+    Brow += t + 1 < steps ? p.bs : 0u;
+    Bb0.load(Brow);
   }
   if constexpr (kScaled) {
 #pragma unroll
@@ -226,43 +255,72 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
   p.dsum[int64_t(chunk) * p.D + d] = dacc - dcomp;
 }
 
-// Pass 2: carries.  One lane per (channel, state) walks the chunks; hsum of chunk c
-// becomes the state that enters chunk c + 1.
-template <int N>
-__global__ void __launch_bounds__(kWave) k_packed_carry(const PackedParams p) {
-  constexpr int U = 8;
-  const int64_t i = int64_t(blockIdx.x) * kWave + threadIdx.x, DN = p.D * N;
-  if (i >= DN) return;
-  const float a2 = p.A[i] * kLog2e;
-  const float* ds = p.dsum + i / N;
-  float* hs = p.hsum + i;
+// Pass 2: carries; hsum of chunk c becomes the state that enters chunk c + 1.  A lane
+// per (channel, state); the 16 waves of a workgroup share the chunks of its 64.  Each
+// folds its share from zero, takes the state that enters it from the shares
+// before (in LDS), and walks it again.  A chunk's fold is 25 instructions, so one wave
+// walking 512 chunks alone takes 50 us, which nothing else overlaps.
+constexpr int kCarryWaves = 16;
+
+template <int N, bool REV>
+__device__ __forceinline__ void carry_walk(const float* A, const float* dsum, float* hsum, const int32_t* reset, int64_t D,
+                                           int32_t n) {
+  constexpr int U = 8;   // chunks whose loads are issued before they are folded
+  __shared__ float end[kCarryWaves][kWave];
+  __shared__ float span[kCarryWaves][kWave];
+  __shared__ int32_t cut[kCarryWaves];
+  const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), lane = threadIdx.x % kWave;
+  const int64_t DN = D * N, i0 = int64_t(blockIdx.x) * kWave + lane, i = i0 < DN ? i0 : DN - 1;
+  const float a2 = A[i] * kLog2e;
+  const float* ds = dsum + i / N;
+  float* hs = hsum + i;
+  const int32_t share = (n + kCarryWaves - 1) / kCarryWaves;
+  const int32_t c0 = w * share < n ? w * share : n, c1 = c0 + share < n ? c0 + share : n;
+  auto place = [&](int32_t c) { return int64_t(REV ? n - 1 - c : c); };
+  // REV: the chunks from the last to the first
+  auto walk = [&](float carry, auto&& each) {
+    for (int32_t c = c0; c < c1; c += U) {
+      float sv[U], hv[U];
+      int32_t rv[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int64_t at = place(c + j < c1 ? c + j : c1 - 1);
+        sv[j] = ds[at * D];
+        hv[j] = hs[at * DN];
+        rv[j] = reset[at];
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (c + j < c1) {
+          carry = rv[j] ? hv[j] : decay_add(a2 * sv[j], carry, hv[j]);
+          each(c + j, sv[j], rv[j], carry);
+        }
+    }
+    return carry;
+  };
+  double sum = 0.0;   // of Delta, while no chunk starts anew
+  int32_t anew = 0;
+  end[w][lane] = walk(0.0f, [&](int32_t, float sv, int32_t rv, float) {
+    sum += sv;
+    anew |= rv;
+  });
+  span[w][lane] = float(sum);
+  if (lane == 0) cut[w] = anew;
+  __syncthreads();
   float carry = 0.0f;
-  const int32_t n = p.nc - 1;
-  int32_t c = 0;
-  for (; c + U <= n; c += U) {
-    float sv[U], hv[U];
-    int32_t rv[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      sv[j] = ds[(c + j) * p.D];
-      hv[j] = hs[(c + j) * DN];
-      rv[j] = p.reset[c + j];
-    }
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      carry = rv[j] ? hv[j] : decay_add(a2 * sv[j], carry, hv[j]);
-      hs[(c + j) * DN] = carry;
-    }
-  }
-  for (; c < n; ++c) {
-    const float hv = hs[c * DN];
-    carry = p.reset[c] ? hv : decay_add(a2 * ds[c * p.D], carry, hv);
-    hs[c * DN] = carry;
-  }
+  for (int v = 0; v < w; ++v) carry = cut[v] ? end[v][lane] : decay_add(a2 * span[v][lane], carry, end[v][lane]);
+  walk(carry, [&](int32_t c, float, int32_t, float now) {
+    if (i0 < DN) hs[place(c) * DN] = now;
+  });
+}
+
+template <int N>
+__global__ void __launch_bounds__(kWave * kCarryWaves) k_packed_carry(const PackedParams p) {
+  carry_walk<N, false>(p.A, p.dsum, p.hsum, p.reset, p.D, p.nc - 1);
 }
 
 // Pass 3 (or the only one): every chunk from the state that enters it.
-template <int N, typename InT, int DISC, bool GATE>
+template <int N, typename InT, int DISC, bool GATE, bool ODD>
 __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) k_packed_out(const PackedParams p) {
   constexpr int kU = kUnrollOut;
   const int wg = xcd_remap(blockIdx.x, p.nwg);
@@ -278,43 +336,35 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
   float h[N];
   zero_n(h);
 
-  // sequence `open` holds the tokens walked (none: -1), `next` is where it ends or, with
-  // none, where sequence s begins
-  int32_t s = seqs_before(p.q, from), open = -1;
-  int32_t next = s < p.q.S ? seq_start(p.q, s) : INT32_MAX;
-  if (chunk > 0 && s > 0 && from < to) {
-    const int32_t end = seq_start(p.q, s);
-    if (end > from) {
-      open = s - 1;
-      next = end;
-      load_n(h, p.hsum + (int64_t(chunk) - 1) * DN + d * N);
-    }
+  // s: the first sequence not begun; open: sequence s - 1 holds the tokens walked
+  int32_t s = seqs_before(p.q, from);
+  bool open = false;
+  if (chunk > 0 && s > 0 && from < to && seq_start(p.q, s) > from) {
+    open = true;
+    load_n(h, p.hsum + (int64_t(chunk) - 1) * DN + d * N);
   }
-  auto finish = [&] {
-    if (open < 0) return;
-    const int32_t slot = p.h_last ? seq_slot(p.q, open) : -1;
-    if (slot >= 0) store_n(p.h_last + int64_t(slot) * DN + d * N, h);
-    open = -1;
+  // where the open sequence ends, or else the next one begins
+  auto next_of = [&](const PackedParams& a) { return open || s < a.q.S ? seq_start(a.q, s) : INT32_MAX; };
+  auto finish = [&](const PackedParams& a) {
+    if (!open) return;
+    const int32_t slot = a.h_last ? seq_slot(a.q, s - 1) : -1;
+    if (slot >= 0) store_n(a.h_last + (int64_t(slot) * a.D + d) * N, h);
+    open = false;
   };
   // At token t the open sequence has ended; empty ones pass their state on, and the
   // one that holds t is opened.
-  auto meet = [&](int32_t t) {
-    finish();
-    next = INT32_MAX;
-    for (; s < p.q.S && seq_start(p.q, s) <= t; ++s) {
-      const int32_t end = seq_start(p.q, s + 1), slot = seq_slot(p.q, s);
-      const bool given = p.h0 && slot >= 0 && seq_resumed(p.q, s);
+  auto meet = [&](const PackedParams& a, int32_t t) {
+    finish(a);
+    const int64_t last = int64_t(chunk + 1) * a.T;   // (past 32 bits in the last chunk)
+    while (!open && s < a.q.S && seq_start(a.q, s) <= t) {
+      const int32_t end = seq_start(a.q, s + 1), slot = seq_slot(a.q, s);
+      const bool given = a.h0 && slot >= 0 && seq_resumed(a.q, s);
       zero_n(h);
-      if (given) load_n(h, end > t1 && p.hstart ? p.hstart + int64_t(chunk) * DN + d * N : p.h0 + int64_t(slot) * DN + d * N);
-      open = s;
-      if (end > t) {
-        ++s;
-        next = end;
-        return;
-      }
-      finish();
+      if (given) load_n(h, (end > last && a.hstart ? a.hstart + int64_t(chunk) * a.D * N : a.h0 + int64_t(slot) * a.D * N) + d * N);
+      open = true;
+      ++s;
+      if (end <= t) finish(a);
     }
-    if (s < p.q.S) next = seq_start(p.q, s);
   };
 
   const float dsk = p.Dskip ? p.Dskip[d] : 0.0f;
@@ -331,37 +381,55 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
     constexpr InT* kIn = nullptr;
     const InT* Brow = static_cast<const InT*>(p.Bm) + int64_t(from) * p.bs;
     const InT* Crow = static_cast<const InT*>(p.Cm) + int64_t(from) * p.cs;
-    const bool ok = p.rows_ok != 0;
-    float Bb0[N], Bb1[N], Cb0[N], Cb1[N];
-    row_of<N>(Bb0, Brow, ok);
-    row_of<N>(Cb0, Crow, ok);
-    // where the walk stops to keep a state or to change sequences
-    int32_t keep = p.hsave ? (from + kSaveStride - 1) / kSaveStride * kSaveStride : INT32_MAX;
-    if (keep == 0) keep = kSaveStride;
-    int32_t stop = next < keep ? next : keep;
-    auto halt = [&](int32_t t) {
-      if (t == keep) {
-        store_n(p.hsave + (int64_t(t / kSaveStride) - 1) * DN + d * N, h);
-        keep += kSaveStride;
-      }
-      if (next <= t) meet(t);
-      stop = next < keep ? next : keep;
+    using R = Row<N, InT, ODD>;
+    R Bb0, Bb1;
+    Bb0.load(Brow);
+    // where the walk stops to keep a state (before tokens 16, 32, ...) or to change
+    // sequences, and the step before which it goes block by block (the last step's next
+    // row is not there to be read)
+    int32_t stop, whole;
+    auto set_stop = [&](const PackedParams& a, int32_t t) {
+      const int32_t keep = a.hsave ? (t / kSaveStride + 1) * kSaveStride : INT32_MAX, next = next_of(a);
+      stop = (next < keep ? next : keep) - from;
+      whole = stop < steps - 1 ? stop : steps - 1;
     };
-    auto one_step = [&](float xv, float dv, float zv, bool has_next, float (&Bcur)[N], float (&Bnext)[N],
-                        float (&Ccur)[N], float (&Cnext)[N]) {
-      const InT* nb = Brow + (has_next ? p.bs : 0);
-      const InT* nc = Crow + (has_next ? p.cs : 0);
-      // the next rows are requested after this step's have been waited for (see chunk_loop)
-      if constexpr (N >= 2) asm volatile("" : "+s"(nb), "+s"(nc) : "s"(Bcur[0]), "s"(Ccur[0]));
-      row_of<N>(Bnext, nb, ok);
-      row_of<N>(Cnext, nc, ok);
-      const float acc = ssm_step_any<N, DISC, true>(h, cc, Bcur, Ccur, xv, dv);
-      float yv = fmaf(dsk, xv, acc);
+    auto halt = [&](int32_t t) {
+      const PackedParams& a = args_again<PackedParams>();
+      if (a.hsave && t % kSaveStride == 0 && t > 0)
+        store_n(a.hsave + ((int64_t(t / kSaveStride) - 1) * a.D + d) * N, h);
+      if (next_of(a) <= t) meet(a, t);
+      set_stop(a, t);
+    };
+    halt(from);
+    // B's next row and C's own are requested once this step's B has been waited for
+    // (scalar loads come back in any order, so a wait is for all of them): the states'
+    // update covers both.  (C a step ahead too takes 16 registers more, which spilled:
+    // 16384 x 1536 x 16 fp32 %OLD% us, this %NEW%.)
+    auto one_step = [&](float xv, float dv, float zv, uint32_t ahead, const R& Bcur, R& Bnext) {
+      const InT* nb = Brow + ahead;
+      const InT* nc = Crow;
+      asm volatile("" : "+s"(nb), "+s"(nc) : "s"(Bcur.w[0]));
+      R Ccur;
+      Ccur.load(nc);
+      Bnext.load(nb);
+      float Bv[N], Cv[N];
+      Bcur.widen(Bv);
+      ssm_step_any<N, DISC, false>(h, cc, Bv, Bv, xv, dv);
+      Ccur.widen(Cv);
+      float even = 0.0f, odd = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (n & 1)
+          odd = fmaf(Cv[n], h[n], odd);
+        else
+          even = fmaf(Cv[n], h[n], even);
+      }
+      float yv = fmaf(dsk, xv, even + odd);
       if constexpr (GATE) yv *= silu(zv);
       stb(wy.r, lane, yoff, yv, static_cast<InT*>(nullptr));
       yoff += wy.row;
       Brow = nb;
-      Crow = nc;
+      Crow = nc + p.cs;
     };
     float xc[kU], dc[kU], zc[kU];
     auto at = [&](int32_t t) { return uint32_t(t < steps ? t : steps - 1); };
@@ -383,15 +451,24 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
 #pragma unroll
         for (int j = 0; j < kU; ++j) dc[j] = dt_transform(dc[j], dtb, dtm);
       }
+      if (tb == stop) halt(from + tb);
+      if (tb + kU <= whole) {
 #pragma unroll
-      for (int j = 0; j < kU; j += 2) {
-        if (tb + j < steps) {
-          if (from + tb + j == stop) halt(from + tb + j);
-          one_step(xc[j], dc[j], zc[j], tb + j + 1 < steps, Bb0, Bb1, Cb0, Cb1);
+        for (int j = 0; j < kU; j += 2) {
+          one_step(xc[j], dc[j], zc[j], p.bs, Bb0, Bb1);
+          one_step(xc[j + 1], dc[j + 1], zc[j + 1], p.bs, Bb1, Bb0);
         }
-        if (tb + j + 1 < steps) {
-          if (from + tb + j + 1 == stop) halt(from + tb + j + 1);
-          one_step(xc[j + 1], dc[j + 1], zc[j + 1], tb + j + 2 < steps, Bb1, Bb0, Cb1, Cb0);
+      } else {
+        // a stop within the block, or the last block: step by step
+#pragma unroll 1
+        for (int32_t t = tb; t < tb + kU && t < steps; ++t) {
+          if (t == stop) halt(from + t);
+          const float xv = ldb(wx.r, lane, uint32_t(t) * wx.row, kIn);
+          float dv = ldb(wd.r, lane, uint32_t(t) * wd.row, kIn);
+          const float zv = GATE ? ldb(wz.r, lane, uint32_t(t) * wz.row, kIn) : 0.0f;
+          if (dtm != kDtRaw) dv = dt_transform(dv, dtb, dtm);
+          one_step(xv, dv, zv, t + 1 < steps ? p.bs : 0u, Bb0, Bb1);
+          Bb0 = Bb1;
         }
       }
 #pragma unroll
@@ -405,10 +482,11 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
   // behind the last token walked: the sequence that ends there, and the empty ones
   // whose place is in this chunk
   const int32_t at = from > to ? from : to;
-  if (at < t1 || t1 == p.q.tokens) {
-    if (next <= at || open >= 0) meet(at);
-  } else if (open >= 0 && next <= at) {
-    finish();
+  const PackedParams& a = args_again<PackedParams>();
+  if (at < t1 || t1 == a.q.tokens) {
+    if (open || next_of(a) <= at) meet(a, at);
+  } else if (open && next_of(a) <= at) {
+    finish(a);
   }
 }
 
