@@ -173,10 +173,8 @@ k_packed_bwd(const PackedBwdParams p) {
   // of the sequences that begin among 16 tokens, at the place of their first token:
   // which one it is, and which one ends before it (each wave its own)
   __shared__ int32_t ids[NG][2][F];
-  // bf16 rows of B and C, widened once, double-buffered by 16 tokens; fp32 rows go
-  // through scalar loads
-  constexpr bool kRowsLds = !std::is_same<InT, float>::value;
-  __shared__ __attribute__((aligned(16))) float rows[kRowsLds ? 2 : 1][2][kRowsLds ? F : 1][N];
+  // rows of B and C as fp32, double-buffered by 16 tokens
+  __shared__ __attribute__((aligned(16))) float rows[2][2][F][N];
 
   const int wg = xcd_remap(blockIdx.x, p.nwg);
   const int32_t dtile = wg % p.dtiles;
@@ -197,7 +195,7 @@ k_packed_bwd(const PackedBwdParams p) {
   ChanConst<NS, DISC> cc;
   load_chan<NS, DISC>(cc, p.A + dn, p.exact_thr);
   const float dsk = p.Dskip ? p.Dskip[d] : 0.0f;
-  constexpr bool kShortSeries = kRowsLds;
+  constexpr bool kShortSeries = !std::is_same<InT, float>::value;
   float zoh_thr = 0.0f;   // below it ZOH's factor is taken from its series
   if constexpr (DISC == kZoh) {
     float amin = __builtin_inff();
@@ -242,7 +240,7 @@ k_packed_bwd(const PackedBwdParams p) {
 
   // the rows each thread moves into LDS, loaded 16 tokens ahead (rows of tokens of no
   // sequence as 0)
-  constexpr int kRowVals = kRowsLds ? 2 * F * N : 1;
+  constexpr int kRowVals = 2 * F * N;
   constexpr int RV = (kRowVals + kWave * NG - 1) / (kWave * NG);
   float rpre[RV];
   auto rows_load = [&](const PackedBwdParams& a, int32_t f0) {
@@ -257,7 +255,7 @@ k_packed_bwd(const PackedBwdParams p) {
     }
   };
   const int32_t f_top = (t1 - 1) / F * F;
-  if constexpr (kRowsLds) rows_load(p, f_top);
+  rows_load(p, f_top);
   int rb = 0;
 
   for (int32_t f0 = f_top; f0 >= t0; f0 -= F) {
@@ -289,28 +287,19 @@ k_packed_bwd(const PackedBwdParams p) {
       }
       for (int e = threadIdx.x; e < len * 2 * N; e += kWave * NG)
         stb(rs, uint32_t(e / (2 * N)) * sums_row + uint32_t(e % (2 * N)) * 4u, 0, 0.0f, kF);
-      if constexpr (kRowsLds) {
-        if (f0 > t0) rows_load(a, f0 - F);
-      }
+      if (f0 > t0) rows_load(a, f0 - F);
       continue;
     }
-    if constexpr (kRowsLds) {
 #pragma unroll
-      for (int i = 0; i < RV; ++i) {
-        const int e = static_cast<int>(threadIdx.x) + i * kWave * NG;
-        if (e < kRowVals) (&rows[rb][0][0][0])[e] = rpre[i];
-      }
-      __syncthreads();
-      if (f0 > t0) rows_load(a, f0 - F);
+    for (int i = 0; i < RV; ++i) {
+      const int e = static_cast<int>(threadIdx.x) + i * kWave * NG;
+      if (e < kRowVals) (&rows[rb][0][0][0])[e] = rpre[i];
     }
-    const float* Brow = &rows[kRowsLds ? rb : 0][0][0][n0];
-    const float* Crow = &rows[kRowsLds ? rb : 0][1][0][n0];
+    __syncthreads();
+    if (f0 > t0) rows_load(a, f0 - F);
     const RowWindow wx = window<InT>(a.x, a.xs, a.D, dbase, f0, len);
     const RowWindow wd = window<InT>(a.delta, a.dls, a.D, dbase, f0, len);
     const RowWindow wy = window<InT>(a.dy, a.ys, a.D, dbase, f0, len);
-    const InT* Bc = static_cast<const InT*>(a.Bm) + int64_t(f0) * a.bs + n0;
-    const InT* Cc = static_cast<const InT*>(a.Cm) + int64_t(f0) * a.cs + n0;
-    const uint32_t bs = a.bs, cs = a.cs;
     auto in = [&](int j) { return uint32_t(j < len ? j : len - 1); };   // a row of the tensors
     const float* hin = f0 > 0 ? a.hsave + (int64_t(f0 / F) - 1) * a.D * N + dn : nullptr;
     // the state before the first token of a sequence
@@ -319,56 +308,43 @@ k_packed_bwd(const PackedBwdParams p) {
       zero_n(h);
       if (b.h0) load_n(h, b.h0 + int64_t(__builtin_amdgcn_readfirstlane(ids[w][0][j])) * b.D * N + dn);
     };
-#pragma unroll
-    for (int half = F / H - 1; half >= 0; --half) {
-      const int j0 = half * H;
+    // The later half first: from the state kept, through the earlier half, its own steps
+    // forwards with the states between them in registers, and back.  (A rolled loop:
+    // both halves' steps unrolled are 56 KB of instructions.)
+#pragma unroll 1
+    for (int j0 = F - H; j0 >= 0; j0 -= H) {
       if (j0 >= len) continue;   // wave-uniform
+      const uint32_t live_h = live >> j0, begins_h = begins >> j0;
+      const float* Brow = &rows[rb][0][j0][n0];
+      const float* Crow = &rows[rb][1][j0][n0];
       float h[NS];
       zero_n(h);
       if (hin) load_n(h, hin);
-      // the state after the step before each step of the half
-      float stash[H][NS];
+      auto forward = [&](float xv, float dv, const float* row) {
+        float Bv[NS];
+        lds_row<NS>(Bv, row);
+        if (any_exact<NS, DISC>(cc, dv))
+          ssm_step_lane<NS, DISC, false, true, true>(h, cc, Bv, Bv, xv, dv);
+        else
+          ssm_step_lane<NS, DISC, false, false>(h, cc, Bv, Bv, xv, dv);
+      };
       float xa[K], da[K];
+      auto rows_of = [&](float (&u)[K], float (&v)[K], int j) {
 #pragma unroll
-      for (int jj = 0; jj < K; ++jj) {
-        xa[jj] = ldb(wx.r, lane_in, in(jj) * wx.row, kIn);
-        da[jj] = ldb(wd.r, lane_in, in(jj) * wd.row, kIn);
-      }
-#pragma unroll
-      for (int jb = 0; jb < (j0 + H) / K; ++jb) {
+        for (int jj = 0; jj < K; ++jj) {
+          u[jj] = ldb(wx.r, lane_in, in(j + jj) * wx.row, kIn);
+          v[jj] = ldb(wd.r, lane_in, in(j + jj) * wd.row, kIn);
+        }
+      };
+      rows_of(xa, da, 0);
+#pragma unroll 1
+      for (int jb = 0; jb < j0; jb += K) {
         float xn[K], dn_[K];
-        const int nb = (jb + 1 < (j0 + H) / K) ? jb + 1 : jb;
+        rows_of(xn, dn_, jb + K);
 #pragma unroll
         for (int jj = 0; jj < K; ++jj) {
-          xn[jj] = ldb(wx.r, lane_in, in(nb * K + jj) * wx.row, kIn);
-          dn_[jj] = ldb(wd.r, lane_in, in(nb * K + jj) * wd.row, kIn);
-        }
-        float Bb[K][NS];
-        if constexpr (!kRowsLds) {
-#pragma unroll
-          for (int jj = 0; jj < K; ++jj) load_row<NS>(Bb[jj], Bc + in(jb * K + jj) * bs);
-        }
-#pragma unroll
-        for (int jj = 0; jj < K; ++jj) {
-          const int j = jb * K + jj;
-          float Bv[NS];
-          if constexpr (kRowsLds) {
-            lds_row<NS>(Bv, Brow + j * N);
-          } else {
-#pragma unroll
-            for (int n = 0; n < NS; ++n) Bv[n] = Bb[jj][n];
-          }
-          if (j >= j0) {
-#pragma unroll
-            for (int n = 0; n < NS; ++n) stash[j - j0][n] = h[n];
-          }
-          if (begins >> j & 1) initial(h, j);
-          if (live >> j & 1) {
-            if (any_exact<NS, DISC>(cc, da[jj]))
-              ssm_step_lane<NS, DISC, false, true, true>(h, cc, Bv, Bv, xa[jj], da[jj]);
-            else
-              ssm_step_lane<NS, DISC, false, false>(h, cc, Bv, Bv, xa[jj], da[jj]);
-          }
+          if (begins >> (jb + jj) & 1) initial(h, jb + jj);
+          if (live >> (jb + jj) & 1) forward(xa[jj], da[jj], &rows[rb][0][jb + jj][n0]);
         }
 #pragma unroll
         for (int jj = 0; jj < K; ++jj) {
@@ -376,55 +352,57 @@ k_packed_bwd(const PackedBwdParams p) {
           da[jj] = dn_[jj];
         }
       }
+      // the state after the step before each step of the half
+      float stash[H][NS];
 #pragma unroll
-      for (int jb = (j0 + H) / K - 1; jb >= j0 / K; --jb) {
-        if (jb * K >= len) continue;   // wave-uniform
-        float ub[K], db[K], yb[K], Bb[K][NS], Cb[K][NS];
+      for (int jb = 0; jb < H; jb += K) {
+        float xn[K], dn_[K];
+        if (jb + K < H) rows_of(xn, dn_, j0 + jb + K);
 #pragma unroll
         for (int jj = 0; jj < K; ++jj) {
-          const uint32_t j = in(jb * K + jj);
+          const int js = jb + jj;
+#pragma unroll
+          for (int n = 0; n < NS; ++n) stash[js][n] = h[n];
+          if (begins_h >> js & 1) initial(h, j0 + js);
+          if (live_h >> js & 1) forward(xa[jj], da[jj], Brow + js * N);
+        }
+        if (jb + K < H) {
+#pragma unroll
+          for (int jj = 0; jj < K; ++jj) {
+            xa[jj] = xn[jj];
+            da[jj] = dn_[jj];
+          }
+        }
+      }
+#pragma unroll
+      for (int jb = H - K; jb >= 0; jb -= K) {
+        if (j0 + jb >= len) continue;   // wave-uniform
+        float ub[K], db[K], yb[K];
+#pragma unroll
+        for (int jj = 0; jj < K; ++jj) {
+          const uint32_t j = in(j0 + jb + jj);
           ub[jj] = ldb(wx.r, lane_in, j * wx.row, kIn);
           db[jj] = ldb(wd.r, lane_in, j * wd.row, kIn);
           yb[jj] = ldb(wy.r, lane_in, j * wy.row, kIn);
-          if constexpr (!kRowsLds) {
-            load_row<NS>(Bb[jj], Bc + j * bs);
-            load_row<NS>(Cb[jj], Cc + j * cs);
-          }
-        }
-        // keep the scalar row loads here, together
-        if constexpr (!kRowsLds && NS == 4) {
-#pragma unroll
-          for (int jj = 0; jj < K; ++jj)
-            asm volatile("" ::"s"(Bb[jj][0]), "s"(Bb[jj][1]), "s"(Bb[jj][2]), "s"(Bb[jj][3]),
-                         "s"(Cb[jj][0]), "s"(Cb[jj][1]), "s"(Cb[jj][2]), "s"(Cb[jj][3]));
         }
 #pragma unroll
         for (int jj = K - 1; jj >= 0; --jj) {
-          const int j = jb * K + jj;
+          const int js = jb + jj;
           float pB[NS], pC[NS], du = 0.0f, ddt = 0.0f;
           zero_n(pB);
           zero_n(pC);
-          const float u = ub[jj], dv = db[jj], dyv = yb[jj];
-          float Bv[NS], Cv[NS];
-          if constexpr (kRowsLds) {
-            lds_row<NS>(Bv, Brow + j * N);
-            lds_row<NS>(Cv, Crow + j * N);
-          } else {
-#pragma unroll
-            for (int n = 0; n < NS; ++n) {
-              Bv[n] = Bb[jj][n];
-              Cv[n] = Cb[jj][n];
-            }
-          }
-          if (live >> j & 1) {
-            const int js = j - j0;
+          if (live_h >> js & 1) {
+            const float u = ub[jj], dv = db[jj], dyv = yb[jj];
+            float Bv[NS], Cv[NS];
+            lds_row<NS>(Bv, Brow + js * N);
+            lds_row<NS>(Cv, Crow + js * N);
             float hp[NS], hn[NS];   // the states before and after the step
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
               hp[n] = stash[js][n];
               hn[n] = (js + 1 < H) ? stash[js + 1 < H ? js + 1 : js][n] : h[n];
             }
-            if (begins >> j & 1) initial(hp, j);
+            if (begins_h >> js & 1) initial(hp, j0 + js);
             const bool exact = any_exact<NS, DISC>(cc, dv);
             const bool series = DISC == kZoh && __builtin_amdgcn_ballot_w64(dv < zoh_thr) != 0;
             if (series)
@@ -434,10 +412,10 @@ k_packed_bwd(const PackedBwdParams p) {
               bwd_lane_step<NS, DISC, false, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, exact, pB, pC, du,
                                                            ddt);
             dDacc = fmaf(dyv, u, dDacc);
-            if (begins >> j & 1) {
+            if (begins_h >> js & 1) {
               const PackedBwdParams& b = args_again<PackedBwdParams>();
-              const int32_t s = __builtin_amdgcn_readfirstlane(ids[w][0][j]);
-              const int32_t before = __builtin_amdgcn_readfirstlane(ids[w][1][j]);
+              const int32_t s = __builtin_amdgcn_readfirstlane(ids[w][0][j0 + js]);
+              const int32_t before = __builtin_amdgcn_readfirstlane(ids[w][1][j0 + js]);
               if (b.dh0) store_n(b.dh0 + int64_t(s) * b.D * N + dn, g);
               zero_n(g);
               // (of a sequence that ends before this super-chunk, g goes no further)
@@ -477,14 +455,14 @@ k_packed_bwd(const PackedBwdParams p) {
               acc += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc), 0x140, 0xF, 0xF, false));
             // rows of tokens past the last end behind the window (the row's offset goes
             // with the lane's, which is what the window is checked against)
-            stb(rs, sums_at + uint32_t(j) * sums_row, 0, acc, kF);
+            stb(rs, sums_at + uint32_t(j0 + js) * sums_row, 0, acc, kF);
             __builtin_amdgcn_wave_barrier();
           }
         }
         __syncthreads();
 #pragma unroll
         for (int jj = w; jj < K; jj += NG) {
-          const int j = jb * K + jj;
+          const int j = j0 + jb + jj;
           if (j < len) {
             float su = 0.0f, sd = 0.0f;
 #pragma unroll
