@@ -72,88 +72,112 @@ ssm_status_t check_fwd(const ssm_add_norm_args_t* a) {
   return SSM_OK;
 }
 
-// How the lanes are dealt: TG lanes to a row, R times V channels each (V = 1, or
-// 16 bytes' worth of x where every row starts on 16 bytes), and `per` rows to a
-// lane.  TG = 0: the row is too long for registers.
+constexpr int64_t kL2Bytes = int64_t(32) << 20;   // of the eight XCDs
+
+// Neighbouring channels of a lane where every row allows it: 16 bytes of the row's
+// widest type, so that a wave's loads and stores have no gaps.  (8 channels of bf16 x
+// beside an fp32 residual: two loads 32 bytes apart, 32768 x 2560 to 8 bits 181 us for 161.)
+constexpr int kWide16 = 8, kWide32 = 4;
+template <typename A, typename B>
+constexpr int wide() { return sizeof(A) == 2 && sizeof(B) == 2 ? kWide16 : kWide32; }
+
+// How the lanes are dealt: TG lanes to a row, R times V channels each (V = 1 or as
+// above), and in the backward pass `per` rows to a lane.  TG = 0: the row is too long
+// for registers.
 struct Deal {
   int TG = 0, R = 0;
   bool vec = false;
   int64_t per = 1, blocks = 0;
 };
 
-Deal deal_row(int64_t C, bool vec, int elem) {
+Deal deal_row(int64_t C, bool vec, int64_t v, bool bwd) {
   Deal d;
   d.vec = vec;
-  const int64_t n = vec ? C / (16 / elem) : C;   // turns of the lanes
+  const int64_t n = vec ? C / v : C;   // turns of the lanes
   if (vec && n <= 16) {
     d.TG = n <= 4 ? 4 : 16;
     d.R = 1;
   } else if (n <= 64) {
     d.TG = 64;
     d.R = 1;
-  } else if (n <= 256) {
+  } else if (n <= 128 || (n <= 256 && !(vec && bwd))) {
     d.TG = 64;
     d.R = vec && n <= 128 ? 2 : 4;
-  } else if (n <= (vec ? 2048 : 4096)) {
-    d.TG = 256;
-    d.R = vec ? (n <= 512 ? 2 : n <= 1024 ? 4 : 8) : 16;
+  } else {
+    // at most 64 channels to a lane, and 32 in the backward pass, which holds more of a
+    // row; beyond, registers would spill
+    const int64_t turns = (n + 255) / 256, most = (bwd && vec ? 32 : 64) / (vec ? v : 1);
+    if (vec ? turns <= most : turns <= 16) {
+      d.TG = 256;
+      d.R = !vec ? 16 : turns <= 4 ? int(turns) : turns <= 8 ? 8 : 16;
+    }
   }
   return d;
 }
 
-// Rows to a lane, at most `most`, and no more than leaves the GPU 2^18 lanes (four
-// waves a SIMD): the weights are read once for them, and the sums for dweight
-// leave registers once.
-void deal_rows(Deal* d, int64_t rows, int64_t most) {
+// Rows to a lane in the backward pass, at most 64, and no more than leaves the GPU 2^17
+// lanes (two waves a SIMD, what its registers allow): the weights are read once for
+// them, and the sums for dweight leave registers once.
+void deal_rows(Deal* d, int64_t rows) {
   const int64_t lanes = rows * (d->TG ? d->TG : 256);
-  d->per = std::max<int64_t>(1, std::min(most, lanes >> 18));
+  d->per = std::max<int64_t>(1, std::min<int64_t>(64, lanes >> 17));
   d->blocks = (rows + d->per - 1) / d->per;
 }
 
-uint32_t groups(const Deal& d) { return uint32_t((d.blocks * d.TG + 255) / 256); }
+// Workgroups for n groups of TG lanes.
+uint32_t workgroups(int64_t n, int TG) { return uint32_t((n * TG + 255) / 256); }
 
 template <typename InT, typename ResT, typename OutT, int V, int TG, int R>
-ssm_status_t launch(const AddNormParams& p, const Deal& d, hipStream_t s) {
-  hipLaunchKernelGGL((k_add_norm<InT, ResT, OutT, V, TG, R>), dim3(groups(d)), dim3(256), 0, s, p);
+ssm_status_t launch(const AddNormParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((k_add_norm<InT, ResT, OutT, V, TG, R>), dim3(workgroups(p.rows, TG)), dim3(256), 0, s, p);
   return launch_status("k_add_norm");
 }
 
 template <typename InT, typename ResT, typename OutT>
 ssm_status_t run_fwd(AddNormParams p, const Deal& d, hipStream_t s) {
-  p.per = d.per;
-  constexpr int V = 16 / int(sizeof(InT));
+  constexpr int V = wide<InT, ResT>();
   if (d.TG == 0) {
-    hipLaunchKernelGGL((k_add_norm_long<InT, ResT, OutT>), dim3(uint32_t(p.rows)), dim3(256), 0, s, p);
+    if (d.vec)
+      hipLaunchKernelGGL((k_add_norm_long<InT, ResT, OutT, V>), dim3(uint32_t(p.rows)), dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_add_norm_long<InT, ResT, OutT, 1>), dim3(uint32_t(p.rows)), dim3(256), 0, s, p);
     return launch_status("k_add_norm_long");
   }
   if (!d.vec) {
-    if (d.TG == 256) return launch<InT, ResT, OutT, 1, 256, 16>(p, d, s);
-    return d.R == 1 ? launch<InT, ResT, OutT, 1, 64, 1>(p, d, s) : launch<InT, ResT, OutT, 1, 64, 4>(p, d, s);
+    if (d.TG == 256) return launch<InT, ResT, OutT, 1, 256, 16>(p, s);
+    return d.R == 1 ? launch<InT, ResT, OutT, 1, 64, 1>(p, s) : launch<InT, ResT, OutT, 1, 64, 4>(p, s);
   }
   switch (d.TG) {
-    case 4: return launch<InT, ResT, OutT, V, 4, 1>(p, d, s);
-    case 16: return launch<InT, ResT, OutT, V, 16, 1>(p, d, s);
+    case 4: return launch<InT, ResT, OutT, V, 4, 1>(p, s);
+    case 16: return launch<InT, ResT, OutT, V, 16, 1>(p, s);
     case 64:
-      return d.R == 1 ? launch<InT, ResT, OutT, V, 64, 1>(p, d, s)
-                      : d.R == 2 ? launch<InT, ResT, OutT, V, 64, 2>(p, d, s) : launch<InT, ResT, OutT, V, 64, 4>(p, d, s);
+      return d.R == 1 ? launch<InT, ResT, OutT, V, 64, 1>(p, s)
+                      : d.R == 2 ? launch<InT, ResT, OutT, V, 64, 2>(p, s) : launch<InT, ResT, OutT, V, 64, 4>(p, s);
     default:
-      return d.R == 2 ? launch<InT, ResT, OutT, V, 256, 2>(p, d, s)
-                      : d.R == 4 ? launch<InT, ResT, OutT, V, 256, 4>(p, d, s) : launch<InT, ResT, OutT, V, 256, 8>(p, d, s);
+      if (d.R == 1) return launch<InT, ResT, OutT, V, 256, 1>(p, s);
+      if (d.R == 3) return launch<InT, ResT, OutT, V, 256, 3>(p, s);
+      if constexpr (V == kWide32)
+        if (d.R == 16) return launch<InT, ResT, OutT, V, 256, 16>(p, s);
+      return d.R == 2 ? launch<InT, ResT, OutT, V, 256, 2>(p, s)
+                      : d.R == 4 ? launch<InT, ResT, OutT, V, 256, 4>(p, s) : launch<InT, ResT, OutT, V, 256, 8>(p, s);
   }
 }
 
 template <typename InT, typename SumT, int V, int TG, int R>
 ssm_status_t launch_bwd(const AddNormBwdParams& p, const Deal& d, hipStream_t s) {
-  hipLaunchKernelGGL((k_add_norm_bwd<InT, SumT, V, TG, R>), dim3(groups(d)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((k_add_norm_bwd<InT, SumT, V, TG, R>), dim3(workgroups(d.blocks, TG)), dim3(256), 0, s, p);
   return launch_status("k_add_norm_bwd");
 }
 
 template <typename InT, typename SumT>
 ssm_status_t run_bwd(AddNormBwdParams p, const Deal& d, hipStream_t s) {
   p.per = d.per;
-  constexpr int V = 16 / int(sizeof(InT));
+  constexpr int V = wide<InT, SumT>();
   if (d.TG == 0) {
-    hipLaunchKernelGGL((k_add_norm_bwd_long<InT, SumT>), dim3(uint32_t(d.blocks)), dim3(256), 0, s, p);
+    if (d.vec)
+      hipLaunchKernelGGL((k_add_norm_bwd_long<InT, SumT, V>), dim3(uint32_t(d.blocks)), dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_add_norm_bwd_long<InT, SumT, 1>), dim3(uint32_t(d.blocks)), dim3(256), 0, s, p);
     return launch_status("k_add_norm_bwd_long");
   }
   if (!d.vec) {
@@ -167,17 +191,22 @@ ssm_status_t run_bwd(AddNormBwdParams p, const Deal& d, hipStream_t s) {
       return d.R == 1 ? launch_bwd<InT, SumT, V, 64, 1>(p, d, s)
                       : d.R == 2 ? launch_bwd<InT, SumT, V, 64, 2>(p, d, s) : launch_bwd<InT, SumT, V, 64, 4>(p, d, s);
     default:
+      if (d.R == 1) return launch_bwd<InT, SumT, V, 256, 1>(p, d, s);
+      if (d.R == 3) return launch_bwd<InT, SumT, V, 256, 3>(p, d, s);
+      if constexpr (V == kWide32)
+        if (d.R == 8) return launch_bwd<InT, SumT, V, 256, 8>(p, d, s);
       return d.R == 2 ? launch_bwd<InT, SumT, V, 256, 2>(p, d, s) : launch_bwd<InT, SumT, V, 256, 4>(p, d, s);
   }
 }
 
-bool row_wide(const void* p, int64_t stride, int64_t k) { return !misaligned(p, 16) && stride % k == 0; }
+// Rows that all start on v elements.
+bool row_wide(const void* p, int64_t stride, int64_t v, size_t es) { return !misaligned(p, size_t(v) * es) && stride % v == 0; }
+
+int64_t wide_of(int32_t dtype, int32_t other) { return dtype == SSM_BF16 && other == SSM_BF16 ? kWide16 : kWide32; }
 
 Deal bwd_deal(const ssm_add_norm_bwd_args_t* a, bool vec) {
-  Deal d = deal_row(a->channels, vec, a->dtype == SSM_BF16 ? 2 : 4);
-  // the backward holds more of a row: past 4 turns of 256 lanes its registers would spill
-  if (d.vec && d.TG == 256 && d.R > 4) d.TG = d.R = 0;
-  deal_rows(&d, a->rows, 64);
+  Deal d = deal_row(a->channels, vec, wide_of(a->dtype, a->sum_dtype), true);
+  deal_rows(&d, a->rows);
   return d;
 }
 
@@ -247,14 +276,16 @@ ssm_status_t ssm_add_norm_fwd(const ssm_add_norm_args_t* a, void* hip_stream) {
   p.eps = a->eps;
   p.block = a->block && a->block < a->channels ? int32_t(a->block) : int32_t(a->channels);
   p.nblk = int32_t((a->channels + p.block - 1) / p.block);
-  const int64_t k = a->dtype == SSM_BF16 ? 8 : 4;
+  const int64_t v = wide_of(a->dtype, a->residual_dtype);
+  const size_t es = dtype_size(a->dtype), rs = dtype_size(a->residual_dtype);
   const bool quant = a->y_dtype == SSM_E4M3;
-  const bool vec = a->channels % k == 0 && row_wide(a->x, a->x_stride, k) && row_wide(a->residual, p.rs, k) &&
-                   !misaligned(a->weight, 16) && !misaligned(a->sum, 16) && !misaligned(a->y, quant ? k : 16);
-  Deal d = deal_row(a->channels, vec, a->dtype == SSM_BF16 ? 2 : 4);
+  const bool vec = a->channels % v == 0 && row_wide(a->x, a->x_stride, v, es) && row_wide(a->residual, p.rs, v, rs) &&
+                   !misaligned(a->weight, 16) && !misaligned(a->sum, size_t(v) * rs) &&
+                   !misaligned(a->y, size_t(v) * (quant ? 1 : es));
+  p.stream = a->rows * a->channels * int64_t((quant ? 1 : es) + (a->sum ? rs : 0)) > kL2Bytes;
+  Deal d = deal_row(a->channels, vec, v, false);
   // blocks are formed within a wave's turn, side by side
-  if (p.nblk > 1 && !(vec && d.TG * k >= p.block)) d.TG = d.R = 0;
-  deal_rows(&d, a->rows, d.TG ? 8 : 1);
+  if (p.nblk > 1 && !(vec && d.TG * v >= p.block)) d.TG = d.R = 0;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   if (a->dtype == SSM_F32)
     return quant ? run_fwd<float, float, fp8_t>(p, d, s) : run_fwd<float, float, float>(p, d, s);
@@ -290,10 +321,11 @@ ssm_status_t ssm_add_norm_bwd(const ssm_add_norm_bwd_args_t* a, void* hip_stream
     p.ds = a->dy_stride;
     p.gs = a->dsum ? a->dsum_stride : 0;
     p.eps = a->eps;
-    const int64_t k = a->dtype == SSM_BF16 ? 8 : 4;
-    const bool vec = a->channels % k == 0 && row_wide(a->sum, p.ss, k) && row_wide(a->dy, p.ds, k) &&
-                     row_wide(a->dsum, p.gs, k) && !misaligned(a->weight, 16) && !misaligned(a->dx, 16) &&
-                     !misaligned(a->dresidual, 16);
+    const int64_t v = wide_of(a->dtype, a->sum_dtype);
+    const size_t es = dtype_size(a->dtype), ss = dtype_size(a->sum_dtype);
+    const bool vec = a->channels % v == 0 && row_wide(a->sum, p.ss, v, ss) && row_wide(a->dy, p.ds, v, es) &&
+                     row_wide(a->dsum, p.gs, v, ss) && !misaligned(a->weight, 16) && !misaligned(a->dx, size_t(v) * es) &&
+                     !misaligned(a->dresidual, size_t(v) * ss);
     const Deal d = bwd_deal(a, vec);
     blocks = d.blocks;
     ssm_status_t st;

@@ -32,8 +32,8 @@ struct AddNormParams {
   float* scale;          // e4m3: (rows, nblk)
   int64_t rows, C;
   int64_t xs, rs;        // row strides of x and the residual
-  int64_t per;           // rows of a block: a lane walks them with its channels' weights in registers
   int32_t block, nblk;   // channels per scale (C: one scale per row) and scales per row
+  int32_t stream;        // outputs larger than the L2 caches
   float eps;
 };
 
@@ -47,7 +47,7 @@ struct AddNormBwdParams {
   float* dw;             // (blocks of rows, C), each block's sums over its rows; or null
   int64_t rows, C;
   int64_t ss, ds, gs;    // row strides of sum, dy and dsum
-  int64_t per;
+  int64_t per;           // rows of a block: a lane walks them with its channels' weights in registers
   float eps;
 };
 
@@ -93,16 +93,58 @@ __device__ __forceinline__ void load_v(float* v, const bf16_t* p) {
     }
   }
 }
-template <int V>
+// The same as they lie in memory: what is requested ahead takes half the registers
+// with bf16.
+template <typename T, int V>
+struct Raw {
+  static constexpr int W = V * int(sizeof(T)) / 4 > 0 ? V * int(sizeof(T)) / 4 : 1;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (V == 1) {
+      w[0] = __builtin_bit_cast(uint32_t, ld(p));
+    } else {
+      // not kept in the caches, where it would take the place of what is written
+      // (the convolution of 32768 x 2560 bf16 rows: 83 -> 73 us)
+      constexpr int L = W < 4 ? W : 4;
+      typedef uint32_t words __attribute__((ext_vector_type(L)));
+#pragma unroll
+      for (int i = 0; i < W; i += L) {
+        const words u = __builtin_nontemporal_load(reinterpret_cast<const words*>(p) + i / L);
+#pragma unroll
+        for (int k = 0; k < L; ++k) w[i + k] = u[k];
+      }
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (V == 1 || sizeof(T) == 4)
+      return __uint_as_float(w[i]);
+    else
+      return __uint_as_float(i % 2 == 0 ? w[i / 2] << 16 : w[i / 2] & 0xffff0000u);
+  }
+};
+
+// STREAM: past the caches, for outputs that they cannot hold until they are read.
+template <int V, bool STREAM = false>
 __device__ __forceinline__ void store_v(float* p, const float* v) {
   if constexpr (V == 1) {
     *p = v[0];
   } else {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    for (int i = 0; i < V; i += 4) {
+      const f32x4 u = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(u, reinterpret_cast<f32x4*>(p + i));
+      else
+        *reinterpret_cast<f32x4*>(p + i) = u;
+    }
   }
 }
-template <int V>
+template <int V, bool STREAM = false>
 __device__ __forceinline__ void store_v(bf16_t* p, const float* v) {
   if constexpr (V == 1) {
     st(p, v[0]);
@@ -111,7 +153,10 @@ __device__ __forceinline__ void store_v(bf16_t* p, const float* v) {
     bf16s u;
 #pragma unroll
     for (int i = 0; i < V; ++i) u[i] = static_cast<__bf16>(v[i]);
-    *reinterpret_cast<bf16s*>(p) = u;
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(u, reinterpret_cast<bf16s*>(p));
+    else
+      *reinterpret_cast<bf16s*>(p) = u;
   }
 }
 
@@ -120,7 +165,7 @@ __device__ __forceinline__ float to_range(float v) {
   return v != v ? v : __builtin_amdgcn_fmed3f(v, -kE4m3Max, kE4m3Max);
 }
 // To e4m3, to nearest even.
-template <int V>
+template <int V, bool STREAM = false>
 __device__ __forceinline__ void store_v(fp8_t* p, const float* v) {
   if constexpr (V == 1) {
     p->v = uint8_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[0], 0.0f, 0, false));
@@ -187,148 +232,191 @@ __device__ __forceinline__ void load_row(float (&v)[R * V], const T* p, int lane
     }
   }
 }
-template <int V, int R, int TG, typename T>
+template <int V, int R, int TG, bool STREAM = false, typename T>
 __device__ __forceinline__ void store_row(T* p, const float (&v)[R * V], int lane, int C) {
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     const int c = (k * TG + lane) * V;
-    if (c < C) store_v<V>(p + c, v + k * V);
+    if (c < C) store_v<V, STREAM>(p + c, v + k * V);
   }
 }
 
-// Forward: TG lanes share a row and walk p.per rows; a workgroup of 256 holds
-// 256 / TG of them.
+// A row as it lies in memory.
+template <typename T, int V, int R>
+struct RawRow {
+  Raw<T, V> v[R];
+  template <int TG>
+  __device__ __forceinline__ void load(const T* p, int lane, int C) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int c = (k * TG + lane) * V;
+      v[k].clear();
+      if (c < C) v[k].load(p + c);
+    }
+  }
+  __device__ __forceinline__ float at(int i) const { return v[i / V].at(i % V); }
+};
+
+// Forward: TG lanes to a row, 256 / TG rows to a workgroup.  Bound by memory; rows
+// enough are on their way in the waves a SIMD holds.  (A lane that walks 8 rows, the
+// weights in registers and the next row requested ahead: 32768 x 2560 bf16 131 us
+// for 120, to 8 bits with an fp32 residual 190 for 175.  Stores past the caches then
+// 118 -> 111 and 161 -> 145; outputs that the L2 caches hold are left there.)
 template <typename InT, typename ResT, typename OutT, int V, int TG, int R>
 __global__ __launch_bounds__(256) void k_add_norm(AddNormParams p) {
   constexpr bool kQuant = sizeof(OutT) == 1;
   __shared__ float part[8];
   const int lane = threadIdx.x & (TG - 1);
-  const int64_t row0 = (int64_t(blockIdx.x) * (256 / TG) + threadIdx.x / TG) * p.per;
-  const int64_t end = row0 + p.per < p.rows ? row0 + p.per : p.rows;
-  if (row0 >= end) return;
+  const int64_t row = int64_t(blockIdx.x) * (256 / TG) + threadIdx.x / TG;
+  if (row >= p.rows) return;
   const int C = int(p.C);
-  const float inv = 1.0f / float(C);
+  float x[R * V];
+  {
+    RawRow<InT, V, R> a;
+    RawRow<ResT, V, R> b;
+    a.template load<TG>(static_cast<const InT*>(p.x) + row * p.xs, lane, C);
+    if (p.res) b.template load<TG>(static_cast<const ResT*>(p.res) + row * p.rs, lane, C);
+#pragma unroll
+    for (int i = 0; i < R * V; ++i) x[i] = p.res ? a.at(i) + b.at(i) : a.at(i);
+  }
+  if (p.sum) {
+    ResT* sum = static_cast<ResT*>(p.sum) + row * p.C;
+    if (p.stream)
+      store_row<V, R, TG, true>(sum, x, lane, C);
+    else
+      store_row<V, R, TG>(sum, x, lane, C);
+  }
   float w[R * V];
 #pragma unroll
   for (int i = 0; i < R * V; ++i) w[i] = 1.0f;
   if (p.w) load_row<V, R, TG>(w, p.w, lane, C);
-  const InT* px = static_cast<const InT*>(p.x) + row0 * p.xs;
-  const ResT* pr = static_cast<const ResT*>(p.res) + row0 * p.rs;
-  float x[R * V], q[R * V];
-  load_row<V, R, TG>(x, px, lane, C);
-  if (p.res) load_row<V, R, TG>(q, pr, lane, C);
-  for (int64_t row = row0; row < end; ++row) {
-    if (p.res) {
+  float ss = 0.0f, zero = 0.0f;
 #pragma unroll
-      for (int i = 0; i < R * V; ++i) x[i] += q[i];
+  for (int i = 0; i < R * V; ++i) ss += x[i] * x[i];
+  group_sum<TG>(ss, zero, part);
+  const float r = 1.0f / sqrtf(ss * (1.0f / float(C)) + p.eps);
+#pragma unroll
+  for (int i = 0; i < R * V; ++i) x[i] = x[i] * r * w[i];
+  if constexpr (kQuant) {
+    float top[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      top[k] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) top[k] = fmaxf(top[k], fabsf(x[k * V + i]));
     }
-    float nx[R * V];
-    const bool more = row + 1 < end;   // the next row is on its way while this one is worked on
-    if (more) {
-      load_row<V, R, TG>(nx, px += p.xs, lane, C);
-      if (p.res) load_row<V, R, TG>(q, pr += p.rs, lane, C);
-    }
-    if (p.sum) store_row<V, R, TG>(static_cast<ResT*>(p.sum) + row * p.C, x, lane, C);
-    float ss = 0.0f, zero = 0.0f;
+    float* ps = p.scale + row * p.nblk;
+    if (p.nblk == 1) {
 #pragma unroll
-    for (int i = 0; i < R * V; ++i) ss += x[i] * x[i];
-    group_sum<TG>(ss, zero, part);
-    const float r = 1.0f / sqrtf(ss * inv + p.eps);
+      for (int k = 1; k < R; ++k) top[0] = fmaxf(top[0], top[k]);
+      float inverse;
+      const float s = scale_of(row_max<TG>(top[0], part), &inverse);
+      if (lane == 0) *ps = s;
 #pragma unroll
-    for (int i = 0; i < R * V; ++i) x[i] = x[i] * r * w[i];
-    if constexpr (kQuant) {
-      float top[R];
+      for (int i = 0; i < R * V; ++i) x[i] = to_range(x[i] * inverse);
+    } else {
+      // a block is the same turn of block / V neighbouring lanes (the host sees to it)
+      const int lanes = p.block / V;
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        top[k] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) top[k] = fmaxf(top[k], fabsf(x[k * V + i]));
-      }
-      float* ps = p.scale + row * p.nblk;
-      if (p.nblk == 1) {
-#pragma unroll
-        for (int k = 1; k < R; ++k) top[0] = fmaxf(top[0], top[k]);
         float inverse;
-        const float s = scale_of(row_max<TG>(top[0], part), &inverse);
-        if (lane == 0) *ps = s;
+        const float s = scale_of(lanes_max(top[k], lanes), &inverse);
+        const int c = (k * TG + lane) * V;
+        if ((lane & (lanes - 1)) == 0 && c < C) ps[c / p.block] = s;
 #pragma unroll
-        for (int i = 0; i < R * V; ++i) x[i] = to_range(x[i] * inverse);
-      } else {
-        // a block is the same turn of block / V neighbouring lanes (the host sees to it)
-        const int lanes = p.block / V;
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-          float inverse;
-          const float s = scale_of(lanes_max(top[k], lanes), &inverse);
-          const int c = (k * TG + lane) * V;
-          if ((lane & (lanes - 1)) == 0 && c < C) ps[c / p.block] = s;
-#pragma unroll
-          for (int i = 0; i < V; ++i) x[k * V + i] = to_range(x[k * V + i] * inverse);
-        }
+        for (int i = 0; i < V; ++i) x[k * V + i] = to_range(x[k * V + i] * inverse);
       }
     }
-    store_row<V, R, TG>(static_cast<OutT*>(p.y) + row * p.C, x, lane, C);
-#pragma unroll
-    for (int i = 0; i < R * V; ++i) x[i] = nx[i];
   }
+  OutT* y = static_cast<OutT*>(p.y) + row * p.C;
+  if (p.stream)
+    store_row<V, R, TG, true>(y, x, lane, C);
+  else
+    store_row<V, R, TG>(y, x, lane, C);
 }
 
 // Rows too long for registers, and blocks of channels that no lane group of one turn
-// covers: a workgroup to a row, read again for every pass over it (from the caches).
-// Nothing is written before the last pass, which reads an element before it writes
-// it: the sum may take the residual's place.
-template <typename InT, typename ResT>
-__device__ __forceinline__ float long_sum(const AddNormParams& p, int64_t row, int64_t c) {
-  const float x = ld(static_cast<const InT*>(p.x) + row * p.xs + c);
-  return p.res ? x + ld(static_cast<const ResT*>(p.res) + row * p.rs + c) : x;
-}
-
-template <typename InT, typename ResT, typename OutT>
+// covers: a workgroup to a row, read again for every pass over it (from the caches), V
+// channels to a lane in turn.  Nothing is written before the last pass, which reads an
+// element before it writes it: the sum may take the residual's place.
+template <typename InT, typename ResT, typename OutT, int V>
 __global__ __launch_bounds__(256) void k_add_norm_long(AddNormParams p) {
   constexpr bool kQuant = sizeof(OutT) == 1;
   __shared__ float part[8];
   const int64_t row = blockIdx.x;
+  const InT* x = static_cast<const InT*>(p.x) + row * p.xs;
+  const ResT* res = static_cast<const ResT*>(p.res) + row * p.rs;
+  auto load = [&](float (&s)[V], int64_t c) {
+    load_v<V>(s, x + c);
+    if (p.res) {
+      float q[V];
+      load_v<V>(q, res + c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] += q[i];
+    }
+  };
   float ss = 0.0f, zero = 0.0f;
-  for (int64_t c = threadIdx.x; c < p.C; c += 256) {
-    const float s = long_sum<InT, ResT>(p, row, c);
-    ss += s * s;
+  for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) {
+    float s[V];
+    load(s, c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) ss += s[i] * s[i];
   }
   group_sum<256>(ss, zero, part);
   const float r = 1.0f / sqrtf(ss * (1.0f / float(p.C)) + p.eps);
   ResT* sum = static_cast<ResT*>(p.sum) + row * p.C;
   OutT* y = static_cast<OutT*>(p.y) + row * p.C;
-  auto value = [&](float s, int64_t c) { return s * r * (p.w ? p.w[c] : 1.0f); };
+  // s of V channels, and y of them
+  auto values = [&](float (&s)[V], float (&v)[V], int64_t c) {
+    load(s, c);
+    float w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = 1.0f;
+    if (p.w) load_v<V>(w, p.w + c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = s[i] * r * w[i];
+  };
   auto finish = [&](int64_t c, float inverse) {
-    const float s = long_sum<InT, ResT>(p, row, c);
-    float v = value(s, c);
-    if constexpr (kQuant) v = to_range(v * inverse);
-    if (p.sum) st(sum + c, s);
-    store_v<1>(y + c, &v);
+    float s[V], v[V];
+    values(s, v, c);
+    if constexpr (kQuant) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = to_range(v[i] * inverse);
+    }
+    if (p.sum) store_v<V>(sum + c, s);
+    store_v<V>(y + c, v);
+  };
+  auto largest = [&](float top, int64_t c) {
+    float s[V], v[V];
+    values(s, v, c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(v[i]));
+    return top;
   };
   if constexpr (!kQuant) {
-    for (int64_t c = threadIdx.x; c < p.C; c += 256) finish(c, 1.0f);
+    for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) finish(c, 1.0f);
   } else if (p.nblk == 1) {
     float top = 0.0f, inverse;
-    for (int64_t c = threadIdx.x; c < p.C; c += 256) top = fmaxf(top, fabsf(value(long_sum<InT, ResT>(p, row, c), c)));
+    for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) top = largest(top, c);
     const float s = scale_of(row_max<256>(top, part), &inverse);
     if (threadIdx.x == 0) p.scale[row] = s;
-    for (int64_t c = threadIdx.x; c < p.C; c += 256) finish(c, inverse);
+    for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) finish(c, inverse);
   } else {
     // a wave to a block of channels
     const int lane = threadIdx.x & 63;
     for (int64_t k = threadIdx.x >> 6; k < p.nblk; k += 4) {
       const int64_t c0 = k * p.block, c1 = c0 + p.block < p.C ? c0 + p.block : p.C;
       float top = 0.0f, inverse;
-      for (int64_t c = c0 + lane; c < c1; c += 64) top = fmaxf(top, fabsf(value(long_sum<InT, ResT>(p, row, c), c)));
+      for (int64_t c = c0 + lane * V; c < c1; c += 64 * V) top = largest(top, c);
       const float s = scale_of(lanes_max(top, 64), &inverse);
       if (lane == 0) p.scale[row * p.nblk + k] = s;
-      for (int64_t c = c0 + lane; c < c1; c += 64) finish(c, inverse);
+      for (int64_t c = c0 + lane * V; c < c1; c += 64 * V) finish(c, inverse);
     }
   }
 }
 
-// Backward, the same walk: ds of every row, and the sums over the block's rows
-// for the weight's gradient.
+// Backward: TG lanes walk the p.per rows of a block: ds of every row, and the sums
+// over the block's rows for the weight's gradient.
 template <typename InT, typename SumT, int V, int TG, int R>
 __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
   __shared__ float part[8];
@@ -349,19 +437,27 @@ __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
   const SumT* ps = static_cast<const SumT*>(p.sum) + row0 * p.ss;
   const InT* pd = static_cast<const InT*>(p.dy) + row0 * p.ds;
   const SumT* pg = static_cast<const SumT*>(p.dsum) + row0 * p.gs;
-  float s[R * V], d[R * V], g[R * V];
-  load_row<V, R, TG>(s, ps, lane, C);
-  load_row<V, R, TG>(d, pd, lane, C);
-#pragma unroll
-  for (int i = 0; i < R * V; ++i) g[i] = 0.0f;
-  if (p.dsum) load_row<V, R, TG>(g, pg, lane, C);
+  RawRow<SumT, V, R> ns, ng;
+  RawRow<InT, V, R> nd;
+  auto request = [&] {
+    ns.template load<TG>(ps, lane, C);
+    nd.template load<TG>(pd, lane, C);
+    if (p.dsum) ng.template load<TG>(pg, lane, C);
+  };
+  request();
   for (int64_t row = row0; row < end; ++row) {
-    float ns[R * V], nd[R * V], ng[R * V];
-    const bool more = row + 1 < end;
-    if (more) {
-      load_row<V, R, TG>(ns, ps += p.ss, lane, C);
-      load_row<V, R, TG>(nd, pd += p.ds, lane, C);
-      if (p.dsum) load_row<V, R, TG>(ng, pg += p.gs, lane, C);
+    float s[R * V], d[R * V], g[R * V];
+#pragma unroll
+    for (int i = 0; i < R * V; ++i) {
+      s[i] = ns.at(i);
+      d[i] = nd.at(i);
+      g[i] = p.dsum ? ng.at(i) : 0.0f;
+    }
+    if (row + 1 < end) {
+      ps += p.ss;
+      pd += p.ds;
+      pg += p.gs;
+      request();
     }
     float ss = 0.0f, sdn = 0.0f;
 #pragma unroll
@@ -381,17 +477,12 @@ __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
     store_row<V, R, TG>(static_cast<InT*>(p.dx) + row * p.C, g, lane, C);
     if constexpr (sizeof(SumT) != sizeof(InT))
       if (p.dres) store_row<V, R, TG>(static_cast<SumT*>(p.dres) + row * p.C, g, lane, C);
-#pragma unroll
-    for (int i = 0; i < R * V; ++i) {
-      s[i] = ns[i];
-      d[i] = nd[i];
-      g[i] = p.dsum ? ng[i] : 0.0f;
-    }
   }
   if (p.dw) store_row<V, R, TG>(p.dw + block * p.C, dw, lane, C);
 }
 
-template <typename InT, typename SumT>
+// Rows too long for registers, read twice.
+template <typename InT, typename SumT, int V>
 __global__ __launch_bounds__(256) void k_add_norm_bwd_long(AddNormBwdParams p) {
   __shared__ float part[8];
   const int64_t row0 = blockIdx.x * p.per, end = row0 + p.per < p.rows ? row0 + p.per : p.rows;
@@ -400,22 +491,45 @@ __global__ __launch_bounds__(256) void k_add_norm_bwd_long(AddNormBwdParams p) {
     const SumT* ps = static_cast<const SumT*>(p.sum) + row * p.ss;
     const InT* pd = static_cast<const InT*>(p.dy) + row * p.ds;
     const SumT* pg = static_cast<const SumT*>(p.dsum) + row * p.gs;
+    auto weight = [&](float (&w)[V], int64_t c) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = 1.0f;
+      if (p.w) load_v<V>(w, p.w + c);
+    };
     float ss = 0.0f, sdn = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.C; c += 256) {
-      const float s = ld(ps + c);
-      ss += s * s;
-      sdn += ld(pd + c) * (p.w ? p.w[c] : 1.0f) * s;
+    for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) {
+      float s[V], d[V], w[V];
+      load_v<V>(s, ps + c);
+      load_v<V>(d, pd + c);
+      weight(w, c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        ss += s[i] * s[i];
+        sdn += d[i] * w[i] * s[i];
+      }
     }
     group_sum<256>(ss, sdn, part);
     const float inv = 1.0f / float(p.C), r = 1.0f / sqrtf(ss * inv + p.eps), m = sdn * inv * r;
-    for (int64_t c = threadIdx.x; c < p.C; c += 256) {
-      const float n = ld(ps + c) * r, dy = ld(pd + c);
+    for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) {
+      float s[V], d[V], w[V], g[V], sum[V];
+      load_v<V>(s, ps + c);
+      load_v<V>(d, pd + c);
+      weight(w, c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] = sum[i] = 0.0f;
+      if (p.dsum) load_v<V>(g, pg + c);
       // the block's sums, this lane's channels from row to row
-      if (dw) dw[c] = (row == row0 ? 0.0f : dw[c]) + dy * n;
-      const float g = (p.dsum ? ld(pg + c) : 0.0f) + r * (dy * (p.w ? p.w[c] : 1.0f) - n * m);
-      st(static_cast<InT*>(p.dx) + row * p.C + c, g);
+      if (dw && row > row0) load_v<V>(sum, dw + c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float n = s[i] * r;
+        sum[i] += d[i] * n;
+        g[i] += r * (d[i] * w[i] - n * m);
+      }
+      if (dw) store_v<V>(dw + c, sum);
+      store_v<V>(static_cast<InT*>(p.dx) + row * p.C + c, g);
       if constexpr (sizeof(SumT) != sizeof(InT))
-        if (p.dres) st(static_cast<SumT*>(p.dres) + row * p.C + c, g);
+        if (p.dres) store_v<V>(static_cast<SumT*>(p.dres) + row * p.C + c, g);
     }
   }
 }

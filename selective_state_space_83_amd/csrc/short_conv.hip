@@ -93,7 +93,12 @@ ssm_status_t check_step(const ssm_short_conv_step_args_t* a) {
   return SSM_OK;
 }
 
-bool row_wide(const void* p, int64_t stride, int64_t k) { return !misaligned(p, 16) && stride % k == 0; }
+// A lane's channels.  (8 bf16 channels, 16 bytes, take twice the registers: 32768 x 2560
+// 70 us for 64, the gradients of 16384 x 2560 75 us for 60.)
+constexpr int V = 4;
+
+// Rows that all start on V elements.
+bool row_wide(const void* p, int64_t stride, size_t es) { return !misaligned(p, V * es) && stride % V == 0; }
 
 // Tokens per tile: short enough that the tiles fill the GPU with `waves` waves, at
 // least 8 (a tile reads up to three rows more than its own).
@@ -103,7 +108,7 @@ int32_t tile_len(int64_t tokens, int64_t cgroups, int64_t waves, int64_t most) {
   return int32_t(t);
 }
 
-int64_t channel_groups(int64_t C, int64_t V) { return (C + 64 * V - 1) / (64 * V); }
+int64_t channel_groups(int64_t C, int64_t v) { return (C + 64 * v - 1) / (64 * v); }
 
 template <typename Args>
 Seqs sequences(const Args* a) {
@@ -115,9 +120,9 @@ Seqs sequences(const Args* a) {
   return q;
 }
 
-ssm_status_t set_tiles(ConvParams* p, int64_t V, int32_t tile, uint32_t* grid) {
+ssm_status_t set_tiles(ConvParams* p, int64_t v, int32_t tile, uint32_t* grid) {
   p->tile = tile;
-  p->cgroups = int32_t(channel_groups(p->C, V));
+  p->cgroups = int32_t(channel_groups(p->C, v));
   p->tiles = int32_t(std::max<int64_t>(1, (int64_t(p->q.tokens) + tile - 1) / tile));
   const int64_t n = (int64_t(p->tiles) * p->cgroups + 3) / 4;
   if (n > int64_t(UINT32_MAX) / 256) return fail(SSM_ERR_SHAPE, "problem too large for one launch");
@@ -125,27 +130,27 @@ ssm_status_t set_tiles(ConvParams* p, int64_t V, int32_t tile, uint32_t* grid) {
   return SSM_OK;
 }
 
-template <typename T, int V, int K>
+template <typename T, int W, int K>
 ssm_status_t launch_fwd(ConvParams p, hipStream_t s) {
   uint32_t grid;
-  if (ssm_status_t st = set_tiles(&p, V, tile_len(p.q.tokens, channel_groups(p.C, V), 4096, 32), &grid)) return st;
-  hipLaunchKernelGGL((k_short_conv<T, V, K>), dim3(grid), dim3(256), 0, s, p);
+  if (ssm_status_t st = set_tiles(&p, W, tile_len(p.q.tokens, channel_groups(p.C, W), 2048, 64), &grid)) return st;
+  hipLaunchKernelGGL((k_short_conv<T, W, K>), dim3(grid), dim3(256), 0, s, p);
   return launch_status("k_short_conv");
 }
 
-template <typename T, int V, int K>
+template <typename T, int W, int K>
 ssm_status_t launch_step(const ConvParams& p, hipStream_t s) {
-  const int64_t n = int64_t(p.q.S) * ((p.C + V - 1) / V);
-  if (n > int64_t(UINT32_MAX) - 256) return fail(SSM_ERR_SHAPE, "problem too large for one launch");
-  hipLaunchKernelGGL((k_short_conv_step<T, V, K>), dim3(uint32_t((n + 255) / 256)), dim3(256), 0, s, p);
+  const int64_t rows = (p.q.S + kStepRows - 1) / kStepRows, y = std::min<int64_t>(rows, 32768);
+  const dim3 grid(uint32_t((p.C + 256 * W - 1) / (256 * W)), uint32_t(y));
+  hipLaunchKernelGGL((k_short_conv_step<T, W, K>), grid, dim3(256), 0, s, p);
   return launch_status("k_short_conv_step");
 }
 
-template <typename T, int V, int K>
+template <typename T, int W, int K>
 ssm_status_t launch_bwd(ConvParams p, int32_t tile, hipStream_t s) {
   uint32_t grid;
-  if (ssm_status_t st = set_tiles(&p, V, tile, &grid)) return st;
-  hipLaunchKernelGGL((k_short_conv_bwd<T, V, K>), dim3(grid), dim3(256), 0, s, p);
+  if (ssm_status_t st = set_tiles(&p, W, tile, &grid)) return st;
+  hipLaunchKernelGGL((k_short_conv_bwd<T, W, K>), dim3(grid), dim3(256), 0, s, p);
   return launch_status("k_short_conv_bwd");
 }
 
@@ -160,17 +165,14 @@ ssm_status_t launch_bwd(ConvParams p, int32_t tile, hipStream_t s) {
 
 template <typename T>
 ssm_status_t run_fwd(const ConvParams& p, int taps, bool vec, hipStream_t s) {
-  constexpr int V = 16 / int(sizeof(T));
   SSM_CONV_CASES(launch_fwd, p, s)
 }
 template <typename T>
 ssm_status_t run_step(const ConvParams& p, int taps, bool vec, hipStream_t s) {
-  constexpr int V = 4;   // 4 bf16 channels are 8 bytes: the window, in fp32, is the traffic
   SSM_CONV_CASES(launch_step, p, s)
 }
 template <typename T>
 ssm_status_t run_bwd(const ConvParams& p, int taps, bool vec, int32_t tile, hipStream_t s) {
-  constexpr int V = 16 / int(sizeof(T));
   SSM_CONV_CASES(launch_bwd, p, tile, s)
 }
 #undef SSM_CONV_CASES
@@ -178,7 +180,7 @@ ssm_status_t run_bwd(const ConvParams& p, int taps, bool vec, int32_t tile, hipS
 // Tokens per tile of the backward pass: the tiles' sums for dweight and dbias are
 // written once a tile.  By sizes alone, as the workspace is.
 int32_t bwd_tile(const ssm_short_conv_bwd_args_t* a) {
-  return tile_len(a->tokens, channel_groups(a->channels, a->dtype == SSM_BF16 ? 8 : 4), 2048, 64);
+  return tile_len(a->tokens, channel_groups(a->channels, V), 1536, 64);
 }
 
 size_t bwd_workspace(const ssm_short_conv_bwd_args_t* a) {
@@ -252,8 +254,8 @@ ssm_status_t ssm_short_conv_fwd(const ssm_short_conv_args_t* a, void* hip_stream
   p.q.slots = int32_t(a->slots);
   p.state = a->taps > 1 ? a->state : nullptr;
   p.y = a->y;
-  const int64_t k = a->dtype == SSM_BF16 ? 8 : 4;
-  const bool vec = a->channels % k == 0 && row_wide(a->x, a->x_stride, k) && !misaligned(a->y, 16) &&
+  const size_t es = dtype_size(a->dtype);
+  const bool vec = a->channels % V == 0 && row_wide(a->x, a->x_stride, es) && !misaligned(a->y, V * es) &&
                    !misaligned(a->weight, 16) && !misaligned(a->bias, 16) && !misaligned(a->state, 16);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   return a->dtype == SSM_F32 ? run_fwd<float>(p, a->taps, vec, s) : run_fwd<bf16_t>(p, a->taps, vec, s);
@@ -270,8 +272,7 @@ ssm_status_t ssm_short_conv_step(const ssm_short_conv_step_args_t* a, void* hip_
   p.state = a->state;
   p.y = a->y;
   const size_t es = dtype_size(a->dtype);
-  const bool vec = a->channels % 4 == 0 && !misaligned(a->x, 4 * es) && a->x_stride % 4 == 0 &&
-                   !misaligned(a->y, 4 * es) && !misaligned(a->weight, 16) && !misaligned(a->bias, 16) &&
+  const bool vec = a->channels % V == 0 && row_wide(a->x, a->x_stride, es) && !misaligned(a->y, V * es) && !misaligned(a->weight, 16) && !misaligned(a->bias, 16) &&
                    !misaligned(a->state, 16);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   return a->dtype == SSM_F32 ? run_step<float>(p, a->taps, vec, s) : run_step<bf16_t>(p, a->taps, vec, s);
@@ -298,9 +299,9 @@ ssm_status_t ssm_short_conv_bwd(const ssm_short_conv_bwd_args_t* a, void* hip_st
     p.ds = a->dy_stride;
     p.y = a->dx;
     p.part = a->dweight || a->dbias ? static_cast<float*>(a->workspace) : nullptr;
-    const int64_t k = a->dtype == SSM_BF16 ? 8 : 4;
-    const bool vec = a->channels % k == 0 && row_wide(a->x, a->x_stride, k) && row_wide(a->dy, a->dy_stride, k) &&
-                     !misaligned(a->dx, 16) && !misaligned(a->weight, 16) && !misaligned(a->bias, 16);
+    const size_t es = dtype_size(a->dtype);
+    const bool vec = a->channels % V == 0 && row_wide(a->x, a->x_stride, es) && row_wide(a->dy, a->dy_stride, es) &&
+                     !misaligned(a->dx, V * es) && !misaligned(a->weight, 16) && !misaligned(a->bias, 16);
     const int32_t tile = bwd_tile(a);
     tiles = (a->tokens + tile - 1) / tile;
     if (ssm_status_t st = a->dtype == SSM_F32 ? run_bwd<float>(p, a->taps, vec, tile, s)

@@ -8,8 +8,7 @@
 //   da = dy act'(a),  dx[t] = sum_k w[k] da[t+K-1-k],  dw[k] = sum_t da[t] x[t-K+1+k],
 // silu'(a) = s (1 + a (1 - s)), s = 1 / (1 + exp(-a)).
 //
-// A lane holds V neighbouring channels (16 bytes of x, or one where rows do not
-// lie on 16 bytes) and walks a tile of tokens with the last three inputs in
+// A lane holds V neighbouring channels (4, or one where rows do not start on 4) and walks a tile of tokens with the last three inputs in
 // registers; a wave covers 64 V channels, and the waves of a workgroup lie side by
 // side on the same tokens.  Bound by memory: a tile reads K - 1 rows more than its
 // own.
@@ -21,6 +20,7 @@
 namespace ssmc {
 
 using ssma::load_v;
+using ssma::Raw;
 using ssma::store_v;
 using ssmn::bf16_t;
 using ssmn::sigmoid;
@@ -218,11 +218,11 @@ __global__ __launch_bounds__(256) void k_short_conv(ConvParams p) {
     }
   };
 
-  float cur[kAhead][V], nxt[kAhead][V];
-  auto rows = [&](float (&v)[kAhead][V], int32_t t) {
+  Raw<T, V> cur[kAhead], nxt[kAhead];
+  auto rows = [&](Raw<T, V> (&v)[kAhead], int32_t t) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
-      if (live && t + j < to) load_v<V>(v[j], x + int64_t(t + j) * p.xs);
+      if (live && t + j < to) v[j].load(x + int64_t(t + j) * p.xs);
   };
   if (from < to) rows(cur, from);
   for (int32_t t = from; t < to; t += kAhead) {
@@ -231,50 +231,63 @@ __global__ __launch_bounds__(256) void k_short_conv(ConvParams p) {
     for (int j = 0; j < kAhead; ++j) {
       if (t + j >= to) break;
       if (next <= t + j) meet(t + j);
-      float a[V];
-      taps_sum<V, K>(f, cur[j], h, a);
+      float u[V], a[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[i] = cur[j].at(i);
+      taps_sum<V, K>(f, u, h, a);
       if (p.silu) {
 #pragma unroll
         for (int i = 0; i < V; ++i) a[i] *= sigmoid(a[i]);
       }
       if (live) store_v<V>(y + int64_t(t + j) * p.C, a);
-      h.push(cur[j]);
+      h.push(u);
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) cur[j][i] = nxt[j][i];
+    for (int j = 0; j < kAhead; ++j) cur[j] = nxt[j];
   }
   // empty sequences behind the last token: of the tile whose range holds their place
   const int32_t at = from > to ? from : to;
   if (at < t1 || t1 == p.q.tokens) meet(at);
 }
 
-// One token of every row of the batch: a lane to V channels of a row.
+// One token of every row of the batch: a lane to V channels of kStepRows neighbouring
+// rows, which share its taps.  Bound by memory, the windows above all.
+constexpr int kStepRows = 2;
+
 template <typename T, int V, int K>
 __global__ __launch_bounds__(256) void k_short_conv_step(ConvParams p) {
-  const int64_t cv = (p.C + V - 1) / V;
-  const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t row = id / cv, c = id % cv * V;
-  if (row >= p.q.S) return;
-  const int32_t slot = p.q.slot ? p.q.slot[row] : int32_t(row);
-  float x[V], a[V];
-  Past<V, K> h;
-  h.clear();
-  const bool kept = K > 1 && slot >= 0 && slot < p.q.slots;
-  float* win = p.state + (int64_t(slot) * p.C + c) * (K - 1);
-  if (kept) load_window<V, K>(h, win);
-  load_v<V>(x, static_cast<const T*>(p.x) + row * p.xs + c);
+  const int64_t c = (int64_t(blockIdx.x) * 256 + threadIdx.x) * V;
+  if (c >= p.C) return;
   Filter<V, K> f;
   f.load(p, c);
-  taps_sum<V, K>(f, x, h, a);
-  if (p.silu) {
+  for (int64_t row0 = int64_t(blockIdx.y) * kStepRows; row0 < p.q.S; row0 += int64_t(gridDim.y) * kStepRows) {
+    // all rows are read before any is written
+    float x[kStepRows][V];
+    Past<V, K> h[kStepRows];
+    float* win[kStepRows];
 #pragma unroll
-    for (int i = 0; i < V; ++i) a[i] *= sigmoid(a[i]);
+    for (int r = 0; r < kStepRows; ++r) {
+      const int64_t row = row0 + r < p.q.S ? row0 + r : p.q.S - 1;
+      const int32_t slot = p.q.slot ? ((ssmq::const_i32_ptr)(p.q.slot))[row] : int32_t(row);
+      win[r] = K > 1 && slot >= 0 && slot < p.q.slots ? p.state + (int64_t(slot) * p.C + c) * (K - 1) : nullptr;
+      h[r].clear();
+      if (win[r]) load_window<V, K>(h[r], win[r]);
+      load_v<V>(x[r], static_cast<const T*>(p.x) + row * p.xs + c);
+    }
+#pragma unroll
+    for (int r = 0; r < kStepRows; ++r) {
+      if (row0 + r >= p.q.S) break;
+      float a[V];
+      taps_sum<V, K>(f, x[r], h[r], a);
+      if (p.silu) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] *= sigmoid(a[i]);
+      }
+      store_v<V>(static_cast<T*>(p.y) + (row0 + r) * p.C + c, a);
+      h[r].push(x[r]);
+      if (win[r]) store_window<V, K>(h[r], win[r]);
+    }
   }
-  store_v<V>(static_cast<T*>(p.y) + row * p.C + c, a);
-  h.push(x);
-  if (kept) store_window<V, K>(h, win);
 }
 
 // Gradients: a tile walks its tokens and the K - 1 behind them, whose da reach back
@@ -345,13 +358,13 @@ __global__ __launch_bounds__(256) void k_short_conv_bwd(ConvParams p) {
     }
   };
 
-  float cx[kAhead][V], cd[kAhead][V], nx[kAhead][V], nd[kAhead][V];
-  auto rows = [&](float (&u)[kAhead][V], float (&v)[kAhead][V], int32_t t) {
+  Raw<T, V> cx[kAhead], cd[kAhead], nx[kAhead], nd[kAhead];
+  auto rows = [&](Raw<T, V> (&u)[kAhead], Raw<T, V> (&v)[kAhead], int32_t t) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
       if (live && t + j < to) {
-        load_v<V>(u[j], x + int64_t(t + j) * p.xs);
-        load_v<V>(v[j], dy + int64_t(t + j) * p.ds);
+        u[j].load(x + int64_t(t + j) * p.xs);
+        v[j].load(dy + int64_t(t + j) * p.ds);
       }
   };
   rows(cx, cd, from);
@@ -374,18 +387,19 @@ __global__ __launch_bounds__(256) void k_short_conv_bwd(ConvParams p) {
         if (first >= t1) to = first;   // nothing of this tile is left
         if (t + j >= to) break;
       }
-      float a[V];
-      taps_sum<V, K>(f, cx[j], h, a);
-      float da[V];
+      float u[V], a[V], da[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[i] = cx[j].at(i);
+      taps_sum<V, K>(f, u, h, a);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float g = sigmoid(a[i]);
-        da[i] = p.silu ? cd[j][i] * (g * (1.0f + a[i] * (1.0f - g))) : cd[j][i];
+        const float g = sigmoid(a[i]), dy_ = cd[j].at(i);
+        da[i] = p.silu ? dy_ * (g * (1.0f + a[i] * (1.0f - g))) : dy_;
       }
       if (t + j < t1) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          dw[K - 1][i] += da[i] * cx[j][i];
+          dw[K - 1][i] += da[i] * u[i];
 #pragma unroll
           for (int k = 1; k < K; ++k) dw[K - 1 - k][i] += da[i] * h.v[k - 1][i];
           db[i] += da[i];
@@ -399,17 +413,15 @@ __global__ __launch_bounds__(256) void k_short_conv_bwd(ConvParams p) {
         for (int k = 1; k < K; ++k) v[i] += f.w[k][i] * d.v[k - 1][i];
       }
       put(t + j - (K - 1), v);
-      h.push(cx[j]);
+      h.push(u);
       d.push(da);
       done = t + j + 1;
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        cx[j][i] = nx[j][i];
-        cd[j][i] = nd[j][i];
-      }
+    for (int j = 0; j < kAhead; ++j) {
+      cx[j] = nx[j];
+      cd[j] = nd[j];
+    }
   }
   // the walk ended with the last sequence (or behind the tile, where nothing waits)
   if (done > from && done >= first) flush(done);
