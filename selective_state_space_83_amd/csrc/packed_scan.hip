@@ -37,6 +37,7 @@ constexpr int64_t kTargetWaves = 4096, kShortTargetWaves = 3072;
 constexpr int64_t kShortChunk = 64, kMinChunk = 8, kBalanceChunks = 16, kLongChunk = 256, kNoSplitTokens = 32;
 
 struct Plan {
+  bool wave = false;   // one launch, time across the lanes (k_packed_wave)
   int64_t T = 1, nc = 1, dtiles = 0;
   size_t off_dsum = 0, off_hsum = 0, off_hstart = 0, off_reset = 0, total = 0;
 };
@@ -78,7 +79,19 @@ Plan make_plan(int64_t tokens, int64_t D, int64_t N, int64_t chunk_len, int64_t 
   return pl;
 }
 
+// Whether the launch with time across the lanes takes the problem: the scan's rule
+// (wave_wins in ssm_scan.hip) for one row of its tokens.
+bool wave_wins(int64_t tokens, int64_t D) {
+  const int64_t blocks = (tokens + kWave - 1) / kWave;
+  return tokens <= 512 && D <= std::min<int64_t>(4096, kWave * tokens) / std::max<int64_t>(blocks, 1);
+}
+
 Plan plan_of(const ssm_packed_scan_args_t* a) {
+  if (a->chunk_len == 0 && wave_wins(a->tokens, a->dim)) {
+    Plan pl;
+    pl.wave = true;
+    return pl;
+  }
   int64_t stride = widest_stride(a);
   if (a->z) stride = std::max(stride, a->z_stride);
   return make_plan(a->tokens, a->dim, a->dstate, a->chunk_len, stride, a->h0 && a->h0 == a->h_last);
@@ -252,6 +265,13 @@ ssm_status_t run_chunks(PackedParams p, hipStream_t s) {
 
 template <int N, typename InT, int DISC>
 ssm_status_t run_fwd(const PackedParams& p, hipStream_t s) {
+  if (p.nc == 0) {   // the plan with time across the lanes
+    if (p.z)
+      hipLaunchKernelGGL((k_packed_wave<N, InT, DISC, true>), dim3(uint32_t(p.D)), dim3(kWave * BwdLayout<N>::NG), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_packed_wave<N, InT, DISC, false>), dim3(uint32_t(p.D)), dim3(kWave * BwdLayout<N>::NG), 0, s, p);
+    return launch_status("k_packed_wave");
+  }
   if constexpr (!std::is_same<InT, float>::value && N > 1) {
     if (odd_rows(p.Bm, p.bs) || odd_rows(p.Cm, p.cs)) return run_chunks<N, InT, DISC, true>(p, s);
   }
@@ -477,7 +497,7 @@ ssm_status_t ssm_packed_scan_fwd(const ssm_packed_scan_args_t* a, void* hip_stre
   p.D = a->dim;
   p.q = Seqs{a->offsets, a->slot, a->resume, int32_t(a->tokens), int32_t(a->seqs), 0, int32_t(a->slots)};
   p.T = int32_t(pl.T);
-  p.nc = int32_t(pl.nc);
+  p.nc = pl.wave ? 0 : int32_t(pl.nc);
   p.dtiles = int32_t(pl.dtiles);
   p.exact_thr = exact_threshold(a->disc, a->dtype);
   p.dt_mode = dt_mode_of(a->delta_bias, a->delta_softplus);

@@ -490,6 +490,202 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
   }
 }
 
+// One combine of the lane scan (wave_combine) that stops at sequences: ok says whether
+// the lane the pair comes from belongs to this lane's sequence.
+template <int CTRL, int ROWS, bool RES, int N>
+__device__ __forceinline__ void seq_combine(float (&a)[N], float (&r)[N], float (&bb)[N], bool ok) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float ap = dpp_from<CTRL, ROWS>(a[n], 1.0f), bp = dpp_from<CTRL, ROWS>(bb[n], 0.0f);
+    ap = ok ? ap : 1.0f;
+    bp = ok ? bp : 0.0f;
+    if constexpr (RES) {
+      float rp = dpp_from<CTRL, ROWS>(r[n], 0.0f);
+      rp = ok ? rp : 0.0f;
+      bb[n] = fmaf(a[n], bp, fmaf(r[n], bp, bb[n]));
+      const float m = ap * a[n];
+      r[n] = fmaf(ap, a[n], -m) + fmaf(ap, r[n], rp * a[n]);
+      a[n] = m;
+    } else {
+      bb[n] = fmaf(a[n], bp, bb[n]);
+      a[n] = ap * a[n];
+    }
+  }
+}
+
+// Few tokens of few channels in one launch, with time across the lanes (the scan's
+// k_scan_wave): a workgroup to a channel, a wave to four of its states, 64 tokens at a
+// time, their pairs (Abar, Bbar u) scanned over the lanes.  A block in which sequences begin takes the scan that stops
+// at them (its pairs are chosen, not multiplied by 0, which a NaN would pass).  Bound by
+// latency: 128 x 32 x 16 fp32 in three launches %OLD% us a call, so %NEW%.
+template <int N, typename InT, int DISC, bool GATE>
+__global__ void __launch_bounds__(kWave * BwdLayout<N>::NG) k_packed_wave(const PackedParams p) {
+  constexpr int NS = BwdLayout<N>::NS, NG = BwdLayout<N>::NG;
+  // sequences that begin, and end, at a lane's token (each wave its own)
+  __shared__ int32_t first_at[NG][kWave], last_at[NG][kWave];
+  __shared__ float part[2][NG][kWave];   // the waves' parts of y, double-buffered by block
+  const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), lane = threadIdx.x % kWave;
+  const int64_t d = blockIdx.x, DN = p.D * N, dn = d * N + w * NS;
+  const int32_t tokens = p.q.tokens, S = p.q.S;
+  // what the loop needs first is requested at once: a block's rows (of tokens that may
+  // belong to no sequence: their values are dropped), and 64 sequences' offsets
+  struct Rows {
+    InT x, dl, z, B[NS], C[NS];
+  };
+  auto request = [&](int32_t t0) {
+    const int64_t t = tokens - t0 > lane ? t0 + lane : tokens - 1;
+    Rows r;
+    r.x = static_cast<const InT*>(p.x)[t * p.xs + d];
+    r.dl = static_cast<const InT*>(p.delta)[t * p.dls + d];
+    if constexpr (GATE) r.z = static_cast<const InT*>(p.z)[t * p.zs + d];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      r.B[n] = static_cast<const InT*>(p.Bm)[t * p.bs + w * NS + n];
+      r.C[n] = static_cast<const InT*>(p.Cm)[t * p.cs + w * NS + n];
+    }
+    return r;
+  };
+  auto begin_of = [&](int32_t s) { return ssmq::in_tokens(p.q, p.q.offsets[s < S ? s : S]); };
+  Rows rows{};
+  if (tokens > 0) rows = request(0);
+  const bool few = S <= kWave;
+  int32_t b0 = begin_of(lane), e0 = begin_of(lane + 1);
+  ChanConst<NS, DISC> cc;
+  load_chan<NS, DISC>(cc, p.A + dn, p.exact_thr);
+  const float dsk = p.Dskip ? p.Dskip[d] : 0.0f;
+  const int dtm = p.dt_mode;
+  const float dtb = p.dt_bias ? p.dt_bias[d] : 0.0f;
+  const int32_t lo = seq_start(p.q, 0), hi = seq_start(p.q, S);
+  // the state sequence s starts from, into h
+  auto initial = [&](float (&h)[NS], int32_t s) {
+    zero_n(h);
+    const int32_t slot = p.q.slot ? p.q.slot[s] : s;
+    if (p.h0 && slot >= 0 && slot < p.q.slots && (!p.q.resume || p.q.resume[s])) load_n(h, p.h0 + int64_t(slot) * DN + dn);
+  };
+  auto keep = [&](const float (&h)[NS], int32_t s) {
+    const int32_t slot = p.q.slot ? p.q.slot[s] : s;
+    if (p.h_last && slot >= 0 && slot < p.q.slots) store_n(p.h_last + int64_t(slot) * DN + dn, h);
+  };
+  float hc[NS];   // the state that enters the block (wave-uniform)
+  zero_n(hc);
+  int32_t t0 = 0;
+  do {
+    const int32_t t = t0 + lane, limit = tokens - t0 > kWave ? t0 + kWave : tokens + 1;
+    first_at[w][lane] = last_at[w][lane] = -1;
+    __builtin_amdgcn_wave_barrier();   // (a wave's LDS accesses stay in order)
+    for (int32_t s0 = few ? 0 : seqs_before(p.q, t0) - 1; s0 < S; s0 += kWave) {
+      const int32_t s = s0 + lane;
+      bool more = false;
+      if (s >= 0 && s < S) {
+        const int32_t b = few ? b0 : begin_of(s), e = few ? e0 : begin_of(s + 1);
+        more = b < limit;
+        if (e > b) {
+          if (b >= t0 && b < t0 + kWave) first_at[w][b - t0] = s;
+          if (e > t0 && e <= t0 + kWave) last_at[w][e - 1 - t0] = s;
+        } else if (b >= t0 && b < limit) {
+          float h[NS];   // a sequence without tokens, whose place is here
+          initial(h, s);
+          keep(h, s);
+        }
+      }
+      if (!(__builtin_amdgcn_ballot_w64(more) >> (kWave - 1))) break;
+    }
+    __builtin_amdgcn_wave_barrier();
+    Rows next{};
+    if (t0 + kWave < tokens) next = request(t0 + kWave);
+    if (t0 < hi && t0 + kWave > lo) {
+      const int32_t begins = first_at[w][lane], ends = last_at[w][lane];
+      const bool in = t >= lo && t < hi;
+      float u = ld(&rows.x), dv = ld(&rows.dl);
+      if (dtm != kDtRaw) dv = dt_transform(dv, dtb, dtm);
+      const float zv = GATE ? ld(&rows.z) : 0.0f;
+      float Bv[NS], Cv[NS];
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        Bv[n] = ld(&rows.B[n]);
+        Cv[n] = ld(&rows.C[n]);
+      }
+      if (!in) {   // the identity pair: a = exp(0) = 1, b = 0
+        u = dv = 0.0f;
+        zero_n(Bv);
+      }
+      float hs[NS];
+      zero_n(hs);
+      if (begins >= 0) initial(hs, begins);
+      // the lane of the last first token at or before this one; -1: before the block
+      const uint64_t starts = __builtin_amdgcn_ballot_w64(begins >= 0), at = starts & (~0ull >> (kWave - 1 - lane));
+      const int from = at ? kWave - 1 - __builtin_clzll(at) : -1;
+      float h[NS];
+      auto block = [&](auto form) {
+        constexpr bool RES = decltype(form)::value;
+        float a[NS], r[NS], bb[NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const float z2 = dv * cc.A2[n];
+          a[n] = exp2_fast(z2);
+          r[n] = (RES || DISC == kZoh) ? exp_residual<true>(z2, a[n]) : 0.0f;
+          float gu;   // the input factor times u
+          if constexpr (DISC == kDeltaB) {
+            gu = dv * u;
+          } else {
+            const float e = (a[n] - 1.0f) + r[n];   // expm1(Delta A)
+            gu = (cc.invA[n] != 0.0f) ? (e * cc.invA[n]) * u : dv * u;   // A = 0: limit Delta
+          }
+          bb[n] = gu * Bv[n];
+          if (begins >= 0) bb[n] = fmaf(a[n], hs[n], fmaf(RES ? r[n] : 0.0f, hs[n], bb[n]));
+        }
+        if ((starts & ~1ull) == 0) {   // no sequence begins within the block
+          wave_scan<RES>(a, r, bb);
+        } else {
+          seq_combine<0x111, 0xF, RES>(a, r, bb, lane - 1 >= from);
+          seq_combine<0x112, 0xF, RES>(a, r, bb, lane - 2 >= from);
+          seq_combine<0x114, 0xF, RES>(a, r, bb, lane - 4 >= from);
+          seq_combine<0x118, 0xF, RES>(a, r, bb, lane - 8 >= from);
+          seq_combine<0x142, 0xA, RES>(a, r, bb, (lane & ~15) - 1 >= from);
+          seq_combine<0x143, 0xC, RES>(a, r, bb, 31 >= from);
+        }
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const float on = RES ? fmaf(a[n], hc[n], fmaf(r[n], hc[n], bb[n])) : fmaf(a[n], hc[n], bb[n]);
+          h[n] = from >= 0 ? bb[n] : on;
+        }
+      };
+      if (__builtin_amdgcn_ballot_w64(dv < cc.thr) != 0)
+        block(std::true_type{});
+      else
+        block(std::false_type{});
+      float even = 0.0f, odd = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        if (n & 1)
+          odd = fmaf(Cv[n], h[n], odd);
+        else
+          even = fmaf(Cv[n], h[n], even);
+      }
+      float sum = even + odd;
+      if constexpr (NG > 1) {
+        float(&all)[NG][kWave] = part[(t0 / kWave) & 1];
+        all[w][lane] = sum;
+        __syncthreads();
+        sum = all[0][lane];
+#pragma unroll
+        for (int v = 1; v < NG; ++v) sum += all[v][lane];
+      }
+      float yv = fmaf(dsk, u, sum);
+      if constexpr (GATE) yv *= silu(zv);
+      if (in && w == 0) st(static_cast<InT*>(p.y) + int64_t(t) * p.D + d, yv);
+      if (ends >= 0) keep(h, ends);
+      if (p.hsave && in && t + 1 < tokens && (t + 1) % kSaveStride == 0)
+        store_n(p.hsave + (int64_t((t + 1) / kSaveStride) - 1) * DN + dn, h);
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+        hc[n] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(h[n]), kWave - 1));
+    }
+    rows = next;
+    t0 += kWave;
+  } while (t0 < tokens);
+}
+
 struct PackedStepParams {
   const void* x;
   const void* delta;

@@ -114,7 +114,8 @@ def declare(lib) -> None:
 
 
 # ---------------------------------------------------------------------------
-# checks
+# checks (small calls take as long as the host's part: each argument structure is
+# filled in one go, which takes a third of the time of its fields one by one)
 # ---------------------------------------------------------------------------
 
 def _rows2(t, name, shape, dtype, dev):
@@ -130,6 +131,18 @@ def _even_rows(t, name, like, dev):
     return _norm_rows(t, name, like, dev)
 
 
+def _out(out, name, like, shape, dtype, dev, torch):
+    """An output and its address: the one given, checked, or a new one."""
+    if out is None:
+        # (like has contiguous channels and evenly spaced rows: empty_like is contiguous)
+        if dtype is like.dtype and shape == like.shape:
+            out = torch.empty_like(like)
+        else:
+            out = torch.empty(shape, dtype=dtype, device=like.device)
+        return out, out.data_ptr()
+    return out, _dense(out, name, shape, dtype, dev)
+
+
 def _act(act):
     if act is None:
         return SSM_ACT_NONE
@@ -138,51 +151,38 @@ def _act(act):
     raise ValueError("act must be None or 'silu'")
 
 
-def _offsets(a, offsets, dev):
-    """Fills the offsets; returns the number of sequences."""
-    if offsets.dim() != 1 or offsets.shape[0] < 1:
+def _offsets(offsets, int32, dev):
+    """Address of the offsets, and the number of sequences."""
+    shape = offsets.shape
+    if len(shape) != 1 or shape[0] < 1:
         raise ValueError("offsets must be (sequences + 1,)")
-    a.seqs = offsets.shape[0] - 1
-    a.offsets = _dense(offsets, "offsets", offsets.shape, _torch().int32, dev)
-    return a.seqs
+    return _dense(offsets, "offsets", shape, int32, dev), shape[0] - 1
 
 
-def _places(a, slots, resume, seqs, dev):
-    """Fills the slots and the resume flags of `seqs` sequences."""
-    torch = _torch()
-    a.slot = _dense(slots, "slots", (seqs,), torch.int32, dev)
-    if resume is not None:
-        dt = resume.dtype
-        if dt is not torch.bool and dt is not torch.uint8:
-            raise ValueError("resume must have dtype torch.bool")
-        a.resume = _dense(resume, "resume", (seqs,), dt, dev)
+def _resume(resume, seqs, torch, dev):
+    if resume is None:
+        return None
+    dt = resume.dtype
+    if dt is not torch.bool and dt is not torch.uint8:
+        raise ValueError("resume must have dtype torch.bool")
+    return _dense(resume, "resume", (seqs,), dt, dev)
 
 
-def _recurrence(a, x, delta, A, B, C, D, zoh, dev):
-    """Fills what the three calls of the recurrence share; returns (rows, dim), N and
-    x's dtype."""
-    if x.dim() != 2 or A.dim() != 2:
+def _recurrence(x, delta, A, B, C, D, zoh, f32, dev):
+    """What the three calls of the recurrence share: the shape of x, N, x's dtype, then
+    (strides), (dtype and discretization codes), (addresses)."""
+    shape, coef = x.shape, A.shape
+    if len(shape) != 2 or len(coef) != 2:
         raise ValueError("x must be (tokens, dim) and A (dim, N)")
-    shape, dt, f32 = x.shape, x.dtype, _torch().float32
-    dim, N = shape[1], A.shape[1]
-    a.dim, a.dstate = dim, N
-    a.dtype = _code(x, "x")
-    a.disc = SSM_DISC_ZOH if zoh else SSM_DISC_DELTA_B
-    a.x, a.x_stride = _rows2(x, "x", shape, dt, dev)
-    a.delta, a.delta_stride = _rows2(delta, "delta", shape, dt, dev)
+    dt, dim, N = x.dtype, shape[1], coef[1]
+    code = _code(x, "x")
     narrow = (shape[0], N)
-    a.Bm, a.b_stride = _rows2(B, "B", narrow, dt, dev)
-    a.Cm, a.c_stride = _rows2(C, "C", narrow, dt, dev)
-    a.A = _dense(A, "A", (dim, N), f32, dev)
-    a.Dskip = _dense(D, "D", (dim,), f32, dev)
-    return shape, N, dt
-
-
-def _step_size(a, delta_bias, delta_softplus, z, shape, dt, dev):
-    a.delta_bias = _dense(delta_bias, "delta_bias", shape[1:], _torch().float32, dev)
-    a.delta_softplus = 1 if delta_softplus else 0
-    if z is not None:
-        a.z, a.z_stride = _rows2(z, "z", shape, dt, dev)
+    px, xs = _rows2(x, "x", shape, dt, dev)
+    pd, ds = _rows2(delta, "delta", shape, dt, dev)
+    pb, bs = _rows2(B, "B", narrow, dt, dev)
+    pc, cs = _rows2(C, "C", narrow, dt, dev)
+    return (shape, N, dt, (xs, ds, bs, cs), (code, SSM_DISC_ZOH if zoh else SSM_DISC_DELTA_B),
+            (px, pd, _dense(A, "A", (dim, N), f32, dev), pb, pc, _dense(D, "D", (dim,), f32, dev)))
 
 
 def packed_states_shape(tokens: int, dim: int, dstate: int) -> tuple:
@@ -202,40 +202,43 @@ def packed_scan(x, delta, A, B, C, offsets, D=None, h0=None, h_last=None, slots=
     (dim, N).  Sequence s starts from entry slots[s] (s without slots) of h0 (float32,
     (slots, dim, N)), or from zero, and leaves its last state in that entry of h_last;
     ``h_last=h0`` updates a cache in place.  With ``want_h_last`` and no h_last one is
-    made, a state per sequence.  ``h_saved`` (float32, ``packed_states_shape(...)``) is
-    filled for ``packed_scan_bwd``.  Returns (y, h_last)."""
+    made, a state per sequence (with slots a copy of h0 to begin with).  ``h_saved``
+    (float32, ``packed_states_shape(...)``) is filled for ``packed_scan_bwd``.  Returns
+    (y, h_last)."""
     torch = _torch()
+    f32, int32 = torch.float32, torch.int32
     lib = load_library()
     dev, handle = _current(stream)
     with _on_stream(stream):
-        a = PackedScanArgs()
-        shape, N, dt = _recurrence(a, x, delta, A, B, C, D, zoh, dev)
-        a.tokens = shape[0]
-        seqs = _offsets(a, offsets, dev)
+        shape, N, dt, (xs, ds, bs, cs), codes, (px, pd, pA, pB, pC, pD) = _recurrence(x, delta, A, B, C, D, zoh, f32, dev)
+        tokens, dim = shape
+        p_off, seqs = _offsets(offsets, int32, dev)
         if h_last is None and want_h_last:
             if slots is not None and h0 is None:
                 raise ValueError("with slots, h_last must be given")
-            h_last = x.new_empty((seqs, shape[1], N) if h0 is None else h0.shape, dtype=torch.float32)
+            h_last = torch.empty((seqs, dim, N) if h0 is None else h0.shape, dtype=f32, device=x.device)
             if slots is not None:
                 h_last.copy_(h0)   # the entries of no sequence
+        entries = 0
+        p_h0 = p_last = None
         cache = h0 if h0 is not None else h_last
         if cache is not None:
             if cache.dim() != 3:
                 raise ValueError("states must be (slots, dim, N)")
-            states = (cache.shape[0], shape[1], N)
-            a.slots = states[0]
-            a.h0 = _dense(h0, "h0", states, torch.float32, dev)
-            a.h_last = _dense(h_last, "h_last", states, torch.float32, dev)
-        _places(a, slots, resume, seqs, dev)
-        _step_size(a, delta_bias, delta_softplus, z, shape, dt, dev)
-        a.h_saved = _dense(h_saved, "h_saved", packed_states_shape(shape[0], shape[1], N), torch.float32, dev)
-        if y is None:
-            y = x.new_empty(shape)
-        a.y = _dense(y, "y", shape, dt, dev)
-        a.chunk_len = int(chunk_len)
-        need = lib.ssm_packed_scan_workspace_size(ctypes.byref(a))
-        workspace = _workspace(a, need, workspace, x, dev)
-        status = lib.ssm_packed_scan_fwd(ctypes.byref(a), handle)
+            entries = cache.shape[0]
+            states = (entries, dim, N)
+            p_h0 = _dense(h0, "h0", states, f32, dev)
+            p_last = p_h0 if h_last is h0 else _dense(h_last, "h_last", states, f32, dev)
+        p_z, zs = (None, 0) if z is None else _rows2(z, "z", shape, dt, dev)
+        y, p_y = _out(y, "y", x, shape, dt, dev, torch)
+        a = PackedScanArgs(
+            tokens, seqs, entries, dim, N, xs, ds, zs, bs, cs, *codes, 1 if delta_softplus else 0, int(chunk_len),
+            px, pd, pA, pB, pC, pD, _dense(delta_bias, "delta_bias", (dim,), f32, dev), p_z, p_off,
+            _dense(slots, "slots", (seqs,), int32, dev), _resume(resume, seqs, torch, dev), p_h0, p_last,
+            _dense(h_saved, "h_saved", packed_states_shape(tokens, dim, N), f32, dev), p_y)
+        arg = ctypes.byref(a)
+        workspace = _workspace(a, lib.ssm_packed_scan_workspace_size(arg), workspace, x, dev)
+        status = lib.ssm_packed_scan_fwd(arg, handle)
     _raise_for(lib, status)
     return y, h_last
 
@@ -245,21 +248,22 @@ def packed_step(h, x, delta, A, B, C, D=None, slots=None, zoh=False, delta_bias=
     """One token for each row of a batch: x, delta, z (batch, dim), B, C (batch, N); row
     b's state is entry slots[b] (b without slots) of h (float32, (slots, dim, N)), updated
     in place.  Returns y (batch, dim)."""
+    torch = _torch()
+    f32 = torch.float32
     lib = load_library()
     dev, handle = _current(stream)
     with _on_stream(stream):
-        a = PackedStepArgs()
-        shape, N, dt = _recurrence(a, x, delta, A, B, C, D, zoh, dev)
-        a.batch = shape[0]
+        shape, N, dt, (xs, ds, bs, cs), codes, (px, pd, pA, pB, pC, pD) = _recurrence(x, delta, A, B, C, D, zoh, f32, dev)
+        batch, dim = shape
         if h.dim() != 3:
             raise ValueError("h must be (slots, dim, N)")
-        a.slots = h.shape[0]
-        a.h = _dense(h, "h", (h.shape[0], shape[1], N), _torch().float32, dev)
-        a.slot = _dense(slots, "slots", shape[:1], _torch().int32, dev)
-        _step_size(a, delta_bias, delta_softplus, z, shape, dt, dev)
-        if y is None:
-            y = x.new_empty(shape)
-        a.y = _dense(y, "y", shape, dt, dev)
+        entries = h.shape[0]
+        p_z, zs = (None, 0) if z is None else _rows2(z, "z", shape, dt, dev)
+        y, p_y = _out(y, "y", x, shape, dt, dev, torch)
+        a = PackedStepArgs(
+            batch, entries, dim, N, xs, ds, zs, bs, cs, *codes, 1 if delta_softplus else 0, 0,
+            px, pd, pA, pB, pC, pD, _dense(delta_bias, "delta_bias", (dim,), f32, dev), p_z,
+            _dense(slots, "slots", (batch,), torch.int32, dev), _dense(h, "h", (entries, dim, N), f32, dev), p_y)
         status = lib.ssm_packed_step(ctypes.byref(a), handle)
     _raise_for(lib, status)
     return y
@@ -271,32 +275,32 @@ def packed_scan_bwd(x, delta, A, B, C, offsets, dy, h_saved, D=None, h0=None, dh
     per sequence, no softplus, bias or gate) from the states its call kept (h_saved): a
     dict of float32 tensors dx, ddelta, dA, dB, dC and, when asked, dD and dh0."""
     torch = _torch()
+    f32 = torch.float32
     lib = load_library()
     dev, handle = _current(stream)
-    f32 = torch.float32
     with _on_stream(stream):
-        a = PackedScanBwdArgs()
-        shape, N, dt = _recurrence(a, x, delta, A, B, C, D, zoh, dev)
-        a.tokens = shape[0]
-        seqs = _offsets(a, offsets, dev)
-        states = (seqs, shape[1], N)
-        a.dy, a.dy_stride = _rows2(dy, "dy", shape, dt, dev)
-        a.h0 = _dense(h0, "h0", states, f32, dev)
-        a.dh_last = _dense(dh_last, "dh_last", states, f32, dev)
-        a.h_saved = _dense(h_saved, "h_saved", packed_states_shape(shape[0], shape[1], N), f32, dev)
-        g = {"dx": x.new_empty(shape, dtype=f32), "ddelta": x.new_empty(shape, dtype=f32),
-             "dA": A.new_empty(A.shape), "dB": x.new_empty((shape[0], N), dtype=f32),
-             "dC": x.new_empty((shape[0], N), dtype=f32)}
+        shape, N, dt, (xs, ds, bs, cs), codes, (px, pd, pA, pB, pC, pD) = _recurrence(x, delta, A, B, C, D, zoh, f32, dev)
+        tokens, dim = shape
+        p_off, seqs = _offsets(offsets, torch.int32, dev)
+        states = (seqs, dim, N)
+        p_dy, ys = _rows2(dy, "dy", shape, dt, dev)
+        g = {"dx": torch.empty(shape, dtype=f32, device=x.device), "ddelta": torch.empty(shape, dtype=f32, device=x.device),
+             "dA": A.new_empty(A.shape), "dB": torch.empty((tokens, N), dtype=f32, device=x.device),
+             "dC": torch.empty((tokens, N), dtype=f32, device=x.device)}
         if want_dD:
-            g["dD"] = x.new_empty(shape[1:], dtype=f32)
+            g["dD"] = torch.empty((dim,), dtype=f32, device=x.device)
         if want_dh0:
-            g["dh0"] = x.new_empty(states, dtype=f32)
-        for name, t in g.items():
-            setattr(a, name, t.data_ptr())
-        a.super_chunk = int(super_chunk)
-        need = lib.ssm_packed_scan_bwd_workspace_size(ctypes.byref(a))
-        workspace = _workspace(a, need, workspace, x, dev)
-        status = lib.ssm_packed_scan_bwd(ctypes.byref(a), handle)
+            g["dh0"] = torch.empty(states, dtype=f32, device=x.device)
+        a = PackedScanBwdArgs(
+            tokens, seqs, dim, N, xs, ds, bs, cs, ys, *codes, int(super_chunk), 0,
+            px, pd, pA, pB, pC, pD, p_off, _dense(h0, "h0", states, f32, dev),
+            _dense(h_saved, "h_saved", packed_states_shape(tokens, dim, N), f32, dev), p_dy,
+            _dense(dh_last, "dh_last", states, f32, dev), g["dx"].data_ptr(), g["ddelta"].data_ptr(), g["dA"].data_ptr(),
+            g["dB"].data_ptr(), g["dC"].data_ptr(), g["dD"].data_ptr() if want_dD else None,
+            g["dh0"].data_ptr() if want_dh0 else None)
+        arg = ctypes.byref(a)
+        workspace = _workspace(a, lib.ssm_packed_scan_bwd_workspace_size(arg), workspace, x, dev)
+        status = lib.ssm_packed_scan_bwd(arg, handle)
     _raise_for(lib, status)
     return g
 
@@ -305,30 +309,31 @@ def packed_scan_bwd(x, delta, A, B, C, offsets, dy, h_saved, D=None, h0=None, dh
 # short convolution
 # ---------------------------------------------------------------------------
 
-def _conv_args(a, x, weight, bias, act, dev):
-    if weight.dim() != 2:
+def _conv_args(x, weight, bias, f32, dev):
+    """channels, K, x's stride and dtype code, and the addresses of x, weight and bias."""
+    taps, shape = weight.shape, x.shape
+    if len(taps) != 2:
         raise ValueError("weight must be (channels, K)")
-    if x.dim() < 2:
+    if len(shape) < 2:
         raise ValueError("x must be (tokens, channels) or (batch, L, channels)")
-    f32, C = _torch().float32, x.shape[-1]
-    a.channels, a.taps = C, weight.shape[1]
-    a.dtype, a.act = _code(x, "x"), _act(act)
-    a.x, a.x_stride = _even_rows(x, "x", x, dev)
-    a.weight = _dense(weight, "weight", (C, weight.shape[1]), f32, dev)
-    a.bias = _dense(bias, "bias", (C,), f32, dev)
+    channels = shape[-1]
+    code = _code(x, "x")
+    px, xs = _even_rows(x, "x", x, dev)
+    return (channels, taps[1], xs, code,
+            (px, _dense(weight, "weight", (channels, taps[1]), f32, dev), _dense(bias, "bias", (channels,), f32, dev)))
 
 
-def _conv_seqs(a, x, offsets, dev):
+def _conv_seqs(x, offsets, int32, dev):
+    """tokens, sequences, tokens of each (0 with offsets) and the offsets' address."""
+    shape = x.shape
     if offsets is not None:
-        if x.dim() != 2:
+        if len(shape) != 2:
             raise ValueError("with offsets x must be (tokens, channels)")
-        a.tokens = x.shape[0]
-        return _offsets(a, offsets, dev)
-    if x.dim() != 3:
+        p_off, seqs = _offsets(offsets, int32, dev)
+        return shape[0], seqs, 0, p_off
+    if len(shape) != 3:
         raise ValueError("without offsets x must be (batch, L, channels)")
-    a.seqs, a.seqlen = x.shape[:2]
-    a.tokens = a.seqs * a.seqlen
-    return a.seqs
+    return shape[0] * shape[1], shape[0], shape[1], None
 
 
 def short_conv(x, weight, bias=None, offsets=None, act="silu", state=None, slots=None, resume=None, y=None,
@@ -338,21 +343,22 @@ def short_conv(x, weight, bias=None, offsets=None, act="silu", state=None, slots
     (channels,), float32.  ``state`` (float32, (slots, channels, K - 1), oldest input
     first) holds the inputs before each sequence and is moved on in place; without it
     sequences start from zeros.  Returns y like x."""
+    torch = _torch()
+    f32, int32 = torch.float32, torch.int32
     lib = load_library()
     dev, handle = _current(stream)
     with _on_stream(stream):
-        a = ShortConvArgs()
-        _conv_args(a, x, weight, bias, act, dev)
-        seqs = _conv_seqs(a, x, offsets, dev)
+        channels, K, xs, code, where = _conv_args(x, weight, bias, f32, dev)
+        tokens, seqs, seqlen, p_off = _conv_seqs(x, offsets, int32, dev)
+        entries, p_state = 0, None
         if state is not None:
             if state.dim() != 3:
                 raise ValueError("state must be (slots, channels, K - 1)")
-            a.slots = state.shape[0]
-            a.state = _dense(state, "state", (state.shape[0], x.shape[-1], weight.shape[1] - 1), _torch().float32, dev)
-        _places(a, slots, resume, seqs, dev)
-        if y is None:
-            y = x.new_empty(x.shape)
-        a.y = _dense(y, "y", x.shape, x.dtype, dev)
+            entries = state.shape[0]
+            p_state = _dense(state, "state", (entries, channels, K - 1), f32, dev)
+        y, p_y = _out(y, "y", x, x.shape, x.dtype, dev, torch)
+        a = ShortConvArgs(tokens, seqs, seqlen, entries, channels, xs, code, K, _act(act), 0, *where, p_off,
+                          _dense(slots, "slots", (seqs,), int32, dev), _resume(resume, seqs, torch, dev), p_state, p_y)
         status = lib.ssm_short_conv_fwd(ctypes.byref(a), handle)
     _raise_for(lib, status)
     return y
@@ -361,19 +367,19 @@ def short_conv(x, weight, bias=None, offsets=None, act="silu", state=None, slots
 def short_conv_step(state, x, weight, bias=None, act="silu", slots=None, y=None, stream=None):
     """One token for each row of x (batch, channels): row b's window is entry slots[b] (b
     without slots) of state, moved on in place.  Returns y (batch, channels)."""
+    torch = _torch()
+    f32 = torch.float32
     lib = load_library()
     dev, handle = _current(stream)
     with _on_stream(stream):
-        a = ShortConvStepArgs()
         if x.dim() != 2 or state.dim() != 3:
             raise ValueError("x must be (batch, channels) and state (slots, channels, K - 1)")
-        _conv_args(a, x, weight, bias, act, dev)
-        a.batch, a.slots = x.shape[0], state.shape[0]
-        a.state = _dense(state, "state", (state.shape[0], x.shape[1], weight.shape[1] - 1), _torch().float32, dev)
-        a.slot = _dense(slots, "slots", x.shape[:1], _torch().int32, dev)
-        if y is None:
-            y = x.new_empty(x.shape)
-        a.y = _dense(y, "y", x.shape, x.dtype, dev)
+        channels, K, xs, code, where = _conv_args(x, weight, bias, f32, dev)
+        batch, entries = x.shape[0], state.shape[0]
+        y, p_y = _out(y, "y", x, x.shape, x.dtype, dev, torch)
+        a = ShortConvStepArgs(batch, entries, channels, xs, code, K, _act(act), 0, *where,
+                              _dense(slots, "slots", (batch,), torch.int32, dev),
+                              _dense(state, "state", (entries, channels, K - 1), f32, dev), p_y)
         status = lib.ssm_short_conv_step(ctypes.byref(a), handle)
     _raise_for(lib, status)
     return y
@@ -383,24 +389,25 @@ def short_conv_bwd(x, weight, dy, bias=None, offsets=None, act="silu", want_dwei
                    workspace=None, stream=None) -> dict:
     """The gradients of sum(dy * y) of ``short_conv`` without a state: dx (x's dtype) and,
     when asked, dweight and dbias (float32; dbias also where bias is None)."""
+    torch = _torch()
+    f32 = torch.float32
     lib = load_library()
     dev, handle = _current(stream)
-    f32 = _torch().float32
     with _on_stream(stream):
-        a = ShortConvBwdArgs()
-        _conv_args(a, x, weight, bias, act, dev)
-        _conv_seqs(a, x, offsets, dev)
-        a.dy, a.dy_stride = _even_rows(dy, "dy", x, dev)
+        channels, K, xs, code, where = _conv_args(x, weight, bias, f32, dev)
+        tokens, seqs, seqlen, p_off = _conv_seqs(x, offsets, torch.int32, dev)
+        p_dy, ys = _even_rows(dy, "dy", x, dev)
         g = {"dx": x.new_empty(x.shape)}
         if want_dweight:
             g["dweight"] = weight.new_empty(weight.shape)
         if want_dbias:
-            g["dbias"] = x.new_empty(x.shape[-1:], dtype=f32)
-        for name, t in g.items():
-            setattr(a, name, t.data_ptr())
-        need = lib.ssm_short_conv_bwd_workspace_size(ctypes.byref(a))
-        workspace = _workspace(a, need, workspace, x, dev)
-        status = lib.ssm_short_conv_bwd(ctypes.byref(a), handle)
+            g["dbias"] = torch.empty((channels,), dtype=f32, device=x.device)
+        a = ShortConvBwdArgs(tokens, seqs, seqlen, channels, xs, ys, code, K, _act(act), 0, *where, p_off, p_dy,
+                             g["dx"].data_ptr(), g["dweight"].data_ptr() if want_dweight else None,
+                             g["dbias"].data_ptr() if want_dbias else None)
+        arg = ctypes.byref(a)
+        workspace = _workspace(a, lib.ssm_short_conv_bwd_workspace_size(arg), workspace, x, dev)
+        status = lib.ssm_short_conv_bwd(arg, handle)
     _raise_for(lib, status)
     return g
 
@@ -409,10 +416,10 @@ def short_conv_bwd(x, weight, dy, bias=None, offsets=None, act="silu", want_dwei
 # residual and norm
 # ---------------------------------------------------------------------------
 
-def _wide(t, name, dtype):
+def _wide(t, name, dtype, f32):
     """dtype code of the residual stream: that of x, or float32."""
     code = _code(t, name)
-    if t.dtype is not dtype and t.dtype is not _torch().float32:
+    if t.dtype is not dtype and t.dtype is not f32:
         raise ValueError("%s must have x's dtype or float32" % name)
     return code
 
@@ -426,37 +433,34 @@ def _stream_rows(t, name, shape, dev):
 
 def _add_norm(x, residual, weight, eps, block, quant, y, total, keep, stream):
     torch = _torch()
+    f32 = torch.float32
     lib = load_library()
     dev, handle = _current(stream)
-    f32 = torch.float32
     with _on_stream(stream):
-        a = AddNormArgs()
-        if x.dim() < 1:
+        shape, dt = x.shape, x.dtype
+        if len(shape) < 1:
             raise ValueError("x must be (..., channels)")
-        shape, C = x.shape, x.shape[-1]
-        a.channels, a.rows = C, x.numel() // C if C else 0
-        a.block, a.eps = int(block), float(eps)
-        a.dtype = a.residual_dtype = _code(x, "x")
-        a.x, a.x_stride = _even_rows(x, "x", x, dev)
-        a.weight = _dense(weight, "weight", (C,), f32, dev)
+        C = shape[-1]
+        block = int(block)
+        code = wide = _code(x, "x")
+        px, xs = _even_rows(x, "x", x, dev)
+        p_res, rs, p_sum = None, 0, None
         if residual is None:
             if total is not None:
                 raise ValueError("total goes with residual")
             total = x
         else:
-            a.residual_dtype = _wide(residual, "residual", x.dtype)
-            a.residual, a.residual_stride = _stream_rows(residual, "residual", shape, dev)
-            if total is None and keep:
-                total = residual.new_empty(shape)
-            a.sum = _dense(total, "total", shape, residual.dtype, dev)
-        if y is None:
-            y = x.new_empty(shape, dtype=torch.float8_e4m3fn if quant else x.dtype)
-        a.y = _dense(y, "y", shape, torch.float8_e4m3fn if quant else x.dtype, dev)
-        a.y_dtype = SSM_E4M3 if quant else a.dtype
-        scale = None
+            wide = _wide(residual, "residual", dt, f32)
+            p_res, rs = _stream_rows(residual, "residual", shape, dev)
+            if total is not None or keep:
+                total, p_sum = _out(total, "total", x, shape, residual.dtype, dev, torch)
+        ydt = torch.float8_e4m3fn if quant else dt
+        y, p_y = _out(y, "y", x, shape, ydt, dev, torch)
+        scale, p_scale = None, None
         if quant:
-            scale = x.new_empty(shape[:-1] + (-(-C // block) if block > 0 else 1,), dtype=f32)
-            a.scale = scale.data_ptr()
+            scale, p_scale = _out(None, "scale", x, shape[:-1] + (-(-C // block) if block > 0 else 1,), f32, dev, torch)
+        a = AddNormArgs(x.numel() // C if C else 0, C, block, xs, rs, code, wide, SSM_E4M3 if quant else code, eps, px, p_res,
+                        _dense(weight, "weight", (C,), f32, dev), p_sum, p_y, p_scale)
         status = lib.ssm_add_norm_fwd(ctypes.byref(a), handle)
     _raise_for(lib, status)
     return (y, scale, total) if quant else (y, total)
@@ -483,29 +487,29 @@ def add_rms_norm_bwd(total, dy, weight=None, dsum=None, eps=1e-5, want_dweight=T
     """The gradients of sum(dy * y) + sum(dsum * total) of ``add_rms_norm``, from its
     total: dx in dy's dtype, which is the residual's gradient too; where total has another
     dtype (float32) also dresidual in that; and, when asked, dweight (float32)."""
+    f32 = _torch().float32
     lib = load_library()
     dev, handle = _current(stream)
     with _on_stream(stream):
-        a = AddNormBwdArgs()
-        if dy.dim() < 1:
+        shape, dt = dy.shape, dy.dtype
+        if len(shape) < 1:
             raise ValueError("dy must be (..., channels)")
-        shape, C = dy.shape, dy.shape[-1]
-        a.channels, a.rows, a.eps = C, dy.numel() // C if C else 0, float(eps)
-        a.dtype, a.sum_dtype = _code(dy, "dy"), _wide(total, "total", dy.dtype)
-        a.sum, a.sum_stride = _stream_rows(total, "total", shape, dev)
-        a.dy, a.dy_stride = _even_rows(dy, "dy", dy, dev)
-        if dsum is not None:
-            a.dsum, a.dsum_stride = _even_rows(dsum, "dsum", total, dev)
-        a.weight = _dense(weight, "weight", (C,), _torch().float32, dev)
+        C = shape[-1]
+        code, wide = _code(dy, "dy"), _wide(total, "total", dt, f32)
+        p_sum, ss = _stream_rows(total, "total", shape, dev)
+        p_dy, ds = _even_rows(dy, "dy", dy, dev)
+        p_dsum, gs = (None, 0) if dsum is None else _even_rows(dsum, "dsum", total, dev)
         g = {"dx": dy.new_empty(shape)}
-        if total.dtype is not dy.dtype:
+        both = total.dtype is not dt
+        if both:
             g["dresidual"] = total.new_empty(shape)
         if want_dweight:
-            g["dweight"] = dy.new_empty((C,), dtype=_torch().float32)
-        for name, t in g.items():
-            setattr(a, name, t.data_ptr())
-        need = lib.ssm_add_norm_bwd_workspace_size(ctypes.byref(a))
-        workspace = _workspace(a, need, workspace, dy, dev)
-        status = lib.ssm_add_norm_bwd(ctypes.byref(a), handle)
+            g["dweight"] = dy.new_empty((C,), dtype=f32)
+        a = AddNormBwdArgs(dy.numel() // C if C else 0, C, ss, ds, gs, code, wide, 0, eps, p_sum, p_dy, p_dsum,
+                           _dense(weight, "weight", (C,), f32, dev), g["dx"].data_ptr(),
+                           g["dresidual"].data_ptr() if both else None, g["dweight"].data_ptr() if want_dweight else None)
+        arg = ctypes.byref(a)
+        workspace = _workspace(a, lib.ssm_add_norm_bwd_workspace_size(arg), workspace, dy, dev)
+        status = lib.ssm_add_norm_bwd(arg, handle)
     _raise_for(lib, status)
     return g

@@ -63,7 +63,7 @@ ROWS = dict(x_stride=96, delta_stride=96, b_stride=16, c_stride=16)
 
 
 def scan():
-    return fill(M.PackedScanArgs(), tokens=300, seqs=4, slots=6, dim=96, dstate=16, z_stride=96, workspace_bytes=GB, **ROWS)
+    return fill(M.PackedScanArgs(), tokens=3000, seqs=4, slots=6, dim=96, dstate=16, z_stride=96, workspace_bytes=GB, **ROWS)
 
 
 def step():
