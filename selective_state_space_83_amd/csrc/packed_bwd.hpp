@@ -52,6 +52,86 @@ struct PackedBwdParams {
 // The sequence that holds token t (of those with its first token, the one with any).
 __device__ __forceinline__ int32_t seq_at(const Seqs& q, int32_t t) { return seqs_before(q, t + 1) - 1; }
 
+// One step back of a lane's NS states: bwd_lane_step, with the slow-decay form chosen
+// state by state (see advance).
+template <int NS, int DISC, bool SERIES, bool SHORT>
+__device__ __forceinline__ void retreat(float (&g)[NS], float (&dA)[NS], const ChanConst<NS, DISC>& cc,
+                                        const float (&Bv)[NS], const float (&Cv)[NS], const float (&hp)[NS],
+                                        const float (&hn)[NS], float u, float dv, float dyv, float limit,
+                                        float (&pB)[NS], float (&pC)[NS], float& du, float& ddt) {
+  float z2[NS], a[NS], G[NS], ag[NS];
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    z2[n] = dv * cc.A2[n];
+    a[n] = exp2_fast(z2[n]);
+    G[n] = fmaf(Cv[n], dyv, g[n]);
+    ag[n] = a[n] * G[n];
+  }
+  if (any_exact<NS, DISC>(cc, dv)) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+      // a G plus what rounding took from a (see decay_add)
+      if (any_slow(z2[n], limit)) ag[n] = fmaf(a[n], G[n], exp_residual<true>(z2[n], a[n]) * G[n]);
+  }
+  if constexpr (DISC == kDeltaB) {
+    // du and dDelta's input term are Delta and u times sum_n G B (A is held as
+    // A log2(e); the ln 2 that restores A is applied to the state sum once)
+    const float dvu = dv * u;
+    float gb = 0.0f, dt2 = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      const float agh = ag[n] * hp[n];   // shared by dDelta and dA
+      gb = n ? fmaf(G[n], Bv[n], gb) : G[n] * Bv[n];
+      dt2 = n ? fmaf(cc.A2[n], agh, dt2) : cc.A2[n] * agh;
+      dA[n] = fmaf(dv, agh, dA[n]);
+      pB[n] = G[n] * dvu;
+    }
+    du = dv * gb;
+    ddt = fmaf(dt2, kLn2, u * gb);
+  } else {
+    float su = 0.0f, dt2 = 0.0f, dtb = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      float f = (a[n] - 1.0f) * cc.invA[n];
+      float dfda = fmaf(dv, a[n], -f) * cc.invA[n];
+      if constexpr (SERIES) {
+        // the series of bwd_lane_step where |z| is small, the direct forms elsewhere
+        const float z = z2[n] * kLn2;
+        float q1, q2;
+        if constexpr (SHORT) {
+          q1 = fmaf(z, fmaf(z, 1.0f / 6.0f, 0.5f), 1.0f);
+          q2 = fmaf(z, fmaf(z, 0.125f, 1.0f / 3.0f), 0.5f);
+        } else {
+          q1 = fmaf(z, 1.0f / 120.0f, 1.0f / 24.0f);
+          q1 = fmaf(z, q1, 1.0f / 6.0f);
+          q1 = fmaf(z, q1, 0.5f);
+          q1 = fmaf(z, q1, 1.0f);
+          q2 = fmaf(z, 1.0f / 144.0f, 1.0f / 30.0f);
+          q2 = fmaf(z, q2, 0.125f);
+          q2 = fmaf(z, q2, 1.0f / 3.0f);
+          q2 = fmaf(z, q2, 0.5f);
+        }
+        const bool small = fabsf(z) < series_z<SHORT>() || cc.invA[n] == 0.0f;
+        f = small ? dv * q1 : f;
+        dfda = small ? (dv * dv) * q2 : dfda;
+      }
+      const float agh = ag[n] * hp[n], Bu = Bv[n] * u, Gf = G[n] * f;
+      pB[n] = Gf * u;
+      su = fmaf(Gf, Bv[n], su);
+      dt2 = fmaf(cc.A2[n], agh, dt2);
+      dtb = fmaf(ag[n], Bu, dtb);   // df/dDelta = a
+      dA[n] = fmaf(dv, agh, fmaf(G[n] * dfda, Bu, dA[n]));
+    }
+    du = su;
+    ddt = fmaf(dt2, kLn2, dtb);
+  }
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    pC[n] = dyv * hn[n];
+    g[n] = ag[n];
+  }
+}
+
 // Reverse summary of super-chunks 1 .. nc - 1.
 template <int N, typename InT, int DISC, bool ODD>
 __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) k_packed_bwd_summary(const PackedBwdParams p) {
@@ -78,6 +158,7 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
   const int64_t d = dbase + lo_ch;
   ChanConst<N, DISC> cc;
   load_chan<N, DISC>(cc, p.A + d * N, p.exact_thr);
+  const float limit = p.exact_thr * kLog2e;
   float g[N];
   zero_n(g);
   if (fresh && p.dh_last) load_n(g, p.dh_last + (int64_t(open) * p.D + d) * N);
@@ -97,17 +178,26 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
     Cnext.load(nc);
     float Ccur[N];
     Cthis.widen(Ccur);
-    if (any_exact<N, DISC>(cc, dv)) {   // wave-uniform
+    float z2[N], G[N], a[N];
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float z2 = dv * cc.A2[n];
-        const float G = fmaf(Ccur[n], dyv, g[n]);
-        const float a = exp2_fast(z2);
-        g[n] = fmaf(a, G, exp_residual<true>(z2, a) * G);
+    for (int n = 0; n < N; ++n) {
+      z2[n] = dv * cc.A2[n];
+      a[n] = exp2_fast(z2[n]);
+      G[n] = fmaf(Ccur[n], dyv, g[n]);
+      g[n] = a[n] * G[n];
+    }
+    if (any_exact<N, DISC>(cc, dv)) {   // the slow-decay form, for four states at a time (see advance)
+      constexpr int W = N < 4 ? N : 4;
+#pragma unroll
+      for (int q = 0; q < N; q += W) {
+        float least = fabsf(z2[q]);
+#pragma unroll
+        for (int n = q + 1; n < q + W; ++n) least = fminf(least, fabsf(z2[n]));
+        if (any_slow(least, limit)) {
+#pragma unroll
+          for (int n = q; n < q + W; ++n) g[n] = fmaf(a[n], G[n], exp_residual<true>(z2[n], a[n]) * G[n]);
+        }
       }
-    } else {
-#pragma unroll
-      for (int n = 0; n < N; ++n) g[n] = exp2_fast(dv * cc.A2[n]) * fmaf(Ccur[n], dyv, g[n]);
     }
     Crow = nc;
     const float yv = dv - dcomp, tv = dacc + yv;
@@ -195,6 +285,7 @@ k_packed_bwd(const PackedBwdParams p) {
   ChanConst<NS, DISC> cc;
   load_chan<NS, DISC>(cc, p.A + dn, p.exact_thr);
   const float dsk = p.Dskip ? p.Dskip[d] : 0.0f;
+  const float limit = p.exact_thr * kLog2e;
   constexpr bool kShortSeries = !std::is_same<InT, float>::value;
   float zoh_thr = 0.0f;   // below it ZOH's factor is taken from its series
   if constexpr (DISC == kZoh) {
@@ -323,10 +414,7 @@ k_packed_bwd(const PackedBwdParams p) {
       auto forward = [&](float xv, float dv, const float* row) {
         float Bv[NS];
         lds_row<NS>(Bv, row);
-        if (any_exact<NS, DISC>(cc, dv))
-          ssm_step_lane<NS, DISC, false, true, true>(h, cc, Bv, Bv, xv, dv);
-        else
-          ssm_step_lane<NS, DISC, false, false>(h, cc, Bv, Bv, xv, dv);
+        advance<NS, DISC, false, 1, true>(h, cc, Bv, xv, dv, limit);
       };
       float xa[K], da[K];
       auto rows_of = [&](float (&u)[K], float (&v)[K], int j) {
@@ -403,14 +491,11 @@ k_packed_bwd(const PackedBwdParams p) {
               hn[n] = (js + 1 < H) ? stash[js + 1 < H ? js + 1 : js][n] : h[n];
             }
             if (begins_h >> js & 1) initial(hp, j0 + js);
-            const bool exact = any_exact<NS, DISC>(cc, dv);
             const bool series = DISC == kZoh && __builtin_amdgcn_ballot_w64(dv < zoh_thr) != 0;
             if (series)
-              bwd_lane_step<NS, DISC, true, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, exact, pB, pC, du,
-                                                          ddt);
+              retreat<NS, DISC, true, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, limit, pB, pC, du, ddt);
             else
-              bwd_lane_step<NS, DISC, false, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, exact, pB, pC, du,
-                                                           ddt);
+              retreat<NS, DISC, false, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, limit, pB, pC, du, ddt);
             dDacc = fmaf(dyv, u, dDacc);
             if (begins_h >> js & 1) {
               const PackedBwdParams& b = args_again<PackedBwdParams>();

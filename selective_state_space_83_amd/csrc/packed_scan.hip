@@ -296,7 +296,7 @@ struct BwdPlan {
 
 // Super-chunks: enough for the reverse summary's waves, at most kBwdLong tokens each
 // (more, shorter waves even out the SIMDs).
-constexpr int64_t kBwdLong = 128;
+constexpr int64_t kBwdLong = 64;
 
 BwdPlan bwd_plan(const ssm_packed_scan_bwd_args_t* a) {
   BwdPlan pl;

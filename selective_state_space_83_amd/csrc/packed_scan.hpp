@@ -132,6 +132,75 @@ __device__ __forceinline__ void zero_n(float (&h)[N]) {
   for (int n = 0; n < N; ++n) h[n] = 0.0f;
 }
 
+// |Delta A| log2(e) below this takes the slow-decay form of its step (see
+// ssm_kernels.hpp): the scan's threshold, state by state.
+__device__ __forceinline__ bool any_slow(float z2, float limit) {
+  return __builtin_amdgcn_ballot_w64(fabsf(z2) < limit) != 0;
+}
+
+// One step of a lane's N states.  Where some lane has a decay that slow at all, the
+// form is chosen for every GROUP states on their own: with A[n] about -(n + 1) and
+// steps down to 1e-3, two of three steps are slow for the first state and none for
+// the others (16384 x 1536 x 16 fp32: 88 us for the summaries with one choice for all
+// 16 states, %SUM% so; the output pass 127, %OUT% so).  SCALED carries A h (see
+// ssm_step_lane), SELECT is exp_residual's.
+template <int N, int DISC, bool SCALED, int GROUP, bool SELECT>
+__device__ __forceinline__ void advance(float (&h)[N], const ChanConst<N, DISC>& cc, const float (&Bv)[N], float u,
+                                        float dv, float limit) {
+  const float du = dv * u;
+  auto fast = [&](int n) {
+    const float a = exp2_fast(dv * cc.A2[n]);
+    if constexpr (SCALED) {
+      const float bu = u * Bv[n];
+      h[n] = fmaf(a, h[n] + bu, -bu);
+    } else if constexpr (DISC == kDeltaB) {
+      h[n] = fmaf(a, h[n], du * Bv[n]);
+    } else {
+      const float q = (u * Bv[n]) * cc.invA[n];
+      h[n] = fmaf(a, h[n] + q, -q);
+    }
+  };
+  auto slow = [&](int n) {
+    const float z2 = dv * cc.A2[n], a = exp2_fast(z2), r = exp_residual<SELECT>(z2, a);
+    if constexpr (SCALED) {
+      const float bu = u * Bv[n];
+      h[n] = fmaf(a, h[n], fmaf((a - 1.0f) + r, bu, r * h[n]));   // (a - 1) + r = expm1
+    } else {
+      float gu = du;
+      if constexpr (DISC == kZoh)
+        gu = (cc.invA[n] != 0.0f) ? (((a - 1.0f) + r) * cc.invA[n]) * u : du;   // A = 0: limit Delta
+      h[n] = fmaf(a, h[n], fmaf(gu, Bv[n], r * h[n]));
+    }
+  };
+  if (__builtin_amdgcn_ballot_w64(dv < cc.thr) == 0) {   // wave-uniform, as all these choices
+#pragma unroll
+    for (int n = 0; n < N; ++n) fast(n);
+    return;
+  }
+  constexpr int G = GROUP < N ? GROUP : N;
+  if constexpr (G == N && N > 4) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) slow(n);
+    return;
+  }
+#pragma unroll
+  for (int g = 0; g < N; g += G) {
+    float least = fabsf(dv * cc.A2[g]);
+#pragma unroll
+    for (int n = g + 1; n < g + G; ++n) least = fminf(least, fabsf(dv * cc.A2[n]));
+    if (any_slow(least, limit)) {
+#pragma unroll
+      for (int n = g; n < g + G; ++n) slow(n);
+    } else {
+#pragma unroll
+      for (int n = g; n < g + G; ++n) fast(n);
+    }
+  }
+}
+
+template <int N, typename InT>
+constexpr int kGroup = std::is_same<InT, float>::value ? 4 : N;
+
 // Pass 1: what each chunk but the last hands on.
 template <int N, typename InT, int DISC, bool ODD>
 __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4))) k_packed_summary(const PackedParams p) {
@@ -159,6 +228,7 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
   const int64_t d = dbase + lo_ch;
   ChanConst<N, DISC> cc;
   load_chan<N, DISC>(cc, p.A + d * N, p.exact_thr);
+  const float limit = p.exact_thr * kLog2e;
   float h[N];
   zero_n(h);
   if (fresh && p.h0) {
@@ -198,7 +268,7 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
     Bnext.load(nb);
     float Bv[N];
     Bcur.widen(Bv);
-    ssm_step_any<N, DISC, false, kScaled>(h, cc, Bv, Bv, xv, dv);
+    advance<N, DISC, kScaled, kGroup<N, InT>, false>(h, cc, Bv, xv, dv, limit);
     Brow = nb;
   };
   float xc[kU], dc[kU];
@@ -242,7 +312,7 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
     if (dtm != kDtRaw) dv = dt_transform(dv, dtb, dtm);
     float Bv[N];
     Bb0.widen(Bv);
-    ssm_step_any<N, DISC, false, kScaled>(h, cc, Bv, Bv, xv, dv);
+    advance<N, DISC, kScaled, kGroup<N, InT>, false>(h, cc, Bv, xv, dv, limit);
     sum_add(dv);
     Brow += t + 1 < steps ? p.bs : 0u;
     Bb0.load(Brow);
@@ -333,6 +403,7 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
   const int64_t d = dbase + lo_ch, DN = p.D * N;
   ChanConst<N, DISC> cc;
   load_chan<N, DISC>(cc, p.A + d * N, p.exact_thr);
+  const float limit = p.exact_thr * kLog2e;
   float h[N];
   zero_n(h);
 
@@ -414,7 +485,7 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
       Bnext.load(nb);
       float Bv[N], Cv[N];
       Bcur.widen(Bv);
-      ssm_step_any<N, DISC, false>(h, cc, Bv, Bv, xv, dv);
+      advance<N, DISC, false, kGroup<N, InT>, false>(h, cc, Bv, xv, dv, limit);
       Ccur.widen(Cv);
       float even = 0.0f, odd = 0.0f;
 #pragma unroll
