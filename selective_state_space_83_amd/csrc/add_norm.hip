@@ -23,7 +23,9 @@ ssm_status_t check_sizes(int64_t rows, int64_t channels, std::initializer_list<i
   if (rows < 0 || channels < 0)
     return fail(SSM_ERR_SHAPE, "negative size: rows=%lld channels=%lld", (long long)rows, (long long)channels);
   if (!mul_ok(rows, channels, &n) || n > INT64_MAX / 16) return fail(SSM_ERR_SHAPE, "sizes overflow");
-  if (rows > kMaxGrid || channels > kMaxGrid) return fail(SSM_ERR_SHAPE, "problem too large for one launch");
+  // a launch holds at most 2^32 - 1 lanes, 256 of them to a row at most
+  if (rows > int64_t(UINT32_MAX) / 256 || channels > (int64_t(1) << 27))
+    return fail(SSM_ERR_SHAPE, "problem too large for one launch");
   for (int64_t s : strides)
     if (s < 0 || !mul_ok(rows, s, &n) || n > INT64_MAX / 16)
       return fail(SSM_ERR_SHAPE, "a row stride is negative or overflows");

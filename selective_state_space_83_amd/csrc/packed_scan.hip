@@ -239,14 +239,18 @@ int dt_mode_of(const float* bias, int32_t softplus) { return softplus ? kDtSoftp
 // bf16 rows that do not all start on 4 bytes
 bool odd_rows(const void* p, uint32_t stride) { return misaligned(p, 4) || stride % 2 != 0; }
 
-ssm_status_t grid_ok(int64_t n) {
-  return n > kMaxGrid / 1024 ? fail(SSM_ERR_SHAPE, "problem too large for one launch") : SSM_OK;
+// a launch holds at most 2^32 - 1 lanes
+ssm_status_t grid_ok(int64_t workgroups, int64_t lanes) {
+  return workgroups > int64_t(UINT32_MAX) / lanes || workgroups > kMaxGrid
+             ? fail(SSM_ERR_SHAPE, "problem too large for one launch")
+             : SSM_OK;
 }
 
 template <int N, typename InT, int DISC, bool ODD>
 ssm_status_t run_chunks(PackedParams p, hipStream_t s) {
   const int64_t out = int64_t(p.nc) * p.dtiles;
-  if (ssm_status_t st = grid_ok(out)) return st;
+  if (ssm_status_t st = grid_ok(out, kWave)) return st;
+  if (ssm_status_t st = grid_ok((p.D * N + kWave - 1) / kWave, kWave * kCarryWaves)) return st;
   if (p.nc > 1) {
     p.nwg = (p.nc - 1) * p.dtiles;
     hipLaunchKernelGGL((k_packed_summary<N, InT, DISC, ODD>), dim3(uint32_t(p.nwg)), dim3(kWave), 0, s, p);
@@ -283,7 +287,7 @@ ssm_status_t run_step(PackedStepParams p, hipStream_t s) {
   using L = StepLayout<N>;
   p.dtiles = int32_t((p.D + L::CPW - 1) / L::CPW);
   const int64_t n = (p.Bt + L::ROWS - 1) / L::ROWS * ((p.dtiles + L::WPG - 1) / L::WPG);
-  if (ssm_status_t st = grid_ok(n)) return st;
+  if (ssm_status_t st = grid_ok(n, kWave * L::WPG)) return st;
   p.nwg = int32_t(n);
   hipLaunchKernelGGL((k_packed_step<N, InT, DISC>), dim3(uint32_t(n)), dim3(kWave * L::WPG), 0, s, p);
   return launch_status("k_packed_step");
@@ -395,7 +399,9 @@ ssm_status_t check_bwd(const ssm_packed_scan_bwd_args_t* a) {
 template <int N, typename InT, int DISC>
 ssm_status_t run_bwd(PackedBwdParams p, hipStream_t s) {
   const int64_t DN = p.D * N;
-  if (ssm_status_t st = grid_ok(int64_t(p.nc) * p.dtiles)) return st;
+  if (ssm_status_t st = grid_ok(int64_t(p.nc) * p.dtiles, kWave * BwdLayout<N>::NG)) return st;
+  if (ssm_status_t st = grid_ok((int64_t(p.q.tokens) * 2 * N + 255) / 256, 256)) return st;
+  if (ssm_status_t st = grid_ok((DN + p.D + kWave - 1) / kWave, kWave * std::max<int>(kCarryWaves, kRedWaves))) return st;
   if (p.nc > 1) {
     p.nwg = (p.nc - 1) * p.dtiles;
     bool odd = false;

@@ -142,7 +142,9 @@ __device__ __forceinline__ bool any_slow(float z2, float limit) {
 // form is chosen for every GROUP states on their own: with A[n] about -(n + 1) and
 // steps down to 1e-3, two of three steps are slow for the first state and none for
 // the others (16384 x 1536 x 16 fp32: 88 us for the summaries with one choice for all
-// 16 states, %SUM% so; the output pass 127, %OUT% so).  SCALED carries A h (see
+// 16 states, 80 so; the output pass 127, 121 so).  GROUP = N makes one choice: for
+// bf16, whose limit is an eighth and seldom met, the choices' code costs more than they
+// save (16384 x 2560 x 16: 305 us a call, 316 by fours).  SCALED carries A h (see
 // ssm_step_lane), SELECT is exp_residual's.
 template <int N, int DISC, bool SCALED, int GROUP, bool SELECT>
 __device__ __forceinline__ void advance(float (&h)[N], const ChanConst<N, DISC>& cc, const float (&Bv)[N], float u,
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
 // per (channel, state); the 16 waves of a workgroup share the chunks of its 64.  Each
 // folds its share from zero, takes the state that enters it from the shares
 // before (in LDS), and walks it again.  A chunk's fold is 25 instructions, so one wave
-// walking 512 chunks alone takes 50 us, which nothing else overlaps.
+// walking 512 chunks alone took 50 us, which nothing else overlaps; 16 share them in 20.
 constexpr int kCarryWaves = 16;
 
 template <int N, bool REV>
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
     // B's next row and C's own are requested once this step's B has been waited for
     // (scalar loads come back in any order, so a wait is for all of them): the states'
     // update covers both.  (C a step ahead too takes 16 registers more, which spilled:
-    // 16384 x 1536 x 16 fp32 %OLD% us, this %NEW%.)
+    // 16384 x 1536 x 16 fp32: the pass took 150 us so, then 127.)
     auto one_step = [&](float xv, float dv, float zv, uint32_t ahead, const R& Bcur, R& Bnext) {
       const InT* nb = Brow + ahead;
       const InT* nc = Crow;
@@ -588,7 +590,7 @@ __device__ __forceinline__ void seq_combine(float (&a)[N], float (&r)[N], float 
 // k_scan_wave): a workgroup to a channel, a wave to four of its states, 64 tokens at a
 // time, their pairs (Abar, Bbar u) scanned over the lanes.  A block in which sequences begin takes the scan that stops
 // at them (its pairs are chosen, not multiplied by 0, which a NaN would pass).  Bound by
-// latency: 128 x 32 x 16 fp32 in three launches %OLD% us a call, so %NEW%.
+// latency: 128 x 32 x 16 fp32 in three launches 19.5 us a call, so 12.
 template <int N, typename InT, int DISC, bool GATE>
 __global__ void __launch_bounds__(kWave * BwdLayout<N>::NG) k_packed_wave(const PackedParams p) {
   constexpr int NS = BwdLayout<N>::NS, NG = BwdLayout<N>::NG;

@@ -14,7 +14,8 @@ namespace {
 using namespace ssmh;
 using namespace ssmc;
 
-constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 64;   // tokens are counted in 32 bits
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 4096;   // tokens are counted in 32 bits
+constexpr int64_t kMaxChannels = int64_t(1) << 24;
 
 Range rows_of(const void* p, int64_t rows, int64_t channels, int64_t stride, size_t es) {
   if (!p || rows == 0) return Range{nullptr, 0};
@@ -28,8 +29,8 @@ ssm_status_t check_common(const Args* a, int64_t rows, int64_t seqs, int64_t slo
   if (rows < 0 || seqs < 0 || slots < 0 || a->channels < 0)
     return fail(SSM_ERR_SHAPE, "negative size: tokens=%lld sequences=%lld slots=%lld channels=%lld", (long long)rows,
                 (long long)seqs, (long long)slots, (long long)a->channels);
-  if (rows > kMaxTokens || seqs > kMaxTokens || slots > kMaxTokens || a->channels > kMaxTokens)
-    return fail(SSM_ERR_SHAPE, "problem too large (tokens, sequences, slots and channels are counted in 32 bits)");
+  if (rows > kMaxTokens || seqs > kMaxTokens || slots > kMaxTokens || a->channels > kMaxChannels)
+    return fail(SSM_ERR_SHAPE, "problem too large (tokens, sequences and slots are counted in 32 bits, channels in 24)");
   if (!mul_ok(std::max(rows, slots), std::max<int64_t>(a->channels, 1), &n) || n > INT64_MAX / 64 || a->x_stride < 0 ||
       !mul_ok(rows, a->x_stride, &n) || n > INT64_MAX / 16)
     return fail(SSM_ERR_SHAPE, "sizes overflow, or x_stride is negative");
@@ -94,7 +95,7 @@ ssm_status_t check_step(const ssm_short_conv_step_args_t* a) {
 }
 
 // A lane's channels.  (8 bf16 channels, 16 bytes, take twice the registers: 32768 x 2560
-// 70 us for 64, the gradients of 16384 x 2560 75 us for 60.)
+// 70 us for 64.)
 constexpr int V = 4;
 
 // Rows that all start on V elements.
@@ -280,7 +281,7 @@ ssm_status_t ssm_short_conv_step(const ssm_short_conv_step_args_t* a, void* hip_
 
 size_t ssm_short_conv_bwd_workspace_size(const ssm_short_conv_bwd_args_t* a) {
   if (!a) return 0;
-  if (a->tokens < 0 || a->channels < 0 || a->tokens > kMaxTokens || a->channels > kMaxTokens || a->taps < 1 || a->taps > 4)
+  if (a->tokens < 0 || a->channels < 0 || a->tokens > kMaxTokens || a->channels > kMaxChannels || a->taps < 1 || a->taps > 4)
     return 0;
   int64_t n;
   return mul_ok(a->tokens, a->channels, &n) && n <= INT64_MAX / 64 ? bwd_workspace(a) : 0;
