@@ -325,6 +325,7 @@ ssm_status_t ssm_add_norm_bwd(const ssm_add_norm_bwd_args_t* a, void* hip_stream
     p.eps = a->eps;
     const int64_t v = wide_of(a->dtype, a->sum_dtype);
     const size_t es = dtype_size(a->dtype), ss = dtype_size(a->sum_dtype);
+    p.stream = a->rows * a->channels * int64_t(es + (a->dresidual ? ss : 0)) > kL2Bytes;
     const bool vec = a->channels % v == 0 && row_wide(a->sum, p.ss, v, ss) && row_wide(a->dy, p.ds, v, es) &&
                      row_wide(a->dsum, p.gs, v, ss) && !misaligned(a->weight, 16) && !misaligned(a->dx, size_t(v) * es) &&
                      !misaligned(a->dresidual, size_t(v) * ss);

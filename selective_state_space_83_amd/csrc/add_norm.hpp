@@ -48,6 +48,7 @@ struct AddNormBwdParams {
   int64_t rows, C;
   int64_t ss, ds, gs;    // row strides of sum, dy and dsum
   int64_t per;           // rows of a block: a lane walks them with its channels' weights in registers
+  int32_t stream;        // as AddNormParams'
   float eps;
 };
 
@@ -99,17 +100,18 @@ template <typename T, int V>
 struct Raw {
   static constexpr int W = V * int(sizeof(T)) / 4 > 0 ? V * int(sizeof(T)) / 4 : 1;
   uint32_t w[W];
+  // KEEP: in the caches, for rows that another tile reads too; else past them
+  template <bool KEEP = false>
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (V == 1) {
       w[0] = __builtin_bit_cast(uint32_t, ld(p));
     } else {
-      // not kept in the caches, where it would take the place of what is written
-      // (the convolution of 32768 x 2560 bf16 rows: 83 -> 73 us)
       constexpr int L = W < 4 ? W : 4;
       typedef uint32_t words __attribute__((ext_vector_type(L)));
 #pragma unroll
       for (int i = 0; i < W; i += L) {
-        const words u = __builtin_nontemporal_load(reinterpret_cast<const words*>(p) + i / L);
+        const words* q = reinterpret_cast<const words*>(p) + i / L;
+        const words u = KEEP ? *q : __builtin_nontemporal_load(q);
 #pragma unroll
         for (int k = 0; k < L; ++k) w[i + k] = u[k];
       }
@@ -176,10 +178,14 @@ __device__ __forceinline__ void store_v(fp8_t* p, const float* v) {
       const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
       u[i] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], lo, true));
     }
-    if constexpr (V == 8)
-      *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    typedef uint32_t words __attribute__((ext_vector_type(V / 4)));
+    words q;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) q[i] = u[i];
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(q, reinterpret_cast<words*>(p));
     else
-      *reinterpret_cast<uint32_t*>(p) = u[0];
+      *reinterpret_cast<words*>(p) = q;
   }
 }
 
@@ -260,8 +266,9 @@ struct RawRow {
 // Forward: TG lanes to a row, 256 / TG rows to a workgroup.  Bound by memory; rows
 // enough are on their way in the waves a SIMD holds.  (A lane that walks 8 rows, the
 // weights in registers and the next row requested ahead: 32768 x 2560 bf16 131 us
-// for 120, to 8 bits with an fp32 residual 190 for 175.  Stores past the caches then
-// 118 -> 111 and 161 -> 145; outputs that the L2 caches hold are left there.)
+// for 120, to 8 bits with an fp32 residual 190 for 175.  Loads past the caches 116 ->
+// 109 and 159 -> 147, outputs 118 -> 111 and 161 -> 147; those that the L2 caches hold
+// are left there.)
 template <typename InT, typename ResT, typename OutT, int V, int TG, int R>
 __global__ __launch_bounds__(256) void k_add_norm(AddNormParams p) {
   constexpr bool kQuant = sizeof(OutT) == 1;
@@ -416,7 +423,9 @@ __global__ __launch_bounds__(256) void k_add_norm_long(AddNormParams p) {
 }
 
 // Backward: TG lanes walk the p.per rows of a block: ds of every row, and the sums
-// over the block's rows for the weight's gradient.
+// over the block's rows for the weight's gradient.  (16384 x 1536 bf16 beside an fp32 sum,
+// with the forward pass: loads past the caches 134 -> 125 us, stores of large outputs
+// 131 -> 125.)
 template <typename InT, typename SumT, int V, int TG, int R>
 __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
   __shared__ float part[8];
@@ -474,9 +483,17 @@ __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
       dw[i] += d[i] * n;
       g[i] += r * (d[i] * w[i] - n * m);
     }
-    store_row<V, R, TG>(static_cast<InT*>(p.dx) + row * p.C, g, lane, C);
-    if constexpr (sizeof(SumT) != sizeof(InT))
-      if (p.dres) store_row<V, R, TG>(static_cast<SumT*>(p.dres) + row * p.C, g, lane, C);
+    InT* dx = static_cast<InT*>(p.dx) + row * p.C;
+    SumT* dres = static_cast<SumT*>(p.dres) + row * p.C;
+    if (p.stream) {
+      store_row<V, R, TG, true>(dx, g, lane, C);
+      if constexpr (sizeof(SumT) != sizeof(InT))
+        if (p.dres) store_row<V, R, TG, true>(dres, g, lane, C);
+    } else {
+      store_row<V, R, TG>(dx, g, lane, C);
+      if constexpr (sizeof(SumT) != sizeof(InT))
+        if (p.dres) store_row<V, R, TG>(dres, g, lane, C);
+    }
   }
   if (p.dw) store_row<V, R, TG>(p.dw + block * p.C, dw, lane, C);
 }

@@ -95,14 +95,17 @@ ssm_status_t check_step(const ssm_short_conv_step_args_t* a) {
 }
 
 // A lane's channels.  (8 bf16 channels, 16 bytes, take twice the registers: 32768 x 2560
-// 70 us for 64.)
+// 84 us for 78.)
 constexpr int V = 4;
 
 // Rows that all start on V elements.
 bool row_wide(const void* p, int64_t stride, size_t es) { return !misaligned(p, V * es) && stride % V == 0; }
 
 // Tokens per tile: short enough that the tiles fill the GPU with `waves` waves, at
-// least 8 (a tile reads up to three rows more than its own).
+// least 8 (a tile reads up to three rows more than its own).  The forward pass takes 16 at
+// most (32768 x 2560 bf16 77 us, 78 with 32, 79 with 64; fp32 141, 142, 147; 4000 x 1027
+// bf16, an element at a time, 14, 19, 19), the gradients 64 (16384 x 2560 bf16 after a
+// forward pass 117 us, 126 with 32).
 int32_t tile_len(int64_t tokens, int64_t cgroups, int64_t waves, int64_t most) {
   int64_t t = most;
   while (t > 8 && (tokens + t - 1) / t * cgroups < waves) t /= 2;
@@ -134,7 +137,7 @@ ssm_status_t set_tiles(ConvParams* p, int64_t v, int32_t tile, uint32_t* grid) {
 template <typename T, int W, int K>
 ssm_status_t launch_fwd(ConvParams p, hipStream_t s) {
   uint32_t grid;
-  if (ssm_status_t st = set_tiles(&p, W, tile_len(p.q.tokens, channel_groups(p.C, W), 2048, 64), &grid)) return st;
+  if (ssm_status_t st = set_tiles(&p, W, tile_len(p.q.tokens, channel_groups(p.C, W), 2048, 16), &grid)) return st;
   hipLaunchKernelGGL((k_short_conv<T, W, K>), dim3(grid), dim3(256), 0, s, p);
   return launch_status("k_short_conv");
 }

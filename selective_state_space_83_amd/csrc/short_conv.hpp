@@ -11,7 +11,9 @@
 // A lane holds V neighbouring channels (4, or one where rows do not start on 4) and walks a tile of tokens with the last three inputs in
 // registers; a wave covers 64 V channels, and the waves of a workgroup lie side by
 // side on the same tokens.  Bound by memory: a tile reads K - 1 rows more than its
-// own.
+// own, which the caches hold.  Loads and stores go through the caches: loads past them
+// gain 1% in a forward pass and lose 9% where the gradients follow it (16384 x 1536
+// fp32 114 -> 124 us); stores past them change nothing.
 #pragma once
 
 #include "add_norm.hpp"
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(256) void k_short_conv(ConvParams p) {
   auto rows = [&](Raw<T, V> (&v)[kAhead], int32_t t) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
-      if (live && t + j < to) v[j].load(x + int64_t(t + j) * p.xs);
+      if (live && t + j < to) v[j].template load<true>(x + int64_t(t + j) * p.xs);
   };
   if (from < to) rows(cur, from);
   for (int32_t t = from; t < to; t += kAhead) {
@@ -363,8 +365,8 @@ __global__ __launch_bounds__(256) void k_short_conv_bwd(ConvParams p) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
       if (live && t + j < to) {
-        u[j].load(x + int64_t(t + j) * p.xs);
-        v[j].load(dy + int64_t(t + j) * p.ds);
+        u[j].template load<true>(x + int64_t(t + j) * p.xs);
+        v[j].template load<true>(dy + int64_t(t + j) * p.ds);
       }
   };
   rows(cx, cd, from);
