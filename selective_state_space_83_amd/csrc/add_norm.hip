@@ -23,9 +23,7 @@ ssm_status_t check_sizes(int64_t rows, int64_t channels, std::initializer_list<i
   if (rows < 0 || channels < 0)
     return fail(SSM_ERR_SHAPE, "negative size: rows=%lld channels=%lld", (long long)rows, (long long)channels);
   if (!mul_ok(rows, channels, &n) || n > INT64_MAX / 16) return fail(SSM_ERR_SHAPE, "sizes overflow");
-  // a launch holds at most 2^32 - 1 lanes, 256 of them to a row at most
-  if (rows > int64_t(UINT32_MAX) / 256 || channels > (int64_t(1) << 27))
-    return fail(SSM_ERR_SHAPE, "problem too large for one launch");
+  if (rows > kMaxGrid || channels > (int64_t(1) << 27)) return fail(SSM_ERR_SHAPE, "problem too large for one launch");
   for (int64_t s : strides)
     if (s < 0 || !mul_ok(rows, s, &n) || n > INT64_MAX / 16)
       return fail(SSM_ERR_SHAPE, "a row stride is negative or overflows");
@@ -124,6 +122,11 @@ void deal_rows(Deal* d, int64_t rows) {
   const int64_t lanes = rows * (d->TG ? d->TG : 256);
   d->per = std::max<int64_t>(1, std::min<int64_t>(64, lanes >> 17));
   d->blocks = (rows + d->per - 1) / d->per;
+}
+
+// A launch holds at most 2^32 - 1 lanes; n: groups of them.
+ssm_status_t lanes_ok(const Deal& d, int64_t n) {
+  return n > (int64_t(UINT32_MAX) - 255) / (d.TG ? d.TG : 256) ? fail(SSM_ERR_SHAPE, "problem too large for one launch") : SSM_OK;
 }
 
 // Workgroups for n groups of TG lanes.
@@ -288,6 +291,7 @@ ssm_status_t ssm_add_norm_fwd(const ssm_add_norm_args_t* a, void* hip_stream) {
   Deal d = deal_row(a->channels, vec, v, false);
   // blocks are formed within a wave's turn, side by side
   if (p.nblk > 1 && !(vec && d.TG * v >= p.block)) d.TG = d.R = 0;
+  if (ssm_status_t st = lanes_ok(d, p.rows)) return st;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   if (a->dtype == SSM_F32)
     return quant ? run_fwd<float, float, fp8_t>(p, d, s) : run_fwd<float, float, float>(p, d, s);
@@ -331,7 +335,8 @@ ssm_status_t ssm_add_norm_bwd(const ssm_add_norm_bwd_args_t* a, void* hip_stream
                      !misaligned(a->dresidual, size_t(v) * ss);
     const Deal d = bwd_deal(a, vec);
     blocks = d.blocks;
-    ssm_status_t st;
+    ssm_status_t st = lanes_ok(d, blocks);
+    if (st) return st;
     if (a->dtype == SSM_F32)
       st = run_bwd<float, float>(p, d, s);
     else if (a->sum_dtype == SSM_F32)
