@@ -250,9 +250,14 @@ __global__ void __launch_bounds__(kWave * kCarryWaves) k_packed_bwd_carry(const 
 
 // Main pass; lanes, waves and LDS as in k_bwd_main.  What only some of the steps need is
 // read again from the arguments (args_again) every 16 tokens: kept in scalar registers,
-// it spilled 276 of them (16384 x 1536 x 16 fp32: 632 us, then 503).
+// it spilled 276 of them (16384 x 1536 x 16 fp32: 632 us, then 503).  16 tokens of one
+// sequence take a copy of the steps without the questions for its ends, whose steps
+// overlap; for its registers a SIMD holds three waves rather than four (forward and
+// gradients, fp32 798 -> 776 us, bf16 794 -> 711, ZOH bf16 982 -> 897; with four waves
+// it spills, 910 and 807; sequences of four tokens 1333 -> 1477; one state, which has
+// little to overlap, 305 -> 323 and so keeps the one copy and four waves).
 template <int N, typename InT, int DISC>
-__global__ void __launch_bounds__(kWave * BwdLayout<N>::NG) __attribute__((amdgpu_waves_per_eu(4)))
+__global__ void __launch_bounds__(kWave * BwdLayout<N>::NG) __attribute__((amdgpu_waves_per_eu(N > 1 ? 3 : 4)))
 k_packed_bwd(const PackedBwdParams p) {
   constexpr int NS = BwdLayout<N>::NS, NG = BwdLayout<N>::NG;
   constexpr int F = kBwdFine, K = kBwdBlock, H = kBwdHalf;
@@ -402,9 +407,8 @@ k_packed_bwd(const PackedBwdParams p) {
     // The later half first: from the state kept, through the earlier half, its own steps
     // forwards with the states between them in registers, and back.  (A rolled loop:
     // both halves' steps unrolled are 56 KB of instructions.)
-#pragma unroll 1
-    for (int j0 = F - H; j0 >= 0; j0 -= H) {
-      if (j0 >= len) continue;   // wave-uniform
+    auto half = [&](auto events, int j0) {
+      constexpr bool kEvents = decltype(events)::value;
       const uint32_t live_h = live >> j0, begins_h = begins >> j0;
       const float* Brow = &rows[rb][0][j0][n0];
       const float* Crow = &rows[rb][1][j0][n0];
@@ -414,7 +418,7 @@ k_packed_bwd(const PackedBwdParams p) {
       auto forward = [&](float xv, float dv, const float* row) {
         float Bv[NS];
         lds_row<NS>(Bv, row);
-        advance<NS, DISC, false, 1, true>(h, cc, Bv, xv, dv, limit);
+        advance<NS, DISC, false, NS, true>(h, cc, Bv, xv, dv, limit);
       };
       float xa[K], da[K];
       auto rows_of = [&](float (&u)[K], float (&v)[K], int j) {
@@ -431,8 +435,8 @@ k_packed_bwd(const PackedBwdParams p) {
         rows_of(xn, dn_, jb + K);
 #pragma unroll
         for (int jj = 0; jj < K; ++jj) {
-          if (begins >> (jb + jj) & 1) initial(h, jb + jj);
-          if (live >> (jb + jj) & 1) forward(xa[jj], da[jj], &rows[rb][0][jb + jj][n0]);
+          if (kEvents && (begins >> (jb + jj) & 1)) initial(h, jb + jj);
+          if (!kEvents || (live >> (jb + jj) & 1)) forward(xa[jj], da[jj], &rows[rb][0][jb + jj][n0]);
         }
 #pragma unroll
         for (int jj = 0; jj < K; ++jj) {
@@ -451,8 +455,8 @@ k_packed_bwd(const PackedBwdParams p) {
           const int js = jb + jj;
 #pragma unroll
           for (int n = 0; n < NS; ++n) stash[js][n] = h[n];
-          if (begins_h >> js & 1) initial(h, j0 + js);
-          if (live_h >> js & 1) forward(xa[jj], da[jj], Brow + js * N);
+          if (kEvents && (begins_h >> js & 1)) initial(h, j0 + js);
+          if (!kEvents || (live_h >> js & 1)) forward(xa[jj], da[jj], Brow + js * N);
         }
         if (jb + K < H) {
 #pragma unroll
@@ -464,7 +468,7 @@ k_packed_bwd(const PackedBwdParams p) {
       }
 #pragma unroll
       for (int jb = H - K; jb >= 0; jb -= K) {
-        if (j0 + jb >= len) continue;   // wave-uniform
+        if (kEvents && j0 + jb >= len) continue;   // wave-uniform
         float ub[K], db[K], yb[K];
 #pragma unroll
         for (int jj = 0; jj < K; ++jj) {
@@ -479,7 +483,7 @@ k_packed_bwd(const PackedBwdParams p) {
           float pB[NS], pC[NS], du = 0.0f, ddt = 0.0f;
           zero_n(pB);
           zero_n(pC);
-          if (live_h >> js & 1) {
+          if (!kEvents || (live_h >> js & 1)) {
             const float u = ub[jj], dv = db[jj], dyv = yb[jj];
             float Bv[NS], Cv[NS];
             lds_row<NS>(Bv, Brow + js * N);
@@ -490,14 +494,14 @@ k_packed_bwd(const PackedBwdParams p) {
               hp[n] = stash[js][n];
               hn[n] = (js + 1 < H) ? stash[js + 1 < H ? js + 1 : js][n] : h[n];
             }
-            if (begins_h >> js & 1) initial(hp, j0 + js);
+            if (kEvents && (begins_h >> js & 1)) initial(hp, j0 + js);
             const bool series = DISC == kZoh && __builtin_amdgcn_ballot_w64(dv < zoh_thr) != 0;
             if (series)
               retreat<NS, DISC, true, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, limit, pB, pC, du, ddt);
             else
               retreat<NS, DISC, false, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, limit, pB, pC, du, ddt);
             dDacc = fmaf(dyv, u, dDacc);
-            if (begins_h >> js & 1) {
+            if (kEvents && (begins_h >> js & 1)) {
               const PackedBwdParams& b = args_again<PackedBwdParams>();
               const int32_t s = __builtin_amdgcn_readfirstlane(ids[w][0][j0 + js]);
               const int32_t before = __builtin_amdgcn_readfirstlane(ids[w][1][j0 + js]);
@@ -548,20 +552,28 @@ k_packed_bwd(const PackedBwdParams p) {
 #pragma unroll
         for (int jj = w; jj < K; jj += NG) {
           const int j = j0 + jb + jj;
-          if (j < len) {
+          if (!kEvents || j < len) {
             float su = 0.0f, sd = 0.0f;
 #pragma unroll
             for (int v = 0; v < NG; ++v) {
               su += xch[xb][0][v][jj][lane];
               sd += xch[xb][1][v][jj][lane];
             }
-            if (live >> j & 1) su = fmaf(dsk, ldb(wy.r, lane_in, uint32_t(j) * wy.row, kIn), su);
+            if (!kEvents || (live >> j & 1)) su = fmaf(dsk, ldb(wy.r, lane_in, uint32_t(j) * wy.row, kIn), su);
             stb(rdx, lane_f, uint32_t(j) * row_f, su, kF);
             stb(rdd, lane_f, uint32_t(j) * row_f, sd, kF);
           }
         }
         xb ^= 1;
       }
+    };
+    if (N > 1 && begins == 0 && live == (1u << F) - 1) {
+#pragma unroll 1
+      for (int j0 = F - H; j0 >= 0; j0 -= H) half(std::false_type{}, j0);
+    } else {
+#pragma unroll 1
+      for (int j0 = F - H; j0 >= 0; j0 -= H)
+        if (j0 < len) half(std::true_type{}, j0);   // wave-uniform
     }
     rb ^= 1;
   }

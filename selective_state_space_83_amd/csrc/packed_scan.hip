@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "ssm_scan.h"
@@ -47,6 +48,12 @@ int64_t widest_stride(const Args* a) {
   return std::max(a->x_stride, a->delta_stride);
 }
 
+// The chunk length below which the carries cost more than the walks gain: a token of a
+// chunk takes about 0.55 us in the two walks, a chunk 0.026 us + 0.05 ns a channel in
+// the carries' walk and their traffic.  (bf16, 16 states, without it: 16384 x 100 50 us
+// for 76, 16384 x 256 62 for 71, 65536 x 64 86 for 131, 1024 x 1536 37 for 44.)
+int64_t chunk_floor(int64_t tokens, int64_t D) { return int64_t(std::sqrt(double(tokens) * double(D + 520) / 11000)); }
+
 // Sizes assumed validated.
 Plan make_plan(int64_t tokens, int64_t D, int64_t N, int64_t chunk_len, int64_t stride, bool kept) {
   Plan pl;
@@ -63,6 +70,7 @@ Plan make_plan(int64_t tokens, int64_t D, int64_t N, int64_t chunk_len, int64_t 
     if (nc > 1 && (tokens + nc - 1) / nc < kShortChunk) nc = chunks(kShortTargetWaves);
     if (tokens <= kNoSplitTokens) nc = 1;
     T = ((tokens + nc - 1) / nc + 3) / 4 * 4;
+    T = std::max(T, (chunk_floor(tokens, D) + 3) / 4 * 4);
     if (nc >= kBalanceChunks) T = std::min(T, kLongChunk);
   }
   // rows of 4 bytes an element at most; 4 tokens fit (check_sizes)
@@ -312,7 +320,10 @@ BwdPlan bwd_plan(const ssm_packed_scan_bwd_args_t* a) {
     pl.T = std::min<int64_t>(a->super_chunk, fine * kBwdFine);
   } else {
     const int64_t nc = std::max<int64_t>(1, std::min(kTargetWaves / pl.dtiles, fine));
-    pl.T = std::min((fine + nc - 1) / nc * kBwdFine, kBwdLong);
+    // (see chunk_floor; a token takes 0.83 us here, a chunk 0.06 us + 0.1 ns a channel:
+    // 16384 x 100 fp32 89 us for 122)
+    const int64_t least = int64_t(std::sqrt(double(tokens) * double(a->dim + 600) / 8300)) + kBwdFine / 2;
+    pl.T = std::min(std::max((fine + nc - 1) / nc, least / kBwdFine) * kBwdFine, kBwdLong);
   }
   // the reverse summary's windows
   const int64_t stride = std::max({a->x_stride, a->delta_stride, a->dy_stride, a->dim});

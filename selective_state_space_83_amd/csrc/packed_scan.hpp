@@ -59,24 +59,28 @@ struct PackedParams {
 
 // A row of B or C in scalar registers, as it lies in memory; bf16 rows are widened
 // when their step comes, so that the row requested ahead takes half the registers
-// (the steps of 16 states have none to spare).  ODD: bf16 rows may start on an odd
-// element; they are read by elements, which waits for each row.
+// (the steps of 16 states have none to spare).  A bf16 row of one element is the word
+// that holds it, shifted as it is widened (16384 x 2560: 179 us, and 229 read by itself
+// through the vector unit).  ODD: longer bf16 rows that may start on an odd element are
+// read by elements, which waits for each row (words and shifts spill: 16384 x 2561 with
+// rows of 16 769 us, this 536).
 template <int N, typename InT, bool ODD>
 struct Row {
   static constexpr bool kWide = std::is_same<InT, float>::value;
   static constexpr int W = kWide || N == 1 ? N : N / 2;
   uint32_t w[W];
+  uint32_t shift;   // of a bf16 row of one element
   __device__ __forceinline__ void load(const InT* p) {
-    if constexpr (kWide) {
-      const_u32_ptr q = (const_u32_ptr)(p);
-#pragma unroll
-      for (int k = 0; k < W; ++k) w[k] = q[k];
-    } else if constexpr (N == 1 || ODD) {
+    if constexpr (!kWide && N == 1) {
+      const uint64_t at = reinterpret_cast<uint64_t>(p);
+      shift = uint32_t(at & 2) * 8;
+      w[0] = *(const_u32_ptr)(at & ~uint64_t(3));
+    } else if constexpr (!kWide && ODD) {
       uint32_t v[N];
 #pragma unroll
       for (int n = 0; n < N; ++n) v[n] = __builtin_amdgcn_readfirstlane(uint32_t(p[n]));
 #pragma unroll
-      for (int k = 0; k < W; ++k) w[k] = N == 1 ? v[0] : v[2 * k % N] | v[(2 * k + 1) % N] << 16;
+      for (int k = 0; k < W; ++k) w[k] = v[2 * k] | v[2 * k + 1] << 16;
     } else {
       const_u32_ptr q = (const_u32_ptr)(p);
 #pragma unroll
@@ -84,9 +88,13 @@ struct Row {
     }
   }
   __device__ __forceinline__ void widen(float (&r)[N]) const {
+    if constexpr (!kWide && N == 1) {
+      r[0] = __uint_as_float(w[0] >> shift << 16);
+    } else {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      r[n] = __uint_as_float(kWide ? w[n] : N == 1 || n % 2 == 0 ? w[n / 2] << 16 : w[n / 2] & 0xffff0000u);
+      for (int n = 0; n < N; ++n)
+        r[n] = __uint_as_float(kWide ? w[n] : n % 2 == 0 ? w[n / 2] << 16 : w[n / 2] & 0xffff0000u);
+    }
   }
 };
 
