@@ -1,8 +1,9 @@
 /*
  * ssm_scan.h -- C ABI of libssmscan.so, the selective state-space scan
  * (Mamba's S6 layer core) for AMD Instinct MI355X (gfx950), and beside it the
- * head-decay mixer: decay attention and the group norm that follows it (their
- * own conventions stand with them below).
+ * head-decay mixer: decay attention and the group norm that follows it; and what
+ * stands around the scan in a layer of packed sequences: the packed scan, the short
+ * convolution and the residual norm (their own conventions stand with them below).
  *
  * What is computed.  For every batch row b, channel d and state n the library
  * runs one diagonal single-input single-output state-space model:
