@@ -576,7 +576,7 @@ k_packed_bwd(const PackedBwdParams p) {
           }
           xb ^= 1;
         }
-        if constexpr (kAheadBack) {
+        if (kAheadBack && jb > 0) {
 #pragma unroll
           for (int jj = 0; jj < K; ++jj) {
             xa[jj] = un[jj];
