@@ -32,8 +32,8 @@ __device__ __forceinline__ int32_t seq_start(const Seqs& q, int32_t i) {
 // the offsets 64 at a time, so up to 64 sequences cost one load, 4096 two.
 __device__ __forceinline__ int32_t seqs_before(const Seqs& q, int32_t t) {
   if (!q.offsets) {
-    if (q.seqlen == 0) return t > 0 ? q.S : 0;
-    const int32_t n = (t + q.seqlen - 1) / q.seqlen;
+    if (t <= 0 || q.seqlen == 0) return t > 0 ? q.S : 0;
+    const int32_t n = int32_t((uint32_t(t) + uint32_t(q.seqlen) - 1) / uint32_t(q.seqlen));   // (past 31 bits)
     return n < q.S ? n : q.S;
   }
   const int32_t lane = threadIdx.x & 63;

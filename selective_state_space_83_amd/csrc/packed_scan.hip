@@ -34,7 +34,7 @@ constexpr int64_t kMaxWindow = (int64_t(1) << 31) - 1;
 // tokens three, to each of the 1024 SIMDs; chunks of at least kMinChunk tokens, and
 // of at most kLongChunk once there are kBalanceChunks of them; no cut for
 // kNoSplitTokens or fewer (the scan's plan, whose work a chunk's is).
-constexpr int64_t kTargetWaves = 4096, kShortTargetWaves = 3072;
+constexpr int64_t kTargetWaves = 4 * 1024, kShortTargetWaves = 3 * 1024;
 constexpr int64_t kShortChunk = 64, kMinChunk = 8, kBalanceChunks = 16, kLongChunk = 256, kNoSplitTokens = 32;
 
 struct Plan {

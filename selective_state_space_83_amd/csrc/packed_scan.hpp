@@ -151,8 +151,8 @@ __device__ __forceinline__ bool any_slow(float z2, float limit) {
 // steps down to 1e-3, two of three steps are slow for the first state and none for
 // the others (16384 x 1536 x 16 fp32: 88 us for the summaries with one choice for all
 // 16 states, 80 so; the output pass 127, 121 so).  GROUP = N makes one choice: for
-// bf16, whose limit is an eighth and seldom met, the choices' code costs more than they
-// save (16384 x 2560 x 16: 305 us a call, 316 by fours).  SCALED carries A h (see
+// bf16, whose limit is an eighth of fp32's and seldom met, the choices' code costs more
+// than they save (16384 x 2560 x 16: 305 us a call, 316 by fours).  SCALED carries A h (see
 // ssm_step_lane), SELECT is exp_residual's.
 template <int N, int DISC, bool SCALED, int GROUP, bool SELECT>
 __device__ __forceinline__ void advance(float (&h)[N], const ChanConst<N, DISC>& cc, const float (&Bv)[N], float u,
@@ -441,7 +441,10 @@ __global__ void __launch_bounds__(kWave) __attribute__((amdgpu_waves_per_eu(4)))
       const int32_t end = seq_start(a.q, s + 1), slot = seq_slot(a.q, s);
       const bool given = a.h0 && slot >= 0 && seq_resumed(a.q, s);
       zero_n(h);
-      if (given) load_n(h, (end > last && a.hstart ? a.hstart + int64_t(chunk) * a.D * N : a.h0 + int64_t(slot) * a.D * N) + d * N);
+      if (given) {
+        const float* from_state = end > last && a.hstart ? a.hstart + int64_t(chunk) * a.D * N : a.h0 + int64_t(slot) * a.D * N;
+        load_n(h, from_state + d * N);
+      }
       open = true;
       ++s;
       if (end <= t) finish(a);
@@ -596,9 +599,10 @@ __device__ __forceinline__ void seq_combine(float (&a)[N], float (&r)[N], float 
 
 // Few tokens of few channels in one launch, with time across the lanes (the scan's
 // k_scan_wave): a workgroup to a channel, a wave to four of its states, 64 tokens at a
-// time, their pairs (Abar, Bbar u) scanned over the lanes.  A block in which sequences begin takes the scan that stops
-// at them (its pairs are chosen, not multiplied by 0, which a NaN would pass).  Bound by
-// latency: 128 x 32 x 16 fp32 in three launches 19.5 us a call, so 12.
+// time, their pairs (Abar, Bbar u) scanned over the lanes.  A block in which sequences
+// begin takes the scan that stops at them (its pairs are chosen, not multiplied by 0,
+// which a NaN would pass).  Bound by latency: 128 x 32 x 16 fp32 in three launches
+// 19.5 us a call, so 12.
 template <int N, typename InT, int DISC, bool GATE>
 __global__ void __launch_bounds__(kWave * BwdLayout<N>::NG) k_packed_wave(const PackedParams p) {
   constexpr int NS = BwdLayout<N>::NS, NG = BwdLayout<N>::NG;

@@ -276,8 +276,8 @@ ssm_status_t ssm_short_conv_step(const ssm_short_conv_step_args_t* a, void* hip_
   p.state = a->state;
   p.y = a->y;
   const size_t es = dtype_size(a->dtype);
-  const bool vec = a->channels % V == 0 && row_wide(a->x, a->x_stride, es) && !misaligned(a->y, V * es) && !misaligned(a->weight, 16) && !misaligned(a->bias, 16) &&
-                   !misaligned(a->state, 16);
+  const bool vec = a->channels % V == 0 && row_wide(a->x, a->x_stride, es) && !misaligned(a->y, V * es) &&
+                   !misaligned(a->weight, 16) && !misaligned(a->bias, 16) && !misaligned(a->state, 16);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   return a->dtype == SSM_F32 ? run_step<float>(p, a->taps, vec, s) : run_step<bf16_t>(p, a->taps, vec, s);
 }

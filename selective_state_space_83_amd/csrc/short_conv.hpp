@@ -8,12 +8,12 @@
 //   da = dy act'(a),  dx[t] = sum_k w[k] da[t+K-1-k],  dw[k] = sum_t da[t] x[t-K+1+k],
 // silu'(a) = s (1 + a (1 - s)), s = 1 / (1 + exp(-a)).
 //
-// A lane holds V neighbouring channels (4, or one where rows do not start on 4) and walks a tile of tokens with the last three inputs in
-// registers; a wave covers 64 V channels, and the waves of a workgroup lie side by
-// side on the same tokens.  Bound by memory: a tile reads K - 1 rows more than its
-// own, which the caches hold.  Loads and stores go through the caches: loads past them
-// gain 1% in a forward pass and lose 9% where the gradients follow it (16384 x 1536
-// fp32 114 -> 124 us); stores past them change nothing.
+// A lane holds V neighbouring channels (4, or one where rows do not start on 4) and walks
+// a tile of tokens with the last three inputs in registers; a wave covers 64 V channels,
+// and the waves of a workgroup lie side by side on the same tokens.  Bound by memory: a
+// tile reads K - 1 rows more than its own, which the caches hold.  Loads and stores go
+// through the caches: loads past them gain 1% in a forward pass and lose 9% where the
+// gradients follow it (16384 x 1536 fp32 114 -> 124 us); stores past them change nothing.
 #pragma once
 
 #include "add_norm.hpp"
