@@ -189,12 +189,38 @@ __device__ __forceinline__ void store_v(fp8_t* p, const float* v) {
   }
 }
 
-// The scale of a block whose largest magnitude is top, and its reciprocal.
-__device__ __forceinline__ float scale_of(float top, float* inverse) {
-  const float s = top > 0.0f ? fmaxf(top / kE4m3Max, 0x1p-126f) : 1.0f;
-  *inverse = 1.0f / s;
-  return s;
-}
+// To 8 bits: y is p m with p = (s 2^e) w and r = 2^e m, so that a value in units of its
+// block's scale, p (448 / max|p|), does not depend on the rounding of r.  The product's
+// rest and the quotient's go along, and q is rounded but once before its 8 bits: few
+// values lie on the other side of a step than the exact ones.  (Rounded at each of the
+// five operations: 2 of 655360 values; 32768 x 2560 to 8 bits takes as long either way.)
+struct Unit {
+  float up, m;   // 2^e, and r without it
+  __device__ __forceinline__ explicit Unit(float r) {
+    const uint32_t b = __float_as_uint(r);
+    up = __uint_as_float(b & 0x7f800000u);
+    m = __uint_as_float((b & 0x007fffffu) | 0x3f800000u);
+  }
+};
+// The scale of a block whose largest |p| is top, and what takes p to q.
+struct Step {
+  float scale, c, rest;
+  __device__ __forceinline__ Step(float top, const Unit& u) {
+    const float y = top * u.m;
+    scale = y > 0.0f ? fmaxf(y / kE4m3Max, 0x1p-126f) : 1.0f;
+    rest = 0.0f;
+    if (scale == 0x1p-126f || !(y > 0.0f)) {   // at its least, or a block of zeros
+      c = u.m / scale;
+    } else {
+      c = kE4m3Max / top;
+      if (c > 0.0f) rest = fmaf(-c, top, kE4m3Max) * (c * (1.0f / kE4m3Max));
+    }
+  }
+  __device__ __forceinline__ float operator()(float s, float w) const {
+    const float p = s * w, low = fmaf(s, w, -p);
+    return to_range(fmaf(p, c, fmaf(p, rest, low * c)));
+  }
+};
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_max(float v) {
@@ -302,36 +328,39 @@ __global__ __launch_bounds__(256) void k_add_norm(AddNormParams p) {
   for (int i = 0; i < R * V; ++i) ss += x[i] * x[i];
   group_sum<TG>(ss, zero, part);
   const float r = 1.0f / sqrtf(ss * (1.0f / float(C)) + p.eps);
+  if constexpr (!kQuant) {
 #pragma unroll
-  for (int i = 0; i < R * V; ++i) x[i] = x[i] * r * w[i];
-  if constexpr (kQuant) {
+    for (int i = 0; i < R * V; ++i) x[i] = x[i] * r * w[i];
+  } else {
+    const Unit unit(r);
     float top[R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       top[k] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) top[k] = fmaxf(top[k], fabsf(x[k * V + i]));
+      for (int i = 0; i < V; ++i) {
+        x[k * V + i] *= unit.up;
+        top[k] = fmaxf(top[k], fabsf(x[k * V + i] * w[k * V + i]));
+      }
     }
     float* ps = p.scale + row * p.nblk;
     if (p.nblk == 1) {
 #pragma unroll
       for (int k = 1; k < R; ++k) top[0] = fmaxf(top[0], top[k]);
-      float inverse;
-      const float s = scale_of(row_max<TG>(top[0], part), &inverse);
-      if (lane == 0) *ps = s;
+      const Step q(row_max<TG>(top[0], part), unit);
+      if (lane == 0) *ps = q.scale;
 #pragma unroll
-      for (int i = 0; i < R * V; ++i) x[i] = to_range(x[i] * inverse);
+      for (int i = 0; i < R * V; ++i) x[i] = q(x[i], w[i]);
     } else {
       // a block is the same turn of block / V neighbouring lanes (the host sees to it)
       const int lanes = p.block / V;
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        float inverse;
-        const float s = scale_of(lanes_max(top[k], lanes), &inverse);
+        const Step q(lanes_max(top[k], lanes), unit);
         const int c = (k * TG + lane) * V;
-        if ((lane & (lanes - 1)) == 0 && c < C) ps[c / p.block] = s;
+        if ((lane & (lanes - 1)) == 0 && c < C) ps[c / p.block] = q.scale;
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[k * V + i] = to_range(x[k * V + i] * inverse);
+        for (int i = 0; i < V; ++i) x[k * V + i] = q(x[k * V + i], w[k * V + i]);
       }
     }
   }
@@ -373,51 +402,56 @@ __global__ __launch_bounds__(256) void k_add_norm_long(AddNormParams p) {
   const float r = 1.0f / sqrtf(ss * (1.0f / float(p.C)) + p.eps);
   ResT* sum = static_cast<ResT*>(p.sum) + row * p.C;
   OutT* y = static_cast<OutT*>(p.y) + row * p.C;
-  // s of V channels, and y of them
-  auto values = [&](float (&s)[V], float (&v)[V], int64_t c) {
+  // s of V channels, and their weights
+  auto values = [&](float (&s)[V], float (&w)[V], int64_t c) {
     load(s, c);
-    float w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) w[i] = 1.0f;
     if (p.w) load_v<V>(w, p.w + c);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = s[i] * r * w[i];
-  };
-  auto finish = [&](int64_t c, float inverse) {
-    float s[V], v[V];
-    values(s, v, c);
-    if constexpr (kQuant) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = to_range(v[i] * inverse);
-    }
-    if (p.sum) store_v<V>(sum + c, s);
-    store_v<V>(y + c, v);
-  };
-  auto largest = [&](float top, int64_t c) {
-    float s[V], v[V];
-    values(s, v, c);
-#pragma unroll
-    for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(v[i]));
-    return top;
   };
   if constexpr (!kQuant) {
-    for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) finish(c, 1.0f);
-  } else if (p.nblk == 1) {
-    float top = 0.0f, inverse;
-    for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) top = largest(top, c);
-    const float s = scale_of(row_max<256>(top, part), &inverse);
-    if (threadIdx.x == 0) p.scale[row] = s;
-    for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) finish(c, inverse);
+    for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) {
+      float s[V], w[V], v[V];
+      values(s, w, c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = s[i] * r * w[i];
+      if (p.sum) store_v<V>(sum + c, s);
+      store_v<V>(y + c, v);
+    }
   } else {
-    // a wave to a block of channels
-    const int lane = threadIdx.x & 63;
-    for (int64_t k = threadIdx.x >> 6; k < p.nblk; k += 4) {
-      const int64_t c0 = k * p.block, c1 = c0 + p.block < p.C ? c0 + p.block : p.C;
-      float top = 0.0f, inverse;
-      for (int64_t c = c0 + lane * V; c < c1; c += 64 * V) top = largest(top, c);
-      const float s = scale_of(lanes_max(top, 64), &inverse);
-      if (lane == 0) p.scale[row * p.nblk + k] = s;
-      for (int64_t c = c0 + lane * V; c < c1; c += 64 * V) finish(c, inverse);
+    const Unit unit(r);
+    auto largest = [&](float top, int64_t c) {
+      float s[V], w[V];
+      values(s, w, c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(s[i] * unit.up * w[i]));
+      return top;
+    };
+    auto finish = [&](int64_t c, const Step& q) {
+      float s[V], w[V], v[V];
+      values(s, w, c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = q(s[i] * unit.up, w[i]);
+      if (p.sum) store_v<V>(sum + c, s);
+      store_v<V>(y + c, v);
+    };
+    if (p.nblk == 1) {
+      float top = 0.0f;
+      for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) top = largest(top, c);
+      const Step q(row_max<256>(top, part), unit);
+      if (threadIdx.x == 0) p.scale[row] = q.scale;
+      for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) finish(c, q);
+    } else {
+      // a wave to a block of channels
+      const int lane = threadIdx.x & 63;
+      for (int64_t k = threadIdx.x >> 6; k < p.nblk; k += 4) {
+        const int64_t c0 = k * p.block, c1 = c0 + p.block < p.C ? c0 + p.block : p.C;
+        float top = 0.0f;
+        for (int64_t c = c0 + lane * V; c < c1; c += 64 * V) top = largest(top, c);
+        const Step q(lanes_max(top, 64), unit);
+        if (lane == 0) p.scale[row * p.nblk + k] = q.scale;
+        for (int64_t c = c0 + lane * V; c < c1; c += 64 * V) finish(c, q);
+      }
     }
   }
 }
