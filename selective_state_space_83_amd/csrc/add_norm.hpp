@@ -191,9 +191,9 @@ __device__ __forceinline__ void store_v(fp8_t* p, const float* v) {
 
 // To 8 bits: y is p m with p = (s 2^e) w and r = 2^e m, so that a value in units of its
 // block's scale, p (448 / max|p|), does not depend on the rounding of r.  The product's
-// rest and the quotient's go along, and q is rounded but once before its 8 bits: few
-// values lie on the other side of a step than the exact ones.  (Rounded at each of the
-// five operations: 2 of 655360 values; 32768 x 2560 to 8 bits takes as long either way.)
+// rest and the quotient's go along, and q is rounded but once before its 8 bits: of
+// 7.9 million values 3 lay a step off those of 64 bits, and 7 with every operation
+// rounded.  32768 x 2560 to 8 bits takes as long either way.
 struct Unit {
   float up, m;   // 2^e, and r without it
   __device__ __forceinline__ explicit Unit(float r) {
