@@ -740,8 +740,12 @@ typedef struct {
   float* scale;                       /* (rows, ceil(channels / block)), with SSM_E4M3 only */
 } ssm_add_norm_args_t;
 
-/* Its gradients, from the sum:  with n = s r, r = 1 / sqrt(mean(s^2) + eps),
+/* Its gradients:  with n = s r, r = 1 / sqrt(mean(s^2) + eps),
  *   ds = dsum + r (dy weight - n mean(dy weight n)),  dweight = sum_rows dy n.
+ * s is what `sum` holds: the kept sum, or x of a call without residual.  A sum kept in
+ * fp32 is the forward call's s.  One kept in bf16 is s rounded: from it come the gradients
+ * at the rounded sum, of which dweight is off by about 2e-3 of its norm; those of
+ * the forward call are ssm_add_norm_bwd_residual's.
  * dx and dresidual are both ds: dx in dtype, dresidual in sum_dtype where that is
  * another type (NULL: not wanted). */
 typedef struct {
@@ -766,6 +770,13 @@ typedef struct {
 size_t ssm_add_norm_bwd_workspace_size(const ssm_add_norm_bwd_args_t* args);
 ssm_status_t ssm_add_norm_fwd(const ssm_add_norm_args_t* args, void* hip_stream);
 ssm_status_t ssm_add_norm_bwd(const ssm_add_norm_bwd_args_t* args, void* hip_stream);
+
+/* The same from what the forward call was given: `sum` is x (in dtype) and s = x +
+ * residual, (rows, channels) in sum_dtype with its row stride, formed again as the forward
+ * call forms it.  The residual is required, and still what it was: a sum that took its
+ * place has overwritten it. */
+ssm_status_t ssm_add_norm_bwd_residual(const ssm_add_norm_bwd_args_t* args, const void* residual,
+                                       int64_t residual_stride, void* hip_stream);
 
 /* Static description of a status code. */
 const char* ssm_status_string(ssm_status_t status);

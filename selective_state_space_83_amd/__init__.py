@@ -126,7 +126,8 @@ EXPORTS = ["ssm_abi_version", "ssm_scan_workspace_size", "ssm_scan_plan_chunk_le
            "ssm_packed_scan_bwd_workspace_size", "ssm_packed_scan_bwd",
            "ssm_short_conv_fwd", "ssm_short_conv_step", "ssm_short_conv_bwd_workspace_size",
            "ssm_short_conv_bwd",
-           "ssm_add_norm_fwd", "ssm_add_norm_bwd_workspace_size", "ssm_add_norm_bwd"]
+           "ssm_add_norm_fwd", "ssm_add_norm_bwd_workspace_size", "ssm_add_norm_bwd",
+           "ssm_add_norm_bwd_residual"]
 
 # bytes of device scratch ssm_scan_fwd_noalloc keeps per GPU (SSM_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 64 << 20

@@ -168,40 +168,45 @@ ssm_status_t run_fwd(AddNormParams p, const Deal& d, hipStream_t s) {
   }
 }
 
-template <typename InT, typename SumT, int V, int TG, int R>
+template <typename InT, typename SumT, bool RES, int V, int TG, int R>
 ssm_status_t launch_bwd(const AddNormBwdParams& p, const Deal& d, hipStream_t s) {
-  hipLaunchKernelGGL((k_add_norm_bwd<InT, SumT, V, TG, R>), dim3(workgroups(d.blocks, TG)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((k_add_norm_bwd<InT, SumT, RES, V, TG, R>), dim3(workgroups(d.blocks, TG)), dim3(256), 0, s, p);
   return launch_status("k_add_norm_bwd");
 }
 
-template <typename InT, typename SumT>
-ssm_status_t run_bwd(AddNormBwdParams p, const Deal& d, hipStream_t s) {
+template <typename InT, typename SumT, bool RES>
+ssm_status_t run_bwd_of(AddNormBwdParams p, const Deal& d, hipStream_t s) {
   p.per = d.per;
   constexpr int V = wide<InT, SumT>();
   if (d.TG == 0) {
     if (d.vec)
-      hipLaunchKernelGGL((k_add_norm_bwd_long<InT, SumT, V>), dim3(uint32_t(d.blocks)), dim3(256), 0, s, p);
+      hipLaunchKernelGGL((k_add_norm_bwd_long<InT, SumT, RES, V>), dim3(uint32_t(d.blocks)), dim3(256), 0, s, p);
     else
-      hipLaunchKernelGGL((k_add_norm_bwd_long<InT, SumT, 1>), dim3(uint32_t(d.blocks)), dim3(256), 0, s, p);
+      hipLaunchKernelGGL((k_add_norm_bwd_long<InT, SumT, RES, 1>), dim3(uint32_t(d.blocks)), dim3(256), 0, s, p);
     return launch_status("k_add_norm_bwd_long");
   }
   if (!d.vec) {
-    if (d.TG == 256) return launch_bwd<InT, SumT, 1, 256, 16>(p, d, s);
-    return d.R == 1 ? launch_bwd<InT, SumT, 1, 64, 1>(p, d, s) : launch_bwd<InT, SumT, 1, 64, 4>(p, d, s);
+    if (d.TG == 256) return launch_bwd<InT, SumT, RES, 1, 256, 16>(p, d, s);
+    return d.R == 1 ? launch_bwd<InT, SumT, RES, 1, 64, 1>(p, d, s) : launch_bwd<InT, SumT, RES, 1, 64, 4>(p, d, s);
   }
   switch (d.TG) {
-    case 4: return launch_bwd<InT, SumT, V, 4, 1>(p, d, s);
-    case 16: return launch_bwd<InT, SumT, V, 16, 1>(p, d, s);
+    case 4: return launch_bwd<InT, SumT, RES, V, 4, 1>(p, d, s);
+    case 16: return launch_bwd<InT, SumT, RES, V, 16, 1>(p, d, s);
     case 64:
-      return d.R == 1 ? launch_bwd<InT, SumT, V, 64, 1>(p, d, s)
-                      : d.R == 2 ? launch_bwd<InT, SumT, V, 64, 2>(p, d, s) : launch_bwd<InT, SumT, V, 64, 4>(p, d, s);
+      return d.R == 1 ? launch_bwd<InT, SumT, RES, V, 64, 1>(p, d, s)
+                      : d.R == 2 ? launch_bwd<InT, SumT, RES, V, 64, 2>(p, d, s) : launch_bwd<InT, SumT, RES, V, 64, 4>(p, d, s);
     default:
-      if (d.R == 1) return launch_bwd<InT, SumT, V, 256, 1>(p, d, s);
-      if (d.R == 3) return launch_bwd<InT, SumT, V, 256, 3>(p, d, s);
+      if (d.R == 1) return launch_bwd<InT, SumT, RES, V, 256, 1>(p, d, s);
+      if (d.R == 3) return launch_bwd<InT, SumT, RES, V, 256, 3>(p, d, s);
       if constexpr (V == kWide32)
-        if (d.R == 8) return launch_bwd<InT, SumT, V, 256, 8>(p, d, s);
-      return d.R == 2 ? launch_bwd<InT, SumT, V, 256, 2>(p, d, s) : launch_bwd<InT, SumT, V, 256, 4>(p, d, s);
+        if (d.R == 8) return launch_bwd<InT, SumT, RES, V, 256, 8>(p, d, s);
+      return d.R == 2 ? launch_bwd<InT, SumT, RES, V, 256, 2>(p, d, s) : launch_bwd<InT, SumT, RES, V, 256, 4>(p, d, s);
   }
+}
+
+template <typename InT, typename SumT>
+ssm_status_t run_bwd(const AddNormBwdParams& p, const Deal& d, hipStream_t s) {
+  return p.res ? run_bwd_of<InT, SumT, true>(p, d, s) : run_bwd_of<InT, SumT, false>(p, d, s);
 }
 
 // Rows that all start on v elements.
@@ -223,9 +228,12 @@ size_t bwd_workspace(const ssm_add_norm_bwd_args_t* a) {
   return align256(size_t(blocks) * size_t(a->channels) * 4);
 }
 
-ssm_status_t check_bwd(const ssm_add_norm_bwd_args_t* a) {
+// residual: null for the gradients from the kept sum.
+ssm_status_t check_bwd(const ssm_add_norm_bwd_args_t* a, const void* residual, int64_t residual_stride) {
   if (!a) return fail(SSM_ERR_NULL, "args is NULL");
-  if (ssm_status_t st = check_sizes(a->rows, a->channels, {a->sum_stride, a->dy_stride, a->dsum ? a->dsum_stride : 0}))
+  if (ssm_status_t st = check_sizes(a->rows, a->channels,
+                                    {a->sum_stride, residual ? residual_stride : 0, a->dy_stride,
+                                     a->dsum ? a->dsum_stride : 0}))
     return st;
   if (!known(a->dtype)) return fail(SSM_ERR_DTYPE, "unknown dtype %d", a->dtype);
   if (a->sum_dtype != a->dtype && a->sum_dtype != SSM_F32)
@@ -239,15 +247,18 @@ ssm_status_t check_bwd(const ssm_add_norm_bwd_args_t* a) {
   if (a->rows * a->channels == 0) return SSM_OK;
   if (!a->sum || !a->dy || !a->dx) return fail(SSM_ERR_NULL, "sum, dy and dx are required");
   const size_t es = dtype_size(a->dtype), ss = dtype_size(a->sum_dtype), need = bwd_workspace(a);
-  if (misaligned(a->sum, ss) || misaligned(a->dsum, ss) || misaligned(a->dresidual, ss) || misaligned(a->dy, es) ||
-      misaligned(a->dx, es) || misaligned(a->weight, 4) || misaligned(a->workspace, 256))
+  const size_t first = residual ? es : ss;   // of x, or of the kept sum
+  if (misaligned(a->sum, first) || misaligned(residual, ss) || misaligned(a->dsum, ss) ||
+      misaligned(a->dresidual, ss) || misaligned(a->dy, es) || misaligned(a->dx, es) ||
+      misaligned(a->weight, 4) || misaligned(a->workspace, 256))
     return fail(SSM_ERR_UNSUPPORTED, "misaligned pointer (element alignment; workspace 256 bytes)");
   if (need > 0 && !a->workspace) return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes required", need);
   if (a->workspace_bytes < need)
     return fail(SSM_ERR_WORKSPACE, "workspace has %zu bytes, %zu required", a->workspace_bytes, need);
   const size_t n = size_t(a->rows * a->channels), c4 = size_t(a->channels) * 4;
   const Range outs[] = {{a->dx, n * es}, {a->dresidual, n * ss}, {a->dweight, c4}, {a->workspace, need}};
-  const Range ins[] = {rows_of(a->sum, a->rows, a->channels, a->sum_stride, ss),
+  const Range ins[] = {rows_of(a->sum, a->rows, a->channels, a->sum_stride, first),
+                       rows_of(residual, a->rows, a->channels, residual_stride, ss),
                        rows_of(a->dy, a->rows, a->channels, a->dy_stride, es),
                        rows_of(a->dsum, a->rows, a->channels, a->dsum_stride, ss), {a->weight, c4}};
   for (int i = 0; i < 4; ++i) {
@@ -257,6 +268,53 @@ ssm_status_t check_bwd(const ssm_add_norm_bwd_args_t* a) {
       if (overlap(outs[i], outs[k])) return fail(SSM_ERR_ALIAS, "two outputs overlap");
   }
   return SSM_OK;
+}
+
+ssm_status_t add_norm_bwd(const ssm_add_norm_bwd_args_t* a, const void* residual, int64_t residual_stride, void* hip_stream) {
+  if (ssm_status_t st = check_bwd(a, residual, residual_stride)) return st;
+  if (a->channels == 0) return SSM_OK;
+  hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  int64_t blocks = 0;
+  if (a->rows > 0) {
+    AddNormBwdParams p{};
+    p.sum = a->sum;
+    p.res = residual;
+    p.dy = a->dy;
+    p.dsum = a->dsum;
+    p.w = a->weight;
+    p.dx = a->dx;
+    p.dres = a->dresidual;
+    p.dw = a->dweight ? static_cast<float*>(a->workspace) : nullptr;
+    p.rows = a->rows;
+    p.C = a->channels;
+    p.ss = a->sum_stride;
+    p.rs = residual ? residual_stride : 0;
+    p.ds = a->dy_stride;
+    p.gs = a->dsum ? a->dsum_stride : 0;
+    p.eps = a->eps;
+    const int64_t v = wide_of(a->dtype, a->sum_dtype);
+    const size_t es = dtype_size(a->dtype), ss = dtype_size(a->sum_dtype);
+    p.stream = a->rows * a->channels * int64_t(es + (a->dresidual ? ss : 0)) > kL2Bytes;
+    const bool vec = a->channels % v == 0 && row_wide(a->sum, p.ss, v, residual ? es : ss) &&
+                     row_wide(residual, p.rs, v, ss) && row_wide(a->dy, p.ds, v, es) &&
+                     row_wide(a->dsum, p.gs, v, ss) && !misaligned(a->weight, 16) && !misaligned(a->dx, size_t(v) * es) &&
+                     !misaligned(a->dresidual, size_t(v) * ss);
+    const Deal d = bwd_deal(a, vec);
+    blocks = d.blocks;
+    ssm_status_t st = lanes_ok(d, blocks);
+    if (st) return st;
+    if (a->dtype == SSM_F32)
+      st = run_bwd<float, float>(p, d, s);
+    else if (a->sum_dtype == SSM_F32)
+      st = run_bwd<bf16_t, float>(p, d, s);
+    else
+      st = run_bwd<bf16_t, bf16_t>(p, d, s);
+    if (st) return st;
+  }
+  if (!a->dweight) return SSM_OK;
+  const ssmn::ColsParams c{{static_cast<const float*>(a->workspace), nullptr}, {a->dweight, nullptr}, blocks, a->channels};
+  hipLaunchKernelGGL(ssmn::k_norm_cols, dim3(uint32_t((a->channels + 15) / 16), 1), dim3(256), 0, s, c);
+  return launch_status("k_norm_cols");
 }
 
 }  // namespace
@@ -308,47 +366,15 @@ size_t ssm_add_norm_bwd_workspace_size(const ssm_add_norm_bwd_args_t* a) {
 
 ssm_status_t ssm_add_norm_bwd(const ssm_add_norm_bwd_args_t* a, void* hip_stream) {
   clear_message();
-  if (ssm_status_t st = check_bwd(a)) return st;
-  if (a->channels == 0) return SSM_OK;
-  hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  int64_t blocks = 0;
-  if (a->rows > 0) {
-    AddNormBwdParams p{};
-    p.sum = a->sum;
-    p.dy = a->dy;
-    p.dsum = a->dsum;
-    p.w = a->weight;
-    p.dx = a->dx;
-    p.dres = a->dresidual;
-    p.dw = a->dweight ? static_cast<float*>(a->workspace) : nullptr;
-    p.rows = a->rows;
-    p.C = a->channels;
-    p.ss = a->sum_stride;
-    p.ds = a->dy_stride;
-    p.gs = a->dsum ? a->dsum_stride : 0;
-    p.eps = a->eps;
-    const int64_t v = wide_of(a->dtype, a->sum_dtype);
-    const size_t es = dtype_size(a->dtype), ss = dtype_size(a->sum_dtype);
-    p.stream = a->rows * a->channels * int64_t(es + (a->dresidual ? ss : 0)) > kL2Bytes;
-    const bool vec = a->channels % v == 0 && row_wide(a->sum, p.ss, v, ss) && row_wide(a->dy, p.ds, v, es) &&
-                     row_wide(a->dsum, p.gs, v, ss) && !misaligned(a->weight, 16) && !misaligned(a->dx, size_t(v) * es) &&
-                     !misaligned(a->dresidual, size_t(v) * ss);
-    const Deal d = bwd_deal(a, vec);
-    blocks = d.blocks;
-    ssm_status_t st = lanes_ok(d, blocks);
-    if (st) return st;
-    if (a->dtype == SSM_F32)
-      st = run_bwd<float, float>(p, d, s);
-    else if (a->sum_dtype == SSM_F32)
-      st = run_bwd<bf16_t, float>(p, d, s);
-    else
-      st = run_bwd<bf16_t, bf16_t>(p, d, s);
-    if (st) return st;
-  }
-  if (!a->dweight) return SSM_OK;
-  const ssmn::ColsParams c{{static_cast<const float*>(a->workspace), nullptr}, {a->dweight, nullptr}, blocks, a->channels};
-  hipLaunchKernelGGL(ssmn::k_norm_cols, dim3(uint32_t((a->channels + 15) / 16), 1), dim3(256), 0, s, c);
-  return launch_status("k_norm_cols");
+  return add_norm_bwd(a, nullptr, 0, hip_stream);
+}
+
+ssm_status_t ssm_add_norm_bwd_residual(const ssm_add_norm_bwd_args_t* a, const void* residual, int64_t residual_stride,
+                                       void* hip_stream) {
+  clear_message();
+  if (!a) return fail(SSM_ERR_NULL, "args is NULL");
+  if (!residual && a->rows > 0 && a->channels > 0) return fail(SSM_ERR_NULL, "residual is required");
+  return add_norm_bwd(a, residual, residual_stride, hip_stream);
 }
 
 }  // extern "C"

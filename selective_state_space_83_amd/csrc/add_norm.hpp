@@ -5,8 +5,12 @@
 //
 // in x's type, or as e4m3 values q = round(y / scale) with scale = max|y| / 448
 // of each block of channels; and its gradients, with n = s r:
-//   dn = dy w,  ds = dsum + r (dn - n mean(dn n)),  dw = sum_rows dy n.
+//   dn = dy w,  ds = dsum + r (dn - n mean(dn n)),  dw = sum_rows dy n,
+// from the sum as it was kept, or from x and the residual, whose sum is formed again as
+// the forward pass forms it, before any rounding to the sum's type.
 #pragma once
+
+#include <type_traits>
 
 #include "group_norm.hpp"
 
@@ -38,7 +42,8 @@ struct AddNormParams {
 };
 
 struct AddNormBwdParams {
-  const void* sum;
+  const void* sum;       // the kept sum, or x where res is given
+  const void* res;       // or null
   const void* dy;
   const void* dsum;      // or null
   const float* w;        // or null
@@ -46,7 +51,7 @@ struct AddNormBwdParams {
   void* dres;            // or null
   float* dw;             // (blocks of rows, C), each block's sums over its rows; or null
   int64_t rows, C;
-  int64_t ss, ds, gs;    // row strides of sum, dy and dsum
+  int64_t ss, rs, ds, gs;   // row strides of sum, the residual, dy and dsum
   int64_t per;           // rows of a block: a lane walks them with its channels' weights in registers
   int32_t stream;        // as AddNormParams'
   float eps;
@@ -459,9 +464,10 @@ __global__ __launch_bounds__(256) void k_add_norm_long(AddNormParams p) {
 // Backward: TG lanes walk the p.per rows of a block: ds of every row, and the sums
 // over the block's rows for the weight's gradient.  (16384 x 1536 bf16 beside an fp32 sum,
 // with the forward pass: loads past the caches 134 -> 125 us, stores of large outputs
-// 131 -> 125.)
-template <typename InT, typename SumT, int V, int TG, int R>
+// 131 -> 125.)  RES: s is x + residual.
+template <typename InT, typename SumT, bool RES, int V, int TG, int R>
 __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
+  using FirstT = std::conditional_t<RES, InT, SumT>;
   __shared__ float part[8];
   const int lane = threadIdx.x & (TG - 1);
   const int64_t block = int64_t(blockIdx.x) * (256 / TG) + threadIdx.x / TG;
@@ -477,13 +483,16 @@ __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
     dw[i] = 0.0f;
   }
   if (p.w) load_row<V, R, TG>(w, p.w, lane, C);
-  const SumT* ps = static_cast<const SumT*>(p.sum) + row0 * p.ss;
+  const FirstT* ps = static_cast<const FirstT*>(p.sum) + row0 * p.ss;
+  const SumT* pr = static_cast<const SumT*>(p.res) + row0 * p.rs;
   const InT* pd = static_cast<const InT*>(p.dy) + row0 * p.ds;
   const SumT* pg = static_cast<const SumT*>(p.dsum) + row0 * p.gs;
-  RawRow<SumT, V, R> ns, ng;
+  RawRow<FirstT, V, R> ns;
+  RawRow<SumT, V, R> nr, ng;
   RawRow<InT, V, R> nd;
   auto request = [&] {
     ns.template load<TG>(ps, lane, C);
+    if constexpr (RES) nr.template load<TG>(pr, lane, C);
     nd.template load<TG>(pd, lane, C);
     if (p.dsum) ng.template load<TG>(pg, lane, C);
   };
@@ -493,11 +502,13 @@ __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
 #pragma unroll
     for (int i = 0; i < R * V; ++i) {
       s[i] = ns.at(i);
+      if constexpr (RES) s[i] += nr.at(i);
       d[i] = nd.at(i);
       g[i] = p.dsum ? ng.at(i) : 0.0f;
     }
     if (row + 1 < end) {
       ps += p.ss;
+      if constexpr (RES) pr += p.rs;
       pd += p.ds;
       pg += p.gs;
       request();
@@ -533,15 +544,26 @@ __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
 }
 
 // Rows too long for registers, read twice.
-template <typename InT, typename SumT, int V>
+template <typename InT, typename SumT, bool RES, int V>
 __global__ __launch_bounds__(256) void k_add_norm_bwd_long(AddNormBwdParams p) {
+  using FirstT = std::conditional_t<RES, InT, SumT>;
   __shared__ float part[8];
   const int64_t row0 = blockIdx.x * p.per, end = row0 + p.per < p.rows ? row0 + p.per : p.rows;
   float* dw = p.dw ? p.dw + blockIdx.x * p.C : nullptr;
   for (int64_t row = row0; row < end; ++row) {
-    const SumT* ps = static_cast<const SumT*>(p.sum) + row * p.ss;
+    const FirstT* ps = static_cast<const FirstT*>(p.sum) + row * p.ss;
+    const SumT* pr = static_cast<const SumT*>(p.res) + row * p.rs;
     const InT* pd = static_cast<const InT*>(p.dy) + row * p.ds;
     const SumT* pg = static_cast<const SumT*>(p.dsum) + row * p.gs;
+    auto values = [&](float (&s)[V], int64_t c) {
+      load_v<V>(s, ps + c);
+      if constexpr (RES) {
+        float q[V];
+        load_v<V>(q, pr + c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] += q[i];
+      }
+    };
     auto weight = [&](float (&w)[V], int64_t c) {
 #pragma unroll
       for (int i = 0; i < V; ++i) w[i] = 1.0f;
@@ -550,7 +572,7 @@ __global__ __launch_bounds__(256) void k_add_norm_bwd_long(AddNormBwdParams p) {
     float ss = 0.0f, sdn = 0.0f;
     for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) {
       float s[V], d[V], w[V];
-      load_v<V>(s, ps + c);
+      values(s, c);
       load_v<V>(d, pd + c);
       weight(w, c);
 #pragma unroll
@@ -563,7 +585,7 @@ __global__ __launch_bounds__(256) void k_add_norm_bwd_long(AddNormBwdParams p) {
     const float inv = 1.0f / float(p.C), r = 1.0f / sqrtf(ss * inv + p.eps), m = sdn * inv * r;
     for (int64_t c = threadIdx.x * V; c < p.C; c += 256 * V) {
       float s[V], d[V], w[V], g[V], sum[V];
-      load_v<V>(s, ps + c);
+      values(s, c);
       load_v<V>(d, pd + c);
       weight(w, c);
 #pragma unroll

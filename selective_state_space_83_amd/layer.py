@@ -9,7 +9,7 @@ one behind the other (contract: ``include/ssm_scan.h``).
     grads = short_conv_bwd(x, weight, dy, bias=None, offsets=None, act="silu")
     y, total = add_rms_norm(x, residual, weight)
     q, scale, total = add_rms_norm_8bit(x, residual, weight, block=0)
-    grads = add_rms_norm_bwd(total, dy, weight, dsum=None)
+    grads = add_rms_norm_bwd(x, dy, weight, dsum=None, residual=None)
 
 Packed tensors are (tokens, channels); sequence s holds the tokens offsets[s] to
 offsets[s + 1] - 1 (int32, on the GPU).  Tokens of no sequence are not read and
@@ -105,6 +105,8 @@ def declare(lib) -> None:
                        ("ssm_add_norm_fwd", AddNormArgs), ("ssm_add_norm_bwd", AddNormBwdArgs)):
         f = getattr(lib, name)
         f.restype, f.argtypes = ctypes.c_int, [P(args), ctypes.c_void_p]
+    f = lib.ssm_add_norm_bwd_residual
+    f.restype, f.argtypes = ctypes.c_int, [P(AddNormBwdArgs), ctypes.c_void_p, _i64, ctypes.c_void_p]
     for name, args in (("ssm_packed_scan_workspace_size", PackedScanArgs),
                        ("ssm_packed_scan_bwd_workspace_size", PackedScanBwdArgs),
                        ("ssm_short_conv_bwd_workspace_size", ShortConvBwdArgs),
@@ -483,10 +485,15 @@ def add_rms_norm_8bit(x, residual=None, weight=None, eps=1e-5, block=0, y=None, 
     return _add_norm(x, residual, weight, eps, block, True, y, total, want_total, stream)
 
 
-def add_rms_norm_bwd(total, dy, weight=None, dsum=None, eps=1e-5, want_dweight=True, workspace=None, stream=None) -> dict:
-    """The gradients of sum(dy * y) + sum(dsum * total) of ``add_rms_norm``, from its
-    total: dx in dy's dtype, which is the residual's gradient too; where total has another
-    dtype (float32) also dresidual in that; and, when asked, dweight (float32)."""
+def add_rms_norm_bwd(total, dy, weight=None, dsum=None, eps=1e-5, want_dweight=True, workspace=None, stream=None,
+                     residual=None) -> dict:
+    """The gradients of sum(dy * y) + sum(dsum * total) of ``add_rms_norm``: with
+    ``residual`` (which then has not been updated in place) from x, given as ``total``, and
+    residual; else from its total.  y comes from the sum before it is rounded to total's
+    dtype, so a bfloat16 total gives other gradients, those at the rounded sum (dweight off by
+    about 2e-3 of its norm); a float32 total gives the same.  Returns dx in dy's dtype,
+    which is the residual's gradient too; where the residual (or total) has another dtype
+    (float32) also dresidual in that; and, when asked, dweight (float32)."""
     f32 = _torch().float32
     lib = load_library()
     dev, handle = _current(stream)
@@ -495,14 +502,20 @@ def add_rms_norm_bwd(total, dy, weight=None, dsum=None, eps=1e-5, want_dweight=T
         if len(shape) < 1:
             raise ValueError("dy must be (..., channels)")
         C = shape[-1]
-        code, wide = _code(dy, "dy"), _wide(total, "total", dt, f32)
-        p_sum, ss = _stream_rows(total, "total", shape, dev)
+        code = _code(dy, "dy")
+        if residual is None:
+            kept, wide = total, _wide(total, "total", dt, f32)
+            p_sum, ss = _stream_rows(total, "total", shape, dev)
+        else:
+            kept, wide = residual, _wide(residual, "residual", dt, f32)
+            p_sum, ss = _even_rows(total, "x", dy, dev)
+            p_res, rs = _stream_rows(residual, "residual", shape, dev)
         p_dy, ds = _even_rows(dy, "dy", dy, dev)
-        p_dsum, gs = (None, 0) if dsum is None else _even_rows(dsum, "dsum", total, dev)
+        p_dsum, gs = (None, 0) if dsum is None else _even_rows(dsum, "dsum", kept, dev)
         g = {"dx": dy.new_empty(shape)}
-        both = total.dtype is not dt
+        both = kept.dtype is not dt
         if both:
-            g["dresidual"] = total.new_empty(shape)
+            g["dresidual"] = kept.new_empty(shape)
         if want_dweight:
             g["dweight"] = dy.new_empty((C,), dtype=f32)
         a = AddNormBwdArgs(dy.numel() // C if C else 0, C, ss, ds, gs, code, wide, 0, eps, p_sum, p_dy, p_dsum,
@@ -510,6 +523,9 @@ def add_rms_norm_bwd(total, dy, weight=None, dsum=None, eps=1e-5, want_dweight=T
                            g["dresidual"].data_ptr() if both else None, g["dweight"].data_ptr() if want_dweight else None)
         arg = ctypes.byref(a)
         workspace = _workspace(a, lib.ssm_add_norm_bwd_workspace_size(arg), workspace, dy, dev)
-        status = lib.ssm_add_norm_bwd(arg, handle)
+        if residual is None:
+            status = lib.ssm_add_norm_bwd(arg, handle)
+        else:
+            status = lib.ssm_add_norm_bwd_residual(arg, p_res, rs, handle)
     _raise_for(lib, status)
     return g
