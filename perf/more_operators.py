@@ -413,7 +413,10 @@ def _run_own(s):
             out = ssm.add_rms_norm(s["x"], s["residual"], s["weight"], eps=EPS)
         return list(out if s["residual"] is not None else out[:-1])
     y, total = ssm.add_rms_norm(s["x"], s["residual"], s["weight"], eps=EPS)
-    g = ssm.add_rms_norm_bwd(total, s["dy"], s["weight"], dsum=s["dsum"], eps=EPS)
+    # y comes from the sum in float32, which a bf16 residual's total no longer holds
+    again = s["residual"] is not None and total.dtype != torch.float32
+    g = ssm.add_rms_norm_bwd(s["x"] if again else total, s["dy"], s["weight"], dsum=s["dsum"], eps=EPS,
+                             residual=s["residual"] if again else None)
     return dict(g, y=y) if s["residual"] is None else dict(g, y=y, sum=total)
 
 
