@@ -637,8 +637,9 @@ typedef struct {
   size_t workspace_bytes;
 } ssm_packed_scan_bwd_args_t;
 
-/* Workspace sizes: pure host functions of the sizes, chunk_len or super_chunk and
- * whether h0 and h_last are given; 0 for invalid sizes. */
+/* Workspace sizes: pure host functions of the sizes and row strides, chunk_len or
+ * super_chunk and whether z, h0 and h_last are given, not of where anything lies; 0 for
+ * invalid sizes. */
 size_t ssm_packed_scan_workspace_size(const ssm_packed_scan_args_t* args);
 size_t ssm_packed_scan_bwd_workspace_size(const ssm_packed_scan_bwd_args_t* args);
 ssm_status_t ssm_packed_scan_fwd(const ssm_packed_scan_args_t* args, void* hip_stream);

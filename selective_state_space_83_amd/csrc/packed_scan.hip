@@ -54,7 +54,8 @@ int64_t widest_stride(const Args* a) {
 // for 76, 16384 x 256 62 for 71, 65536 x 64 86 for 131, 1024 x 1536 37 for 44.)
 int64_t chunk_floor(int64_t tokens, int64_t D) { return int64_t(std::sqrt(double(tokens) * double(D + 520) / 11000)); }
 
-// Sizes assumed validated.
+// Sizes assumed validated.  kept: with room for the initial states that a cache updated in
+// place needs kept; by whether there are states both ways, not by their addresses.
 Plan make_plan(int64_t tokens, int64_t D, int64_t N, int64_t chunk_len, int64_t stride, bool kept) {
   Plan pl;
   pl.dtiles = (D + kWave - 1) / kWave;
@@ -102,7 +103,7 @@ Plan plan_of(const ssm_packed_scan_args_t* a) {
   }
   int64_t stride = widest_stride(a);
   if (a->z) stride = std::max(stride, a->z_stride);
-  return make_plan(a->tokens, a->dim, a->dstate, a->chunk_len, stride, a->h0 && a->h0 == a->h_last);
+  return make_plan(a->tokens, a->dim, a->dstate, a->chunk_len, stride, a->h0 && a->h_last);
 }
 
 bool supported_n(int64_t n) { return n == 1 || n == 2 || n == 4 || n == 8 || n == 16; }
@@ -503,7 +504,7 @@ ssm_status_t ssm_packed_scan_fwd(const ssm_packed_scan_args_t* a, void* hip_stre
   if (pl.nc > 1) {
     p.dsum = reinterpret_cast<float*>(ws);
     p.hsum = reinterpret_cast<float*>(ws + pl.off_hsum);
-    if (pl.off_reset > pl.off_hstart) p.hstart = reinterpret_cast<float*>(ws + pl.off_hstart);
+    if (a->h0 && a->h0 == a->h_last) p.hstart = reinterpret_cast<float*>(ws + pl.off_hstart);
     p.reset = reinterpret_cast<int32_t*>(ws + pl.off_reset);
   }
   p.xs = a->x_stride;
