@@ -722,8 +722,9 @@ ssm_status_t ssm_short_conv_bwd(const ssm_short_conv_bwd_args_t* args, void* hip
  * updated in place); y is formed from the unrounded s, in x's type, or in 8 bits:
  * values of e4m3 (the OCP format: largest 448, NaN, no infinities) and a scale
  * for each `block` neighbouring channels of a row (the last block may be short;
- * 0: one for the row), y ~ q scale, scale = max|y| / 448 of its block, at least 2^-126,
- * and 1 where that maximum is 0 (or no number).  q is rounded once, to nearest even. */
+ * 0: one for the row), y ~ q scale, scale = max|y| / 448 of its block, NaN left out, at
+ * least 2^-126, and 1 where that maximum is 0 or no y is a number.  q is rounded once, to
+ * nearest even, and NaN where y is. */
 #define SSM_E4M3 2                    /* a y_dtype of ssm_add_norm_args_t only */
 
 typedef struct {

@@ -203,11 +203,12 @@ struct Unit {
   float up, m;   // 2^e, and r without it
   __device__ __forceinline__ explicit Unit(float r) {
     const uint32_t b = __float_as_uint(r);
-    up = __uint_as_float(b & 0x7f800000u);
+    up = r != r ? r : __uint_as_float(b & 0x7f800000u);   // (a row of NaN has no largest value)
     m = __uint_as_float((b & 0x007fffffu) | 0x3f800000u);
   }
 };
-// The scale of a block whose largest |p| is top, and what takes p to q.
+// The scale of a block whose largest |p| is top (of its numbers; 0 if it has none), and
+// what takes p to q.
 struct Step {
   float scale, c, rest;
   __device__ __forceinline__ Step(float top, const Unit& u) {
