@@ -54,7 +54,17 @@ __device__ __forceinline__ int32_t seq_at(const Seqs& q, int32_t t) { return seq
 
 // One step back of a lane's NS states: bwd_lane_step, with the slow-decay form chosen
 // state by state (see advance).
-template <int NS, int DISC, bool SERIES, bool SHORT>
+//
+// ZOH's factor f = Delta (e^z - 1) / z and its derivative by A, Delta^2 q with
+// q = (z e^z - (e^z - 1)) / z^2, z = Delta A: the direct forms take differences that lose
+// 2^-24 / |z| and 2^-22 / z^2 of their values, which a dA of few tokens shows (one token
+// of 8 channels, bf16: 9e-5 in norm with the scan's limit of 1/64 for them, and a series of
+// three terms below it).  So they are kept to |z| >= 1/2 (1e-6), and below it
+//   q = sum_k z^k (k + 1) / (k + 2)!, to k = 7 (the rest is below 3e-8 of q),
+//   f = Delta (e^z - z q).
+constexpr float kZohSeries = 0.5f;
+
+template <int NS, int DISC, bool SERIES>
 __device__ __forceinline__ void retreat(float (&g)[NS], float (&dA)[NS], const ChanConst<NS, DISC>& cc,
                                         const float (&Bv)[NS], const float (&Cv)[NS], const float (&hp)[NS],
                                         const float (&hn)[NS], float u, float dv, float dyv, float limit,
@@ -95,25 +105,17 @@ __device__ __forceinline__ void retreat(float (&g)[NS], float (&dA)[NS], const C
       float f = (a[n] - 1.0f) * cc.invA[n];
       float dfda = fmaf(dv, a[n], -f) * cc.invA[n];
       if constexpr (SERIES) {
-        // the series of bwd_lane_step where |z| is small, the direct forms elsewhere
         const float z = z2[n] * kLn2;
-        float q1, q2;
-        if constexpr (SHORT) {
-          q1 = fmaf(z, fmaf(z, 1.0f / 6.0f, 0.5f), 1.0f);
-          q2 = fmaf(z, fmaf(z, 0.125f, 1.0f / 3.0f), 0.5f);
-        } else {
-          q1 = fmaf(z, 1.0f / 120.0f, 1.0f / 24.0f);
-          q1 = fmaf(z, q1, 1.0f / 6.0f);
-          q1 = fmaf(z, q1, 0.5f);
-          q1 = fmaf(z, q1, 1.0f);
-          q2 = fmaf(z, 1.0f / 144.0f, 1.0f / 30.0f);
-          q2 = fmaf(z, q2, 0.125f);
-          q2 = fmaf(z, q2, 1.0f / 3.0f);
-          q2 = fmaf(z, q2, 0.5f);
-        }
-        const bool small = fabsf(z) < series_z<SHORT>() || cc.invA[n] == 0.0f;
-        f = small ? dv * q1 : f;
-        dfda = small ? (dv * dv) * q2 : dfda;
+        float q = fmaf(z, 1.0f / 45360.0f, 1.0f / 5760.0f);
+        q = fmaf(z, q, 1.0f / 840.0f);
+        q = fmaf(z, q, 1.0f / 144.0f);
+        q = fmaf(z, q, 1.0f / 30.0f);
+        q = fmaf(z, q, 0.125f);
+        q = fmaf(z, q, 1.0f / 3.0f);
+        q = fmaf(z, q, 0.5f);
+        const bool small = fabsf(z) < kZohSeries || cc.invA[n] == 0.0f;
+        f = small ? dv * fmaf(-z, q, a[n]) : f;
+        dfda = small ? (dv * dv) * q : dfda;
       }
       const float agh = ag[n] * hp[n], Bu = Bv[n] * u, Gf = G[n] * f;
       pB[n] = Gf * u;
@@ -291,13 +293,12 @@ k_packed_bwd(const PackedBwdParams p) {
   load_chan<NS, DISC>(cc, p.A + dn, p.exact_thr);
   const float dsk = p.Dskip ? p.Dskip[d] : 0.0f;
   const float limit = p.exact_thr * kLog2e;
-  constexpr bool kShortSeries = !std::is_same<InT, float>::value;
   float zoh_thr = 0.0f;   // below it ZOH's factor is taken from its series
   if constexpr (DISC == kZoh) {
     float amin = __builtin_inff();
 #pragma unroll
     for (int n = 0; n < NS; ++n) amin = fminf(amin, fabsf(cc.A2[n] * kLn2));
-    zoh_thr = amin > 0.0f ? series_z<kShortSeries>() / amin : __builtin_inff();
+    zoh_thr = amin > 0.0f ? kZohSeries / amin : __builtin_inff();
   }
 
   const int32_t t0 = chunk * p.T, t1 = p.q.tokens - t0 > p.T ? t0 + p.T : p.q.tokens;
@@ -507,9 +508,9 @@ k_packed_bwd(const PackedBwdParams p) {
               if (kEvents && (begins_h >> js & 1)) initial(hp, j0 + js);
               const bool series = DISC == kZoh && __builtin_amdgcn_ballot_w64(dv < zoh_thr) != 0;
               if (series)
-                retreat<NS, DISC, true, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, limit, pB, pC, du, ddt);
+                retreat<NS, DISC, true>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, limit, pB, pC, du, ddt);
               else
-                retreat<NS, DISC, false, kShortSeries>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, limit, pB, pC, du, ddt);
+                retreat<NS, DISC, false>(g, dAacc, cc, Bv, Cv, hp, hn, u, dv, dyv, limit, pB, pC, du, ddt);
               dDacc = fmaf(dyv, u, dDacc);
               if (kEvents && (begins_h >> js & 1)) {
                 const PackedBwdParams& b = args_again<PackedBwdParams>();
