@@ -465,7 +465,7 @@ __global__ __launch_bounds__(256) void k_add_norm_long(AddNormParams p) {
 // Backward: TG lanes walk the p.per rows of a block: ds of every row, and the sums
 // over the block's rows for the weight's gradient.  (16384 x 1536 bf16 beside an fp32 sum,
 // with the forward pass: loads past the caches 134 -> 125 us, stores of large outputs
-// 131 -> 125.)  RES: s is x + residual.
+// 131 -> 125.)  RES: s is x + residual (16384 x 1536 bf16: 55 us, from the kept sum 46).
 template <typename InT, typename SumT, bool RES, int V, int TG, int R>
 __global__ __launch_bounds__(256) void k_add_norm_bwd(AddNormBwdParams p) {
   using FirstT = std::conditional_t<RES, InT, SumT>;

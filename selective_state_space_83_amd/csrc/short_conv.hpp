@@ -11,7 +11,9 @@
 // A lane holds V neighbouring channels (4, or one where rows do not start on 4) and walks
 // a tile of tokens with the last three inputs in registers; a wave covers 64 V channels,
 // and the waves of a workgroup lie side by side on the same tokens.  Bound by memory: a
-// tile reads K - 1 rows more than its own, which the caches hold.  Loads and stores go
+// tile reads K - 1 rows more than its own, and they come from memory again, since
+// neighbouring tiles lie on different XCDs (32768 x 2560 bf16, tiles of 16: 202 MB read
+// for 168 MB of x; neighbours on one XCD gained nothing).  Loads and stores go
 // through the caches: loads past them gain 1% in a forward pass and lose 9% where the
 // gradients follow it (16384 x 1536 fp32 114 -> 124 us); stores past them change nothing.
 #pragma once
